@@ -263,6 +263,129 @@ int moe_shared_ffn(const moe_experts* W, const uint16_t* x, int32_t T, uint16_t*
                    size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Router training: the load-balance loss of the router's choices and the
+ * gradients that reach its logits.  The pages describe serving and give no
+ * training formula; the loss is the usual product of each expert's share of
+ * the assignments and its mean probability, taken per packed sequence.
+ *
+ * moe_balance_loss — for the sequences s = rows [seq_offsets[s],
+ * seq_offsets[s+1]) of the batch, with p[t] = softmax(logits[t]) over the E
+ * experts and v_t = 1 for tokens that count (token_mask[t] != 0):
+ *   n_tokens[s]  = sum_t v_t                                  device int32 [S]
+ *   counts[s][e] = #{(t, j) : v_t, topk_ids[t][j] == e}       device int32 [S][E]
+ *   probs[s][e]  = sum_t v_t p[t][e]                          device fp32 [S][E]
+ *   loss[s]      = E / (k n_s^2) sum_e counts[s][e] probs[s][e]   device fp32 [S]
+ * loss is 1 for a uniform router; a sequence without counting tokens has
+ * zeros everywhere.
+ *   logits       device fp32 [T][E], topk_ids device int32 [T][k], as for
+ *                moe_route; an id outside [0, E) is an assignment dropped by
+ *                the caller: it is not counted (k in the loss stays k)
+ *   token_mask   device uint8 [T] or NULL (every token counts); the logits and
+ *                ids of masked tokens are not used, whatever they hold
+ *   seq_offsets  device int32 [S+1], non-decreasing in [0, T], or NULL (S = 1:
+ *                the whole batch); rows before the first and behind the last
+ *                sequence belong to none.  Offsets outside this give
+ *                unspecified output but no out-of-bounds access.
+ * A logit of -inf has probability 0 (a row of nothing else: all zero); +inf or
+ * NaN in a counting row makes probs and loss of its sequence NaN.
+ * Sums over tokens are taken in fp32 within a few dozen rows and in double
+ * above, in a fixed order.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 16), T >= 0, T*k <= 2^28, 1 <= S <= 2^20.
+ * ws: device, >= moe_balance_loss_workspace(T, E, S).                       */
+size_t moe_balance_loss_workspace(int32_t T, int32_t E, int32_t S);
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, int32_t T, int32_t E, int32_t k,
+                     const uint8_t* token_mask, const int32_t* seq_offsets, int32_t S,
+                     int32_t* n_tokens, int32_t* counts, float* probs, float* loss, void* ws,
+                     size_t ws_bytes, moe_stream_t stream);
+
+/* moe_route_backward — the gradient of moe_route's weights and of
+ * moe_balance_loss with respect to the logits, in one pass.  Either part may
+ * be absent (d_topk_w NULL or d_loss NULL).
+ *   balance:  a_s = d_loss[s] E / (k n_s^2);
+ *             d_logits[t][e] = a_s p[t][e] (c_se - sum_f p[t][f] c_sf)
+ *   weights:  D = sum_j topk_w[t][j] d_topk_w[t][j];
+ *             renorm = 1: d_logits[t][id_j] += topk_w[t][j] (d_topk_w[t][j] - D)
+ *             renorm = 0: d_logits[t][id_j] += topk_w[t][j] d_topk_w[t][j], and
+ *                         d_logits[t][e] -= p[t][e] D for every e
+ * (an id that appears twice in a row adds twice; ids outside [0, E) and their
+ * weights are left out).  A row whose mask is 0 gets zeros; rows that belong
+ * to no sequence are left as they were.
+ *   topk_ids, topk_w  as written by moe_route with the same renorm (may be
+ *                     NULL when d_topk_w is)
+ *   d_topk_w          device fp32 [T][k] or NULL
+ *   n_tokens, counts  as written by moe_balance_loss (may be NULL when d_loss
+ *                     is); the counts carry no gradient
+ *   d_loss            device fp32 [S] or NULL
+ *   d_logits          device fp32 [T][E] (out)
+ *   token_mask, seq_offsets, S   as for moe_balance_loss
+ * No workspace; limits as for moe_balance_loss.                              */
+int moe_route_backward(const float* logits, int32_t T, int32_t E, int32_t k, int32_t renorm,
+                       const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,
+                       const uint8_t* token_mask, const int32_t* seq_offsets, int32_t S,
+                       const int32_t* n_tokens, const int32_t* counts, const float* d_loss,
+                       float* d_logits, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * FP8 products with a scale for each block of 128 (guide, "CPU layer split"
+ * lists fp8 experts; the weight layout is MOE_W_FP8_B128's, the activations
+ * are E4M3 here instead of bf16).
+ *
+ * moe_fp8_quantize — rows of bf16 to E4M3 with one scale per 128 consecutive
+ * columns (the last block of a row may be shorter):
+ *   scales[t][b] = the least power of two >= amax / 448, not below 2^-126; 1
+ *                  for a block of zeros
+ *   codes[t][c]  = E4M3(x[t][c] / scales[t][c / 128]), nearest-even
+ * The quotient is exact, so each code is one rounding of x; E4M3 being a
+ * floating format, a power of two keeps the relative precision that amax / 448
+ * itself would give.  A block holding an infinity or NaN gets NaN codes and a
+ * NaN scale (products over it are NaN).
+ *   x       device bf16 [T][K], K a multiple of 8, 8 <= K <= 65536
+ *   codes   device uint8 [T][K] (out)
+ *   scales  device fp32 [T][ceil(K/128)] (out)                               */
+int moe_fp8_quantize(const uint16_t* x, int32_t T, int32_t K, uint8_t* codes, float* scales,
+                     moe_stream_t stream);
+
+/* moe_fp8_matmul — y = a w^T over E4M3 operands with block scales:
+ *   y[m][n] = bf16( sum_b a_scale[m][b] w_scale[n/128][b]
+ *                         sum_{k in block b} a[m][k] w[n][k] )
+ * summed in fp32, one rounding to bf16.  The FP8 matrix instruction adds 8
+ * consecutive k at a time and keeps 13 bits below the largest of those 8
+ * products (bits under that are cut off); everything above is fp32.
+ *   a        device uint8 [M][K] E4M3;  a_scale device fp32 [M][ceil(K/128)]
+ *   w        device uint8 [E][N][K] E4M3
+ *   w_scale  device fp32 [E][ceil(N/128)][ceil(K/128)]
+ *   counts, offsets  device int32 [E], [E+1] as from moe_permute: rows
+ *            [offsets[e], offsets[e] + counts[e]) take w[e]; rows of y in no
+ *            segment are left as they were.  Both NULL with E = 1: every row.
+ *            Segments must lie in [0, M).
+ *   y        device bf16 [M][N] (out)
+ * Scales may be any fp32 values (not only moe_fp8_quantize's).  N >= 1; K a
+ * multiple of 16; N, K <= 65536, N * K < 2^32, 1 <= E <= 1024, M <= 2^27.
+ * ws: device, >= moe_fp8_matmul_workspace(M, N, K, E) bytes; may be NULL where
+ * that is 0.                                                                 */
+size_t moe_fp8_matmul_workspace(int32_t M, int32_t N, int32_t K, int32_t E);
+int moe_fp8_matmul(const uint8_t* a, const float* a_scale, int32_t M, const uint8_t* w,
+                   const float* w_scale, int32_t N, int32_t K, const int32_t* counts,
+                   const int32_t* offsets, int32_t E, uint16_t* y, void* ws, size_t ws_bytes,
+                   moe_stream_t stream);
+
+/* moe_expert_ffn_fp8 — moe_expert_ffn over MOE_W_FP8_B128 records with both
+ * operands of both products in E4M3 (half the MFMA work of moe_expert_ffn's
+ * FP8 path, which keeps the bf16 activations to 2^-17 by splitting them in
+ * two; here they carry E4M3's 4 significant bits):
+ *   xq   = moe_fp8_quantize(x);   g, u = the rows' products with W13 (fp32)
+ *   hq   = moe_fp8_quantize's rule applied to fp32 h = SiLU(g) * u
+ *   y_perm = bf16(hq W2^T)
+ * Arguments as for moe_expert_ffn (W->fmt must be MOE_W_FP8_B128, others
+ * return MOE_ERR_UNSUPPORTED).
+ * ws: device, >= moe_expert_ffn_fp8_workspace(W, T, k).                      */
+size_t moe_expert_ffn_fp8_workspace(const moe_experts* W, int32_t T, int32_t k);
+int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_expert, const uint16_t* x,
+                       int32_t T, int32_t k, const int32_t* counts, const int32_t* offsets,
+                       const int32_t* sorted_idx, uint16_t* y_perm, void* ws, size_t ws_bytes,
+                       moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Expert-slot cache (guide, "expert bank & LRU slot cache", "MoE strategies"
  * offload, "minimum cache constraint").  A fixed pool of S slots in HBM,
  * shared by all layers, holds expert records; the slot table maps
@@ -541,7 +664,8 @@ int moe_version(void);            /* ABI version, currently 1 */
  * against [0, E) of the moe_experts they address (the struct carries no
  * pool size, so with a pool of S < E slots an entry in [S, E) passes),
  * sorted_idx values against T*k, each expert's row segment (offsets[e],
- * counts[e]) against [0, T*k), inv_idx values in moe_combine against T*k.
+ * counts[e]) against [0, T*k) ([0, M) in moe_fp8_matmul), each sequence's rows
+ * (seq_offsets) against [0, T), inv_idx values in moe_combine against T*k.
  * An out-of-range value is replaced by an in-range one (the kernel stays
  * inside its buffers; its results are then meaningless) and sets a flag:
  *   1 = slot, 2 = sorted index, 4 = row segment, 8 = inverse index

@@ -104,6 +104,18 @@ _SIGS = {
                                     ctypes.POINTER(BwProfile)]),
     "moe_shared_ffn_workspace": (_sz, [ctypes.POINTER(Experts), _i32]),
     "moe_shared_ffn": (ctypes.c_int, [ctypes.POINTER(Experts), _p, _i32, _p, _p, _sz, _p]),
+    "moe_balance_loss_workspace": (_sz, [_i32, _i32, _i32]),
+    "moe_balance_loss": (ctypes.c_int, [_p, _p, _i32, _i32, _i32, _p, _p, _i32, _p, _p, _p, _p, _p,
+                                        _sz, _p]),
+    "moe_route_backward": (ctypes.c_int, [_p, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _i32, _p,
+                                          _p, _p, _p, _p]),
+    "moe_fp8_quantize": (ctypes.c_int, [_p, _i32, _i32, _p, _p, _p]),
+    "moe_fp8_matmul_workspace": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_fp8_matmul": (ctypes.c_int, [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p, _sz,
+                                      _p]),
+    "moe_expert_ffn_fp8_workspace": (_sz, [ctypes.POINTER(Experts), _i32, _i32]),
+    "moe_expert_ffn_fp8": (ctypes.c_int, [ctypes.POINTER(Experts), _p, _p, _i32, _i32, _p, _p, _p,
+                                          _p, _p, _sz, _p]),
     "moe_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_error": (ctypes.c_char_p, []),
     "moe_version": (ctypes.c_int, []),
@@ -484,6 +496,150 @@ def moe_shared_ffn(W: Experts, x: torch.Tensor, T: int, y: torch.Tensor, ws: tor
                    stream=None) -> None:
     _check(_lib.moe_shared_ffn(ctypes.byref(W), _ptr(x), T, _ptr(y), _ptr(ws),
                                ws.numel() * ws.element_size(), _stream(stream)), "moe_shared_ffn")
+
+
+# ---------------------------------------------------------------------------
+# Router training and FP8 products.  These calls check every tensor's type, size
+# and device against the call's sizes before anything is enqueued.
+# ---------------------------------------------------------------------------
+_F32, _BF16, _I32T, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+_FP8 = (torch.uint8, torch.float8_e4m3fn)   # E4M3 codes, as bytes or typed
+_MASK = (torch.uint8, torch.bool)
+
+
+def _arg(t, name: str, dtype, numel: int | None, dev) -> int | None:
+    """Device pointer of a required tensor of this type (or one of these) and size."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t)}")
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    n = t.numel()
+    if numel is not None and n != numel:
+        raise ValueError(f"{name}: {n} elements, expected {numel}")
+    if n == 0:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    return t.data_ptr()
+
+
+def _opt(t, name: str, dtype, numel: int | None, dev) -> int | None:
+    return None if t is None else _arg(t, name, dtype, numel, dev)
+
+
+def _device_of(t, name: str):
+    """The device that a call runs on: its first tensor's, which must be the current one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: device tensor expected")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _matrix(t, name: str) -> tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
+    return t.shape[0], t.shape[1]
+
+
+def _seq_count(seq_offsets) -> int:
+    return 1 if seq_offsets is None else seq_offsets.numel() - 1
+
+
+def moe_balance_loss_workspace(T: int, E: int, S: int) -> int:
+    return int(_lib.moe_balance_loss_workspace(T, E, S))
+
+
+def moe_balance_loss(logits, topk_ids, k: int, n_tokens, counts, probs, loss, ws, token_mask=None,
+                     seq_offsets=None, stream=None) -> None:
+    """Load-balance loss, counts and probability sums of every sequence (see the header)."""
+    T, E = _matrix(logits, "logits")
+    S = _seq_count(seq_offsets)
+    dev = _device_of(logits, "logits")
+    _check(_lib.moe_balance_loss(
+        _arg(logits, "logits", _F32, None, dev), _arg(topk_ids, "topk_ids", _I32T, T * k, dev), T, E,
+        k, _opt(token_mask, "token_mask", _MASK, T, dev),
+        _opt(seq_offsets, "seq_offsets", _I32T, None, dev), S,
+        _arg(n_tokens, "n_tokens", _I32T, S, dev), _arg(counts, "counts", _I32T, S * E, dev),
+        _arg(probs, "probs", _F32, S * E, dev), _arg(loss, "loss", _F32, S, dev),
+        _arg(ws, "ws", _U8, None, dev), ws.numel(), _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(logits, k: int, topk_ids, topk_w, d_topk_w, n_tokens, counts, d_loss,
+                       d_logits, renorm: bool = True, token_mask=None, seq_offsets=None,
+                       stream=None) -> None:
+    """Gradient of the routing weights (d_topk_w) and of the balance loss (d_loss) with respect
+    to the logits; either may be None, with the tensors only it needs (see the header)."""
+    T, E = _matrix(logits, "logits")
+    S = _seq_count(seq_offsets)
+    dev = _device_of(logits, "logits")
+    _check(_lib.moe_route_backward(
+        _arg(logits, "logits", _F32, None, dev), T, E, k, int(renorm),
+        _opt(topk_ids, "topk_ids", _I32T, T * k, dev), _opt(topk_w, "topk_w", _F32, T * k, dev),
+        _opt(d_topk_w, "d_topk_w", _F32, T * k, dev), _opt(token_mask, "token_mask", _MASK, T, dev),
+        _opt(seq_offsets, "seq_offsets", _I32T, None, dev), S,
+        _opt(n_tokens, "n_tokens", _I32T, S, dev), _opt(counts, "counts", _I32T, S * E, dev),
+        _opt(d_loss, "d_loss", _F32, S, dev), _arg(d_logits, "d_logits", _F32, T * E, dev),
+        _stream(stream)), "moe_route_backward")
+
+
+def moe_fp8_quantize(x, codes, scales, stream=None) -> None:
+    """bf16 rows -> E4M3 codes and one power-of-two scale per 128 columns."""
+    T, K = _matrix(x, "x")
+    dev = _device_of(x, "x")
+    _check(_lib.moe_fp8_quantize(
+        _arg(x, "x", _BF16, None, dev), T, K, _arg(codes, "codes", _FP8, T * K, dev),
+        _arg(scales, "scales", _F32, T * ((K + 127) // 128), dev), _stream(stream)),
+        "moe_fp8_quantize")
+
+
+def moe_fp8_matmul_workspace(M: int, N: int, K: int, E: int = 1) -> int:
+    return int(_lib.moe_fp8_matmul_workspace(M, N, K, E))
+
+
+def moe_fp8_matmul(a, a_scale, w, w_scale, y, ws=None, counts=None, offsets=None,
+                   stream=None) -> None:
+    """y = a w^T over E4M3 codes with block scales; w [N][K], or [E][N][K] with the rows of
+    each expert given by counts and offsets."""
+    M, K = _matrix(a, "a")
+    dev = _device_of(a, "a")
+    if w.dim() not in (2, 3) or w.shape[-1] != K:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected [N, {K}] or [E, N, {K}]")
+    N, E = w.shape[-2], (w.shape[0] if w.dim() == 3 else 1)
+    kb, nb = (K + 127) // 128, (N + 127) // 128
+    _check(_lib.moe_fp8_matmul(
+        _arg(a, "a", _FP8, None, dev), _arg(a_scale, "a_scale", _F32, M * kb, dev), M,
+        _arg(w, "w", _FP8, None, dev), _arg(w_scale, "w_scale", _F32, E * nb * kb, dev), N, K,
+        _opt(counts, "counts", _I32T, E, dev), _opt(offsets, "offsets", _I32T, E + 1, dev), E,
+        _arg(y, "y", _BF16, M * N, dev), _opt(ws, "ws", _U8, None, dev),
+        0 if ws is None else ws.numel(), _stream(stream)), "moe_fp8_matmul")
+
+
+def moe_expert_ffn_fp8_workspace(W: Experts, T: int, k: int) -> int:
+    return int(_lib.moe_expert_ffn_fp8_workspace(ctypes.byref(W), T, k))
+
+
+def moe_expert_ffn_fp8(W: Experts, slot_of_expert, x, T: int, k: int, counts, offsets, sorted_idx,
+                       y_perm, ws, stream=None) -> None:
+    """moe_expert_ffn over FP8 records with E4M3 activations (see the header).  The buffers may
+    be longer than T rows need (as MoELayer's are)."""
+    dev = _device_of(x, "x")
+    A = T * k
+    for t, name, need in ((x, "x", T * W.H), (sorted_idx, "sorted_idx", A), (y_perm, "y_perm", A * W.H),
+                          (counts, "counts", W.E), (offsets, "offsets", W.E + 1)):
+        if t.numel() < need:
+            raise ValueError(f"{name}: {t.numel()} elements, expected at least {need}")
+    _check(_lib.moe_expert_ffn_fp8(
+        ctypes.byref(W), _opt(slot_of_expert, "slot_of_expert", _I32T, W.E, dev),
+        _arg(x, "x", _BF16, None, dev), T, k, _arg(counts, "counts", _I32T, None, dev),
+        _arg(offsets, "offsets", _I32T, None, dev), _arg(sorted_idx, "sorted_idx", _I32T, None, dev),
+        _arg(y_perm, "y_perm", _BF16, None, dev), _arg(ws, "ws", _U8, None, dev), ws.numel(),
+        _stream(stream)), "moe_expert_ffn_fp8")
 
 
 def moe_version() -> int:

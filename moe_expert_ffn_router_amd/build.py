@@ -19,7 +19,7 @@ OBJ = os.path.join(ROOT, "_build", "obj")
 ARCH = "gfx950"
 
 SOURCES = ["status.cpp", "cache.cpp", "cpu_expert.cpp", "route.hip", "permute.hip", "ffn.hip", "combine.hip",
-           "decode.hip", "shared.hip"]
+           "decode.hip", "shared.hip", "balance.hip", "fp8_mm.hip"]
 # measurement helpers: a library of their own (include/moe_measure.h)
 MEASURE_SOURCES = ["measure/hbm_read.hip"]
 MEASURE_OUT = os.path.join(PKG, "libmoe_measure.so")

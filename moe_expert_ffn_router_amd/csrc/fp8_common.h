@@ -1,0 +1,104 @@
+// Shared by the FP8 product kernels: quantisation of a 128-block to E4M3, the
+// plain E4M3 MFMA, and the lookup of a row tile among the experts' segments.
+// Also the debug-flag readers of the translation units outside the bf16 /
+// FP4 layer path.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+typedef __attribute__((__vector_size__(8 * sizeof(int)))) int fp8x32;  // 32 E4M3 codes
+
+constexpr int kFp8Block = 128;  // columns (and weight rows) of one scale
+
+// D (16 x 16) = A (16 x 128) B (128 x 16) + C, E4M3 operands, unit scales.
+// Lane (g, i) = (lane / 16, lane % 16) holds 32 codes of row i of A (column i
+// of B); the instruction pairs equal byte positions of equal lane groups, so
+// any split of the 128 codes over the groups works that is the same for both.
+// C: lane (g, i) element r is C[4g + r][i].
+__device__ __forceinline__ f32x4 mfma_e4m3(fp8x32 a, fp8x32 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+}
+
+// Scale of a block from the bits of its largest magnitude (an fp32 value):
+// 448 = 1.75 * 2^8, so amax = 1.m * 2^q needs 2^(q-8) where 1.m <= 1.75, else
+// 2^(q-7).  inv = 1 / scale (exact).  Non-finite blocks: NaN scale.
+struct Fp8Scale {
+  float scale, inv;
+  bool finite;
+};
+__device__ __forceinline__ Fp8Scale fp8_block_scale(uint32_t amax_bits) {
+  const int q = (int)(amax_bits >> 23);
+  int b = q - ((amax_bits & 0x7fffffu) <= 0x600000u ? 8 : 7);  // biased exponent of the scale
+  b = b < 1 ? 1 : b;
+  b = amax_bits == 0 ? 127 : b;
+  Fp8Scale s;
+  s.finite = q != 255;
+  s.scale = __uint_as_float(s.finite ? (uint32_t)b << 23 : 0x7fc00000u);
+  s.inv = __uint_as_float((uint32_t)(254 - (s.finite ? b : 127)) << 23);
+  return s;
+}
+
+// Four values of a block -> E4M3 codes in one dword.
+__device__ __forceinline__ int fp8_pack4(float a, float b, float c, float d, const Fp8Scale& s) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * s.inv, b * s.inv, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c * s.inv, d * s.inv, w, true);
+  return s.finite ? w : 0x7f7f7f7f;
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The `tile`-th tile of BM rows, experts in ascending order, found by one
+// whole wave: lane l owns the experts [l * per, l * per + per).
+struct RowTile {
+  int e, row0, rows;
+};
+template <int BM>
+__device__ __forceinline__ bool row_tile(const int* __restrict__ counts,
+                                         const int* __restrict__ offsets, int E, int tile, int lane,
+                                         RowTile& t) {
+  const int per = (E + 63) >> 6;  // at most 16
+  const int first = lane * per;
+  int n[kMaxE / 64], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxE / 64; ++i) {
+    const int c = i < per && first + i < E ? counts[first + i] : 0;
+    n[i] = c > 0 ? c : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kMaxE / 64; ++i) mine += (n[i] + BM - 1) / BM;
+  const int upto = wave_incl_scan(mine);
+  const uint64_t owner = __ballot(tile >= upto - mine && tile < upto);
+  if (!owner) return false;
+  const int ol = (int)__builtin_ctzll(owner);
+  int left = tile - (upto - mine), e = first, rows = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxE / 64; ++i) {
+    const int tiles = (n[i] + BM - 1) / BM;
+    if (rows == 0 && left >= 0 && left < tiles) {
+      e = first + i;
+      rows = n[i] - left * BM;
+      mine = left * BM;  // rows of the expert before this tile
+    }
+    left -= tiles;
+  }
+  t.e = __builtin_amdgcn_readlane(e, ol);
+  const int r = __builtin_amdgcn_readlane(rows, ol);
+  t.row0 = offsets[t.e] + __builtin_amdgcn_readlane(mine, ol);
+  t.rows = r < BM ? r : BM;
+  return true;
+}
+
+// Upper bound on the row tiles of A rows over E experts (host).
+inline int64_t row_tiles_bound(int64_t A, int64_t E, int64_t BM) {
+  const int64_t touched = A < E ? A : E;
+  return (A + touched * (BM - 1)) / BM;
+}
+
+#ifdef MOE_DEBUG
+uint32_t dbg_take_balance();
+uint32_t dbg_take_fp8();
+#endif
+
+}  // namespace moe

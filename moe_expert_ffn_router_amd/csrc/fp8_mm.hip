@@ -1,0 +1,383 @@
+// Products of E4M3 operands with a scale for each block of 128, and what
+// feeds them: quantisation of bf16 rows, the dense / grouped product, and the
+// expert FFN of FP8 records with E4M3 activations.
+//
+// The 16x16x128 MFMA sums one scale block (128 columns) of 16 weight rows and
+// 16 activation rows; its fp32 result t enters the accumulators as
+// acc += (a_scale * w_scale) * t.  The weights are the first operand, so a
+// lane's four results are consecutive output columns of one activation row,
+// whose scale it holds once, and the weight scale is the same for the whole
+// 16-row subtile.
+#include "fp8_common.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// bf16 / fp32 rows -> E4M3.  A thread holds 8 consecutive columns, 16 lanes
+// (one DPP row) a 128-block; short blocks leave lanes without columns.
+// ---------------------------------------------------------------------------
+template <typename SRC>
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(const SRC* __restrict__ x, int T, int K,
+                                                           uint8_t* __restrict__ codes,
+                                                           float* __restrict__ scales) {
+  const int kb = (K + kFp8Block - 1) / kFp8Block;
+  const int64_t n = (int64_t)T * kb * 16;  // 8-column units, rows padded to whole blocks
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < n; u += (int64_t)gridDim.x * 256) {
+    const int64_t block = u >> 4;
+    const int64_t row = block / kb;
+    const int b = (int)(block - row * kb);
+    const int col = b * kFp8Block + (int)(u & 15) * 8;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (col < K) {
+      const SRC* p = x + row * K + col;
+      if constexpr (sizeof(SRC) == 2) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f[2 * q] = __uint_as_float(w[q] << 16);
+          f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+        }
+      } else {
+        const float4 v0 = reinterpret_cast<const float4*>(p)[0];
+        const float4 v1 = reinterpret_cast<const float4*>(p)[1];
+        f[0] = v0.x; f[1] = v0.y; f[2] = v0.z; f[3] = v0.w;
+        f[4] = v1.x; f[5] = v1.y; f[6] = v1.z; f[7] = v1.w;
+      }
+    }
+    uint32_t am = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) am = umax(am, __float_as_uint(f[q]) & 0x7fffffffu);
+    am = umax(am, (uint32_t)dpp_i32<0xB1>((int)am, (int)am));
+    am = umax(am, (uint32_t)dpp_i32<0x4E>((int)am, (int)am));
+    am = umax(am, (uint32_t)dpp_i32<0x141>((int)am, (int)am));
+    am = umax(am, (uint32_t)dpp_i32<0x140>((int)am, (int)am));
+    const Fp8Scale s = fp8_block_scale(am);
+    if (col < K) {
+      const int w0 = fp8_pack4(f[0], f[1], f[2], f[3], s);
+      const int w1 = fp8_pack4(f[4], f[5], f[6], f[7], s);
+      *reinterpret_cast<uint2*>(codes + row * K + col) = uint2{(uint32_t)w0, (uint32_t)w1};
+    }
+    if ((u & 15) == 0) scales[block] = s.scale;
+  }
+}
+
+template <typename SRC>
+void launch_quantize(const SRC* x, int T, int K, uint8_t* codes, float* scales, hipStream_t s) {
+  const int64_t n = (int64_t)T * ((K + kFp8Block - 1) / kFp8Block) * 16;
+  const int64_t blocks = (n + 255) / 256;
+  fp8_quantize_kernel<SRC><<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, s>>>(
+      x, T, K, codes, scales);
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+struct Fp8Args {
+  const uint8_t* a;      // codes [.][K]
+  const float* a_scale;  // [.][kb]
+  const int* row_of;     // GATED: sorted_idx (activation row of p = row_of[p] / k), else NULL
+  int k;
+  const uint8_t* w;  // expert record e: w + slot * w_stride
+  int64_t w_stride;
+  const uint8_t* ws;  // its scales: ws + slot * ws_stride
+  int64_t ws_stride;
+  const int* slot_of;
+  const int* counts;  // NULL: dense, rows [0, M)
+  const int* offsets;
+  int E, M, N, K, I;  // N weight rows (gate/up: 2I)
+  uint16_t* y;        // bf16 [M][N]
+  float* h;           // gate/up: fp32 [M][I]
+};
+
+__device__ __forceinline__ const uint8_t* slot_base(const uint8_t* base, int64_t stride,
+                                                    const Fp8Args& p, int e) {
+  const int slot = p.slot_of ? dbg_clamp(p.slot_of[e], p.E, kDbgSlot) : e;
+  return base + (size_t)slot * stride;
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// Tiles of 16 rows x 64 weight rows; the 4 waves split K (blocks w, w+4, ...)
+// and their sums meet in LDS in wave order.
+template <bool GATED>
+__global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
+  constexpr int NSUB = 4, U = 2, COLS = GATED ? 32 : 64;
+  __shared__ f32x4 red[4][NSUB][64];
+  const int nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
+  const int tile = (int)blockIdx.x / nnb, nb = (int)blockIdx.x - tile * nnb;
+  const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile t;
+  if (p.counts) {
+    if (!row_tile<16>(p.counts, p.offsets, p.E, tile, lane, t)) return;  // uniform per block
+    dbg_segment(t.row0, t.rows, p.M);
+  } else {
+    t.e = 0;
+    t.row0 = tile * 16;
+    t.rows = min(16, p.M - t.row0);
+  }
+  const int K = p.K, kb = (K + kFp8Block - 1) / kFp8Block;
+  const uint8_t* w = slot_base(p.w, p.w_stride, p, t.e);
+  const float* ws = reinterpret_cast<const float*>(slot_base(p.ws, p.ws_stride, p, t.e));
+  const int n0 = nb * COLS;
+  uint32_t wo[NSUB];
+  int so[NSUB];
+#pragma unroll
+  for (int j = 0; j < NSUB; ++j) {
+    int base;
+    if constexpr (GATED) base = (j < 2 ? n0 : p.I + n0) + (j & 1) * 16;
+    else base = n0 + j * 16;
+    const int row = min(base + i16, p.N - 1);
+    wo[j] = (uint32_t)row * (uint32_t)K;
+    so[j] = min(base, p.N - 1) / kFp8Block * kb;
+  }
+  const bool have = i16 < t.rows;
+  size_t arow = 0;
+  if (have) {
+    const int r = t.row0 + i16;
+    arow = p.row_of ? (size_t)(dbg_clamp(p.row_of[r], p.M, kDbgSorted) / p.k) : (size_t)r;
+  }
+  const uint8_t* ap = p.a + arow * K;
+  const float* asp = p.a_scale + arow * kb;
+
+  f32x4 acc[NSUB];
+#pragma unroll
+  for (int j = 0; j < NSUB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const i32x4 zero = {0, 0, 0, 0};
+  for (int c0 = wave; c0 < kb; c0 += 4 * U) {
+    i32x4 wf[U][NSUB][2], af[U][2];
+    float sa[U], sw[U][NSUB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + 4 * u;
+      const int col = c * kFp8Block + 32 * g;  // K a multiple of 16: 16-byte units are whole
+      const bool ok0 = c < kb && col < K, ok1 = c < kb && col + 16 < K;
+#pragma unroll
+      for (int j = 0; j < NSUB; ++j) {
+        wf[u][j][0] = ok0 ? *reinterpret_cast<const i32x4*>(w + wo[j] + col) : zero;
+        wf[u][j][1] = ok1 ? *reinterpret_cast<const i32x4*>(w + wo[j] + col + 16) : zero;
+        sw[u][j] = c < kb ? ws[so[j] + c] : 0.0f;
+      }
+      af[u][0] = ok0 && have ? *reinterpret_cast<const i32x4*>(ap + col) : zero;
+      af[u][1] = ok1 && have ? *reinterpret_cast<const i32x4*>(ap + col + 16) : zero;
+      sa[u] = c < kb && have ? asp[c] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const fp8x32 b = {af[u][0][0], af[u][0][1], af[u][0][2], af[u][0][3],
+                        af[u][1][0], af[u][1][1], af[u][1][2], af[u][1][3]};
+#pragma unroll
+      for (int j = 0; j < NSUB; ++j) {
+        const i32x4 x = wf[u][j][0], y = wf[u][j][1];
+        const fp8x32 a = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        const f32x4 d = mfma_e4m3(a, b, f32x4{0.f, 0.f, 0.f, 0.f});
+        const float s = sa[u] * sw[u][j];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(s, d[r], acc[j][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NSUB; ++j) red[wave][j][lane] = acc[j];
+  __syncthreads();
+  auto total = [&](int j) {
+    f32x4 v = red[0][j][lane];
+#pragma unroll
+    for (int q = 1; q < 4; ++q) {
+      const f32x4 x = red[q][j][lane];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] += x[r];
+    }
+    return v;
+  };
+  if constexpr (GATED) {
+    if (wave < 2) {
+      const f32x4 gv = total(wave), uv = total(wave + 2);
+      const int col = n0 + wave * 16 + 4 * g;
+      if (have && col < p.I)
+        *reinterpret_cast<float4*>(p.h + (size_t)(t.row0 + i16) * p.I + col) =
+            float4{swiglu(gv[0], uv[0]), swiglu(gv[1], uv[1]), swiglu(gv[2], uv[2]),
+                   swiglu(gv[3], uv[3])};
+    }
+  } else {
+    const f32x4 v = total(wave);
+    const int col = n0 + wave * 16 + 4 * g;
+    if (have) {
+      uint16_t* dst = p.y + (size_t)(t.row0 + i16) * p.N + col;
+      if (p.N % 4 == 0) {
+        if (col < p.N) {
+          const uint32_t b0 = f32_to_bf16_rne(v[0]), b1 = f32_to_bf16_rne(v[1]);
+          const uint32_t b2 = f32_to_bf16_rne(v[2]), b3 = f32_to_bf16_rne(v[3]);
+          *reinterpret_cast<uint2*>(dst) = uint2{b0 | (b1 << 16), b2 | (b3 << 16)};
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (col + r < p.N) dst[r] = f32_to_bf16_rne(v[r]);
+      }
+    }
+  }
+}
+
+template <bool GATED>
+int launch_product(const Fp8Args& p, hipStream_t s, const char* who) {
+  const int cols = GATED ? 32 : 64;
+  const int64_t nnb = ((GATED ? p.I : p.N) + cols - 1) / cols;
+  const int64_t tiles = p.counts ? row_tiles_bound(p.M, p.E, 16) : ((int64_t)p.M + 15) / 16;
+  if (nnb * tiles > ((int64_t)1 << 31) - 1)
+    return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+  fp8_rows16_kernel<GATED><<<(unsigned)(nnb * tiles), 256, 0, s>>>(p);
+  return check_launch(who);
+}
+
+// FFN workspace: xq, its scales, h (fp32), hq, its scales.
+struct Fp8FfnWs {
+  size_t xq, xs, h, hq, hs, total;
+};
+Fp8FfnWs fp8_ffn_ws(int64_t T, int64_t k, int64_t H, int64_t I) {
+  auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
+  const int64_t A = T * k;
+  Fp8FfnWs w;
+  w.xq = 0;
+  w.xs = w.xq + up(T * H);
+  w.h = w.xs + up(T * (H / kFp8Block) * 4);
+  w.hq = w.h + up(A * I * 4);
+  w.hs = w.hq + up(A * I);
+  w.total = w.hs + up(A * (I / kFp8Block) * 4) + 256;
+  return w;
+}
+
+}  // namespace
+
+#ifdef MOE_DEBUG
+uint32_t dbg_take_fp8() { return dbg_take_unit(); }
+#endif
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_fp8_quantize(const uint16_t* x, int32_t T, int32_t K, uint8_t* codes,
+                                float* scales, moe_stream_t stream) {
+  const char* who = "moe_fp8_quantize";
+  if (T < 0 || K < 8 || K % 8 || K > 65536)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: need T>=0, K a multiple of 8 in [8, 65536] "
+                     "(T=%d K=%d)", who, T, K);
+  if (T == 0) return MOE_OK;
+  if (!x || !codes || !scales) return set_error(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  launch_quantize<uint16_t>(x, T, K, codes, scales, reinterpret_cast<hipStream_t>(stream));
+  return check_launch(who);
+}
+
+extern "C" size_t moe_fp8_matmul_workspace(int32_t M, int32_t N, int32_t K, int32_t E) {
+  (void)M; (void)N; (void)K; (void)E;
+  return 0;
+}
+
+extern "C" int moe_fp8_matmul(const uint8_t* a, const float* a_scale, int32_t M, const uint8_t* w,
+                              const float* w_scale, int32_t N, int32_t K, const int32_t* counts,
+                              const int32_t* offsets, int32_t E, uint16_t* y, void* ws,
+                              size_t ws_bytes, moe_stream_t stream) {
+  const char* who = "moe_fp8_matmul";
+  if (M < 0 || N < 1 || K < 16 || K % 16 || N > 65536 || K > 65536 || E < 1 || E > kMaxE)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: need M>=0, 1<=N<=65536, K a multiple of 16 in "
+                     "[16, 65536], 1<=E<=%d (M=%d N=%d K=%d E=%d)", who, kMaxE, M, N, K, E);
+  if (!counts != !offsets || (!counts && E != 1))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: counts and offsets go together (both NULL: E = 1)",
+                     who);
+  if (M > (1 << 27) || (int64_t)N * K >= ((int64_t)1 << 32))
+    return set_error(MOE_ERR_UNSUPPORTED, "%s: M=%d N=%d K=%d too large", who, M, N, K);
+  if (M == 0) return MOE_OK;
+  const size_t need = moe_fp8_matmul_workspace(M, N, K, E);
+  if (!a || !a_scale || !w || !w_scale || !y || (need && !ws))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned16(a) || !aligned16(a_scale) || !aligned16(w) || !aligned16(w_scale) ||
+      !aligned16(counts) || !aligned16(offsets) || !aligned16(y) || !aligned16(ws))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  if (ws_bytes < need)
+    return set_error(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
+  const int64_t kb = (K + kFp8Block - 1) / kFp8Block, nb = (N + kFp8Block - 1) / kFp8Block;
+  Fp8Args p{};
+  p.a = a;
+  p.a_scale = a_scale;
+  p.k = 1;
+  p.w = w;
+  p.w_stride = (int64_t)N * K;
+  p.ws = reinterpret_cast<const uint8_t*>(w_scale);
+  p.ws_stride = nb * kb * 4;
+  p.counts = counts;
+  p.offsets = offsets;
+  p.E = E; p.M = M; p.N = N; p.K = K;
+  p.y = y;
+  return launch_product<false>(p, reinterpret_cast<hipStream_t>(stream), who);
+}
+
+extern "C" size_t moe_expert_ffn_fp8_workspace(const moe_experts* W, int32_t T, int32_t k) {
+  if (!W || T < 0 || k < 1 || W->H < 1 || W->I < 1) return 0;
+  return fp8_ffn_ws(T, k, W->H, W->I).total;
+}
+
+extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_expert,
+                                  const uint16_t* x, int32_t T, int32_t k, const int32_t* counts,
+                                  const int32_t* offsets, const int32_t* sorted_idx,
+                                  uint16_t* y_perm, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream) {
+  const char* who = "moe_expert_ffn_fp8";
+  if (!W) return set_error(MOE_ERR_INVALID_ARG, "%s: W is NULL", who);
+  if (W->E < 1 || W->E > kMaxE) return set_error(MOE_ERR_INVALID_ARG, "%s: E=%d", who, W->E);
+  Layout L;
+  if (W->fmt != MOE_W_FP8_B128 || !layout_of(W->fmt, W->H, W->I, &L))
+    return set_error(MOE_ERR_UNSUPPORTED, "%s: needs FP8 block-scaled weights (fmt=%d H=%d I=%d)",
+                     who, W->fmt, W->H, W->I);
+  if (!W->base || !aligned16(W->base)) return set_error(MOE_ERR_INVALID_ARG, "%s: base", who);
+  if (W->stride < L.stride || W->stride % 256)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: stride %lld (need >= %lld, multiple of 256)", who,
+                     (long long)W->stride, (long long)L.stride);
+  if (T < 0 || k < 1 || k > W->E || k > kMaxK)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: need T>=0, 1<=k<=min(E,%d)", who, kMaxK);
+  const int64_t A = (int64_t)T * k;
+  if (A > (1 << 27)) return set_error(MOE_ERR_UNSUPPORTED, "%s: T*k too large", who);
+  if (T == 0) return MOE_OK;
+  if (!x || !counts || !offsets || !sorted_idx || !y_perm || !ws)
+    return set_error(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned16(x) || !aligned16(counts) || !aligned16(offsets) || !aligned16(sorted_idx) ||
+      !aligned16(y_perm) || !aligned16(ws) || !aligned16(slot_of_expert))
+    return set_error(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  const int H = W->H, I = W->I;
+  const Fp8FfnWs B = fp8_ffn_ws(T, k, H, I);
+  if (ws_bytes < B.total)
+    return set_error(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, B.total);
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  const uint8_t* rec = static_cast<const uint8_t*>(W->base);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  launch_quantize<uint16_t>(x, T, H, wb + B.xq, reinterpret_cast<float*>(wb + B.xs), s);
+  Fp8Args p{};
+  p.a = wb + B.xq;
+  p.a_scale = reinterpret_cast<const float*>(wb + B.xs);
+  p.row_of = sorted_idx;
+  p.k = k;
+  p.w = rec + L.w13;
+  p.ws = rec + L.w13s;
+  p.w_stride = p.ws_stride = W->stride;
+  p.slot_of = slot_of_expert;
+  p.counts = counts;
+  p.offsets = offsets;
+  p.E = W->E; p.M = (int)A; p.N = 2 * I; p.K = H; p.I = I;
+  p.h = reinterpret_cast<float*>(wb + B.h);
+  int st = launch_product<true>(p, s, who);
+  if (st) return st;
+  launch_quantize<float>(p.h, (int)A, I, wb + B.hq, reinterpret_cast<float*>(wb + B.hs), s);
+  Fp8Args d = p;
+  d.a = wb + B.hq;
+  d.a_scale = reinterpret_cast<const float*>(wb + B.hs);
+  d.row_of = nullptr;
+  d.w = rec + L.w2;
+  d.ws = rec + L.w2s;
+  d.N = H; d.K = I;
+  d.y = y_perm;
+  return launch_product<false>(d, s, who);
+}

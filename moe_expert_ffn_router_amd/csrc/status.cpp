@@ -2,6 +2,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include "fp8_common.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -77,7 +78,8 @@ int moe_version(void) { return 1; }
 int moe_debug_take(uint32_t* flags) {
   if (!flags) return moe::set_error(MOE_ERR_INVALID_ARG, "moe_debug_take: flags is NULL");
 #ifdef MOE_DEBUG
-  *flags = moe::dbg_take_ffn() | moe::dbg_take_decode() | moe::dbg_take_combine();
+  *flags = moe::dbg_take_ffn() | moe::dbg_take_decode() | moe::dbg_take_combine() |
+           moe::dbg_take_balance() | moe::dbg_take_fp8();
   return MOE_OK;
 #else
   *flags = 0;

@@ -14,8 +14,10 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (Experts, experts, moe_combine, moe_expert_ffn, moe_expert_ffn_workspace,
-               moe_expert_ffn_hybrid_host_bytes, moe_expert_ffn_streamed_workspace,
+from . import (Experts, experts, moe_balance_loss, moe_balance_loss_workspace, moe_combine,
+               moe_expert_ffn, moe_expert_ffn_fp8, moe_expert_ffn_fp8_workspace,
+               moe_expert_ffn_workspace, moe_expert_ffn_hybrid_host_bytes,
+               moe_expert_ffn_streamed_workspace, moe_route_backward,
                moe_forward_decode, moe_forward_decode_supported, moe_forward_decode_workspace,
                moe_shared_ffn, moe_shared_ffn_workspace,
                moe_permute, moe_permute_workspace, moe_route, moe_route_permute)
@@ -49,6 +51,7 @@ class MoELayer:
                                   dtype=torch.uint8, device=dev)
         self._probe = probe
         self.stream_ws = None                 # streamed cache path: made on first use
+        self.fp8_ws = None                    # variant "fp8": made on first use
         self.counts_host = torch.zeros(E, dtype=torch.int32).pin_memory()
         self.plan_out = tuple(torch.zeros(E, dtype=torch.int32) for _ in range(3))
         self.hybrid_out = tuple(torch.zeros(E, dtype=torch.int32) for _ in range(4))
@@ -80,6 +83,16 @@ class MoELayer:
 
     def expert_ffn(self, W: Experts, x: torch.Tensor, T: int, slot_of_expert=None,
                    variant="auto", stream=None):
+        """The routed experts.  variant "fp8" (FP8 records only) takes the activations of both
+        products in E4M3 (moe_expert_ffn_fp8); the others keep bf16 activations."""
+        if variant == "fp8":
+            if self.fp8_ws is None:
+                self.fp8_ws = torch.empty(
+                    max(moe_expert_ffn_fp8_workspace(self._probe, self.T_max, self.k), 256),
+                    dtype=torch.uint8, device=self.device)
+            moe_expert_ffn_fp8(W, slot_of_expert, x, T, self.k, self.counts, self.offsets,
+                               self.sorted_idx, self.y_perm, self.fp8_ws, stream)
+            return
         moe_expert_ffn(W, slot_of_expert, x, T, self.k, self.counts, self.offsets, self.sorted_idx,
                        self.y_perm, self.ffn_ws, variant, stream)
 
@@ -95,6 +108,38 @@ class MoELayer:
         moe_route_permute(logits, self.k, self.ids, self.w, self.counts, self.offsets,
                           self.sorted_idx, self.inv_idx, self.perm_ws, self.renorm, stream)
         return logits.shape[0]
+
+    # -- router training ------------------------------------------------------
+    def balance_loss(self, logits: torch.Tensor, token_mask=None, seq_offsets=None,
+                     stream=None) -> dict:
+        """Load-balance loss of the batch last routed (self.ids), per sequence, with the
+        per-expert counts and probability sums (moe_balance_loss)."""
+        T, E = logits.shape
+        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        i32 = dict(dtype=torch.int32, device=self.device)
+        f32 = dict(dtype=torch.float32, device=self.device)
+        r = {"n_tokens": torch.empty(S, **i32), "counts": torch.empty(S, E, **i32),
+             "probs": torch.empty(S, E, **f32), "loss": torch.empty(S, **f32)}
+        ws = torch.empty(max(moe_balance_loss_workspace(T, E, S), 256), dtype=torch.uint8,
+                         device=self.device)
+        moe_balance_loss(logits, self.ids[:T * self.k], self.k, r["n_tokens"], r["counts"],
+                         r["probs"], r["loss"], ws, token_mask, seq_offsets, stream)
+        if stream is not None:          # the scratch is in use there after this call returns
+            ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                             else stream)
+        return r
+
+    def route_backward(self, logits: torch.Tensor, d_logits: torch.Tensor, d_topk_w=None,
+                       balance: dict | None = None, d_loss=None, token_mask=None,
+                       seq_offsets=None, stream=None) -> torch.Tensor:
+        """Gradient of the routing weights last written (d_topk_w [T*k]) and of balance_loss's
+        result (d_loss [S]) with respect to the logits, into d_logits (moe_route_backward)."""
+        T = logits.shape[0]
+        b = balance or {}
+        moe_route_backward(logits, self.k, self.ids[:T * self.k], self.w[:T * self.k], d_topk_w,
+                           b.get("n_tokens"), b.get("counts"), d_loss, d_logits, self.renorm,
+                           token_mask, seq_offsets, stream)
+        return d_logits
 
     # -- whole layer ----------------------------------------------------------
     def weights(self, base) -> Experts:

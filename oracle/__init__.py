@@ -22,4 +22,4 @@ plainest one and is stated in the module that takes it.
 
 Parity status per function is stated in each module's header.
 """
-from . import formats, route, permute, ffn, combine, lru, layer  # noqa: F401
+from . import formats, route, permute, ffn, combine, lru, layer, balance, fp8  # noqa: F401
