@@ -9,6 +9,7 @@
 // whose scale it holds once, and the weight scale is the same for the whole
 // 16-row subtile.
 #include "fp8_common.h"
+#include "lds_copy.h"
 
 namespace moe {
 namespace {
@@ -88,7 +89,10 @@ struct Fp8Args {
   const int* offsets;
   int E, M, N, K, I;  // N weight rows (gate/up: 2I)
   uint16_t* y;        // bf16 [M][N]
-  float* h;           // gate/up: fp32 [M][I]
+  float* h;           // gate/up, few rows: fp32 [M][I]
+  uint8_t* hq;        // gate/up, tiles: E4M3 [M][I]
+  float* hs;          // and its scales [M][I/128]
+  int mt, nnb;        // tiles: row tiles (dense) and column blocks
 };
 
 __device__ __forceinline__ const uint8_t* slot_base(const uint8_t* base, int64_t stride,
@@ -221,8 +225,295 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tiles of BM rows x BN weight rows on WM x WN waves, K in blocks of 128.
+// Both operands and the rows' scales are copied from memory straight into LDS,
+// one block ahead (two stages, one barrier per block).  A wave owns MI x NJ
+// subtiles of 16 x 16: it keeps the block's NJ weight fragments in registers
+// and streams its MI activation fragments past them; each MFMA starts from zero
+// and its result is folded into the accumulators one row subtile later.
+// ---------------------------------------------------------------------------
+template <int BM, int BN>
+struct TileStage {
+  uint8_t a[BM * 128];  // [row][128 codes], 16-byte unit u stored at u ^ a_swz(row)
+  uint8_t b[BN * 128];  // weights, same layout
+  float s[BM];          // the rows' scales of this block
+};
+
+// m-tiles that consecutive workgroups of one XCD share weights over
+constexpr int kPanel = 4;
+
+// Workgroup -> (row tile, column block).  Hardware block b runs on XCD b % 8.
+// Dense: the tiles in panels of kPanel row tiles, column block by column block,
+// cut into eight contiguous ranges.  Grouped: the number of tiles is only bounded
+// on the host and the ones that hold rows come first, so whole panels go to the
+// XCDs in turn.
+__device__ __forceinline__ bool tile_of(const Fp8Args& p, int b, int& tile, int& nb) {
+  const int nnb = p.nnb;
+  if (p.counts) {
+    const int S = kPanel * nnb, x = b & 7, j = b >> 3;
+    const int sl = j / S, r = j - sl * S;
+    tile = (sl * 8 + x) * kPanel + r % kPanel;
+    nb = r / kPanel;
+    return true;
+  }
+  const int G = p.mt * nnb, per = (G + 7) >> 3;
+  const int v = (b & 7) * per + (b >> 3);
+  if ((b >> 3) >= per || v >= G) return false;
+  const int panel = v / (kPanel * nnb), r = v - panel * (kPanel * nnb);
+  const int rows = min(kPanel, p.mt - panel * kPanel);
+  nb = r / rows;
+  tile = panel * kPanel + r - nb * rows;
+  return true;
+}
+
+template <int BM, int BN, int WM, int WN, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
+  constexpr int NW = WM * WN, MI = BM / WM / 16, NJ = BN / WN / 16;
+  constexpr int COLS = GATED ? BN / 2 : BN;    // output columns
+  constexpr int CPA = BM / 8 / NW, CPB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
+  static_assert(NJ == 4 && BM % 64 == 0 && BM / 64 <= NW, "wave shape");
+  static_assert(!GATED || COLS == kFp8Block, "gate/up: one scale block of h per tile");
+  __shared__ TileStage<BM, BN> st[2];
+  __shared__ float row_max[GATED ? WN : 1][GATED ? BM : 1];
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mh = wave / WN, nh = wave % WN;
+  int tile, nb;
+  if (!tile_of(p, (int)blockIdx.x, tile, nb)) return;
+  RowTile t;
+  if (p.counts) {
+    if (!row_tile<BM>(p.counts, p.offsets, p.E, tile, lane, t)) return;  // uniform per block
+    dbg_segment(t.row0, t.rows, p.M);
+    if (t.rows <= 0) return;
+  } else {
+    t.e = 0;
+    t.row0 = tile * BM;
+    t.rows = min(BM, p.M - t.row0);
+  }
+  const int row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  const int rows = __builtin_amdgcn_readfirstlane(t.rows);
+  const int e = __builtin_amdgcn_readfirstlane(t.e);
+  const int K = p.K, kb = (K + kFp8Block - 1) / kFp8Block;
+  const uint8_t* w = slot_base(p.w, p.w_stride, p, e);
+  const float* ws = reinterpret_cast<const float*>(slot_base(p.ws, p.ws_stride, p, e));
+
+  // activation row of local row lr: rows past the tile read its last one
+  auto source = [&](int lr) -> uint32_t {
+    const int r = min(lr, rows - 1);
+    if (p.row_of) return (uint32_t)(dbg_clamp(p.row_of[row0 + r], p.M, kDbgSorted) / p.k);
+    return (uint32_t)r;
+  };
+  const uint8_t* ab = p.row_of ? p.a : p.a + (size_t)row0 * K;
+  const uint8_t* sb = reinterpret_cast<const uint8_t*>(p.row_of ? p.a_scale
+                                                                : p.a_scale + (size_t)row0 * kb);
+  const uint8_t* wb = GATED ? w : w + (size_t)nb * BN * K;
+  uint32_t ao[CPA], wo[CPB], so = 0;
+  const uint32_t unit = (uint32_t)(lane & 7);
+#pragma unroll
+  for (int q = 0; q < CPA; ++q) {
+    const int lr = (wave * CPA + q) * 8 + (lane >> 3);
+    ao[q] = source(lr) * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
+  }
+#pragma unroll
+  for (int q = 0; q < CPB; ++q) {
+    const int lr = (wave * CPB + q) * 8 + (lane >> 3);
+    int wr;
+    if constexpr (GATED) {  // a wave's 64 weight rows: 32 gate rows, then their up rows
+      const int col = nb * COLS + (lr >> 6) * 32 + (lr & 31);
+      wr = (lr & 32) ? p.I + col : col;
+    } else {
+      wr = min(lr, p.N - 1 - nb * BN);
+    }
+    wo[q] = (uint32_t)wr * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
+  }
+  if (wave < BM / 64) so = source(wave * 64 + lane) * (uint32_t)kb * 4u;
+  auto issue = [&](int c, TileStage<BM, BN>& S) {
+    const uint32_t k0 = (uint32_t)(c * kFp8Block);
+    const uint32_t left = (uint32_t)K - k0;  // a short last block: units past K re-read its first
+#pragma unroll
+    for (int q = 0; q < CPA; ++q) {
+      const int n = wave * CPA + q;
+      const uint32_t u = (unit ^ a_swz(n * 8 + (lane >> 3))) * 16;
+      dma16(ab, ao[q] + k0 - (u < left ? 0 : u), S.a + n * 1024);
+    }
+#pragma unroll
+    for (int q = 0; q < CPB; ++q) {
+      const int n = wave * CPB + q;
+      const uint32_t u = (unit ^ a_swz(n * 8 + (lane >> 3))) * 16;
+      dma16(wb, wo[q] + k0 - (u < left ? 0 : u), S.b + n * 1024);
+    }
+    if (wave < BM / 64) dma4(sb, so + (uint32_t)c * 4u, S.s + wave * 64);
+  };
+
+  f32x4 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // weight scales: one per wave and block (gate/up: one each)
+  int sblk0, sblk1 = 0;
+  if constexpr (GATED) {
+    sblk0 = nb * kb;
+    sblk1 = (p.I / kFp8Block + nb) * kb;
+  } else {
+    sblk0 = min(nb * BN + nh * (BN / WN), p.N - 1) / kFp8Block * kb;
+  }
+  auto frag = [&](const uint8_t* base, int r) {
+    const int sw = a_swz(r);
+    const i32x4 x = *reinterpret_cast<const i32x4*>(base + r * 128 + (((2 * g) ^ sw) * 16));
+    const i32x4 y = *reinterpret_cast<const i32x4*>(base + r * 128 + (((2 * g + 1) ^ sw) * 16));
+    return fp8x32{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
+  auto compute = [&](const TileStage<BM, BN>& S, float w0, float w1) {
+    fp8x32 bf[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bf[j] = frag(S.b, nh * (BN / WN) + j * 16 + l16);
+    const int r0 = mh * (BM / WM) + l16;
+    fp8x32 af = frag(S.a, r0);
+    float sa = S.s[r0];
+    f32x4 d[NJ];
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      fp8x32 an = af;
+      float sn = 0.f;
+      if (i + 1 < MI) {
+        an = frag(S.a, r0 + (i + 1) * 16);
+        sn = S.s[r0 + (i + 1) * 16];
+      }
+      f32x4 dn[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) dn[j] = mfma_e4m3(bf[j], af, f32x4{0.f, 0.f, 0.f, 0.f});
+      if (i > 0) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[i - 1][j][r] = fmaf(GATED && j >= 2 ? s1 : s0, d[j][r], acc[i - 1][j][r]);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) d[j] = dn[j];
+      s0 = sa * w0;
+      s1 = sa * w1;
+      af = an;
+      sa = sn;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[MI - 1][j][r] = fmaf(GATED && j >= 2 ? s1 : s0, d[j][r], acc[MI - 1][j][r]);
+  };
+
+  issue(0, st[0]);
+  float w0 = ws[sblk0], w1 = GATED ? ws[sblk1] : 0.f;
+  for (int c = 0; c < kb; ++c) {
+    TileStage<BM, BN>& S = st[c & 1];
+    MOE_DMA_SYNC(0);
+    const int cn = min(c + 1, kb - 1);
+    const float n0 = ws[sblk0 + cn], n1 = GATED ? ws[sblk1 + cn] : 0.f;
+    if (c + 1 < kb) {
+      issue(c + 1, st[(c + 1) & 1]);
+    } else if (K % kFp8Block) {  // zeros past K in the short last block
+      const int u0 = K % kFp8Block / 16, nu = 8 - u0;
+      for (int i = tid; i < (BM + BN) * nu; i += 64 * NW) {
+        const int r = i / nu, u = u0 + i - r * nu, lr = r < BM ? r : r - BM;
+        *reinterpret_cast<i32x4*>((r < BM ? S.a : S.b) + lr * 128 + ((u ^ a_swz(lr)) * 16)) =
+            i32x4{0, 0, 0, 0};
+      }
+      __syncthreads();
+    }
+    compute(S, w0, w1);
+    w0 = n0;
+    w1 = n1;
+  }
+
+  // acc[i][j][r]: row mh*(BM/WM) + 16i + l16, weight row nh*64 + 16j + 4g + r of the tile
+  const int rl = mh * (BM / WM) + l16;
+  if constexpr (GATED) {
+    // h in place of the gate sums, its largest magnitude per row over the waves' 32 columns
+    float hm[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[i][j][r] = swiglu(acc[i][j][r], acc[i][j + 2][r]);
+          m = umax(m, __float_as_uint(acc[i][j][r]) & 0x7fffffffu);
+        }
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+      hm[i] = __uint_as_float(m);
+      if (g == 0) row_max[nh][rl + i * 16] = hm[i];
+    }
+    __syncthreads();
+    uint8_t* hc = st[0].a;  // the tile's codes [BM][128], written out by whole rows
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int q = 0; q < WN; ++q) m = umax(m, __float_as_uint(row_max[q][rl + i * 16]));
+      const Fp8Scale s = fp8_block_scale(m);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<int*>(hc + (rl + i * 16) * 128 + nh * 32 + j * 16 + 4 * g) =
+            fp8_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], s);
+      if (nh == 0 && g == 0 && rl + i * 16 < rows)
+        p.hs[(size_t)(row0 + rl + i * 16) * (p.I / kFp8Block) + nb] = s.scale;
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * 8; i += 64 * NW)
+      *reinterpret_cast<i32x4*>(p.hq + (size_t)(row0 + (i >> 3)) * p.I + nb * COLS + (i & 7) * 16) =
+          *reinterpret_cast<const i32x4*>(hc + i * 16);
+  } else {
+    const int col0 = nb * BN + nh * (BN / WN) + 4 * g;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (rl + i * 16 >= rows) continue;
+      uint16_t* dst = p.y + (size_t)(row0 + rl + i * 16) * p.N + col0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const uint32_t b0 = f32_to_bf16_rne(acc[i][j][0]), b1 = f32_to_bf16_rne(acc[i][j][1]);
+        const uint32_t b2 = f32_to_bf16_rne(acc[i][j][2]), b3 = f32_to_bf16_rne(acc[i][j][3]);
+        const int col = col0 + j * 16;
+        if (p.N % 4 == 0) {
+          if (col < p.N)
+            *reinterpret_cast<uint2*>(dst + j * 16) = uint2{b0 | (b1 << 16), b2 | (b3 << 16)};
+        } else {
+          if (col < p.N) dst[j * 16] = (uint16_t)b0;
+          if (col + 1 < p.N) dst[j * 16 + 1] = (uint16_t)b1;
+          if (col + 2 < p.N) dst[j * 16 + 2] = (uint16_t)b2;
+          if (col + 3 < p.N) dst[j * 16 + 3] = (uint16_t)b3;
+        }
+      }
+    }
+  }
+}
+
+template <int BM, int BN, int WM, int WN, bool GATED>
+int launch_tiles(Fp8Args p, hipStream_t s, const char* who) {
+  constexpr int COLS = GATED ? BN / 2 : BN;
+  p.nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
+  int64_t blocks;
+  if (p.counts) {
+    const int64_t bound = row_tiles_bound(p.M, p.E, BM);
+    blocks = (bound + 8 * kPanel - 1) / (8 * kPanel) * (8 * kPanel) * p.nnb;
+  } else {
+    p.mt = (p.M + BM - 1) / BM;
+    blocks = ((int64_t)p.mt * p.nnb + 7) / 8 * 8;
+  }
+  if (blocks > ((int64_t)1 << 31) - 1)
+    return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+  fp8_tile_kernel<BM, BN, WM, WN, GATED><<<(unsigned)blocks, 64 * WM * WN, 0, s>>>(p);
+  return check_launch(who);
+}
+
 template <bool GATED>
-int launch_product(const Fp8Args& p, hipStream_t s, const char* who) {
+int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
   const int cols = GATED ? 32 : 64;
   const int64_t nnb = ((GATED ? p.I : p.N) + cols - 1) / cols;
   const int64_t tiles = p.counts ? row_tiles_bound(p.M, p.E, 16) : ((int64_t)p.M + 15) / 16;
@@ -313,7 +604,9 @@ extern "C" int moe_fp8_matmul(const uint8_t* a, const float* a_scale, int32_t M,
   p.offsets = offsets;
   p.E = E; p.M = M; p.N = N; p.K = K;
   p.y = y;
-  return launch_product<false>(p, reinterpret_cast<hipStream_t>(stream), who);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (M <= 32 * (int64_t)E) return launch_rows16<false>(p, s, who);
+  return launch_tiles<256, 256, 2, 4, false>(p, s, who);
 }
 
 extern "C" size_t moe_expert_ffn_fp8_workspace(const moe_experts* W, int32_t T, int32_t k) {
@@ -368,9 +661,19 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   p.offsets = offsets;
   p.E = W->E; p.M = (int)A; p.N = 2 * I; p.K = H; p.I = I;
   p.h = reinterpret_cast<float*>(wb + B.h);
-  int st = launch_product<true>(p, s, who);
-  if (st) return st;
-  launch_quantize<float>(p.h, (int)A, I, wb + B.hq, reinterpret_cast<float*>(wb + B.hs), s);
+  p.hq = wb + B.hq;
+  p.hs = reinterpret_cast<float*>(wb + B.hs);
+  // the tile kernel addresses the gathered activation rows with 32-bit offsets
+  const bool tiles = A > 32 * (int64_t)W->E && (int64_t)T * H < ((int64_t)1 << 32);
+  int st;
+  if (tiles) {
+    st = launch_tiles<256, 256, 2, 4, true>(p, s, who);
+    if (st) return st;
+  } else {
+    st = launch_rows16<true>(p, s, who);
+    if (st) return st;
+    launch_quantize<float>(p.h, (int)A, I, p.hq, p.hs, s);
+  }
   Fp8Args d = p;
   d.a = wb + B.hq;
   d.a_scale = reinterpret_cast<const float*>(wb + B.hs);
@@ -379,5 +682,5 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   d.ws = rec + L.w2s;
   d.N = H; d.K = I;
   d.y = y_perm;
-  return launch_product<false>(d, s, who);
+  return tiles ? launch_tiles<256, 256, 2, 4, false>(d, s, who) : launch_rows16<false>(d, s, who);
 }
