@@ -21,6 +21,10 @@ __device__ __forceinline__ f32x4 mfma_e4m3(fp8x32 a, fp8x32 b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
 }
 
+// Keeps a value at this point of the program: without it the compiler moves an MFMA
+// down to the first use of its result, and the loop's order with it.
+__device__ __forceinline__ void pin(f32x4& v) { asm volatile("" : "+v"(v)); }
+
 // Scale of a block from the bits of its largest magnitude (an fp32 value):
 // 448 = 1.75 * 2^8, so amax = 1.m * 2^q needs 2^(q-8) where 1.m <= 1.75, else
 // 2^(q-7).  inv = 1 / scale (exact).  Non-finite blocks: NaN scale.

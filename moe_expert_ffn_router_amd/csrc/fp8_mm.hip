@@ -227,17 +227,23 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
 
 // ---------------------------------------------------------------------------
 // Tiles of BM rows x BN weight rows on WM x WN waves, K in blocks of 128.
-// Both operands and the rows' scales are copied from memory straight into LDS,
-// one block ahead (two stages, one barrier per block).  A wave owns MI x NJ
-// subtiles of 16 x 16: it keeps the block's NJ weight fragments in registers
-// and streams its MI activation fragments past them; each MFMA starts from zero
-// and its result is folded into the accumulators one row subtile later.
+// Both operands are copied from memory straight into LDS, two blocks deep; the
+// rows' scales likewise, four blocks at a time.  A wave owns MI x NJ subtiles of
+// 16 x 16: it keeps the block's NJ weight fragments in registers and streams its
+// MI activation fragments past them; each MFMA starts from zero and its result
+// is folded into the accumulators one row subtile later, so the fold's
+// multiply-adds run under the next MFMAs.
+//   The copies bound this kernel (a block's 64 KB take longer to arrive than
+// to multiply), so a stage is refilled piece by piece as it is read rather than
+// as a whole at its end: the weights once every wave holds its fragments (row
+// subtile 1), the first half of each wave's rows at subtile MI/2, the second at
+// the last.  Every piece then has at least one block's time to arrive, and the
+// waits leave the pieces issued since outstanding.
 // ---------------------------------------------------------------------------
 template <int BM, int BN>
 struct TileStage {
   uint8_t a[BM * 128];  // [row][128 codes], 16-byte unit u stored at u ^ a_swz(row)
   uint8_t b[BN * 128];  // weights, same layout
-  float s[BM];          // the rows' scales of this block
 };
 
 // m-tiles that consecutive workgroups of one XCD share weights over
@@ -267,6 +273,13 @@ __device__ __forceinline__ bool tile_of(const Fp8Args& p, int b, int& tile, int&
   return true;
 }
 
+// Waits for this wave's LDS reads, then a barrier that no memory access moves across.
+#define MOE_LDS_SYNC()                                                   \
+  do {                                                                   \
+    __builtin_amdgcn_s_waitcnt(::moe::waitcnt_vm_lgkm0(63));             \
+    asm volatile("s_barrier" ::: "memory");                              \
+  } while (0)
+
 template <int BM, int BN, int WM, int WN, bool GATED>
 __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   constexpr int NW = WM * WN, MI = BM / WM / 16, NJ = BN / WN / 16;
@@ -275,6 +288,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   static_assert(NJ == 4 && BM % 64 == 0 && BM / 64 <= NW, "wave shape");
   static_assert(!GATED || COLS == kFp8Block, "gate/up: one scale block of h per tile");
   __shared__ TileStage<BM, BN> st[2];
+  __shared__ __attribute__((aligned(16))) float sc[2][BM * 4];  // [row][4 blocks]
+  __shared__ float wsc[2][65536 / kFp8Block];  // the tile's two rows of weight scales
   __shared__ float row_max[GATED ? WN : 1][GATED ? BM : 1];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -310,9 +325,16 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   const uint8_t* wb = GATED ? w : w + (size_t)nb * BN * K;
   uint32_t ao[CPA], wo[CPB], so = 0;
   const uint32_t unit = (uint32_t)(lane & 7);
+  // local row that copy q of this wave starts at: the first CPA / 2 cover the first halves of
+  // the waves' row groups, the others the second halves
+  constexpr int RW = BM / WM, HALF = RW / 2;
+  auto a_row = [&](int q) {
+    const int x = (wave * (CPA / 2) + q % (CPA / 2)) * 8;
+    return x / HALF * RW + x % HALF + (q < CPA / 2 ? 0 : HALF);
+  };
 #pragma unroll
   for (int q = 0; q < CPA; ++q) {
-    const int lr = (wave * CPA + q) * 8 + (lane >> 3);
+    const int lr = a_row(q) + (lane >> 3);
     ao[q] = source(lr) * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
   }
 #pragma unroll
@@ -328,22 +350,41 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
     wo[q] = (uint32_t)wr * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
   }
   if (wave < BM / 64) so = source(wave * 64 + lane) * (uint32_t)kb * 4u;
-  auto issue = [&](int c, TileStage<BM, BN>& S) {
-    const uint32_t k0 = (uint32_t)(c * kFp8Block);
-    const uint32_t left = (uint32_t)K - k0;  // a short last block: units past K re-read its first
+  // a short last block: units past K re-read its first
+  auto back = [&](int lr) -> uint32_t {
+    const uint32_t u = (unit ^ a_swz(lr)) * 16;
+    return u < (uint32_t)(K % kFp8Block) ? 0u : u;
+  };
+  auto is_short = [&](int c) { return c + 1 == kb && K % kFp8Block != 0; };
+  auto issue_a = [&](int c, int half) {
+    uint8_t* dst = st[c & 1].a;
+    const uint8_t* src = ab + (size_t)c * kFp8Block;
+    const bool cut = is_short(c);
 #pragma unroll
-    for (int q = 0; q < CPA; ++q) {
-      const int n = wave * CPA + q;
-      const uint32_t u = (unit ^ a_swz(n * 8 + (lane >> 3))) * 16;
-      dma16(ab, ao[q] + k0 - (u < left ? 0 : u), S.a + n * 1024);
-    }
+    for (int q = half * (CPA / 2); q < (half + 1) * (CPA / 2); ++q)
+      dma16(src, cut ? ao[q] - back(a_row(q) + (lane >> 3)) : ao[q], dst + a_row(q) * 128);
+  };
+  auto issue_b = [&](int c) {
+    uint8_t* dst = st[c & 1].b + wave * CPB * 1024;
+    const uint8_t* src = wb + (size_t)c * kFp8Block;
+    const bool cut = is_short(c);
 #pragma unroll
-    for (int q = 0; q < CPB; ++q) {
-      const int n = wave * CPB + q;
-      const uint32_t u = (unit ^ a_swz(n * 8 + (lane >> 3))) * 16;
-      dma16(wb, wo[q] + k0 - (u < left ? 0 : u), S.b + n * 1024);
-    }
-    if (wave < BM / 64) dma4(sb, so + (uint32_t)c * 4u, S.s + wave * 64);
+    for (int q = 0; q < CPB; ++q)
+      dma16(src, cut ? wo[q] - back((wave * CPB + q) * 8 + (lane >> 3)) : wo[q], dst + q * 1024);
+  };
+  // the rows' scales of blocks [s_first(f), s_first(f) + 4) as group f; fewer than four blocks
+  // in all: one at a time, each a group
+  const bool quad = kb >= 4;
+  auto s_first = [&](int f) { return quad ? min(4 * f, kb - 4) : f; };
+  auto issue_s = [&](int f) {
+    if (wave >= BM / 64) return;
+    float* dst = sc[f & 1] + wave * 64 * (quad ? 4 : 1);
+    if (quad) dma16(sb, so + (uint32_t)s_first(f) * 4u, dst);
+    else dma4(sb, so + (uint32_t)f * 4u, dst);
+  };
+  auto scale_of = [&](int c, int r) {
+    const int f = quad ? c >> 2 : c;
+    return quad ? sc[f & 1][r * 4 + c - s_first(f)] : sc[f & 1][r];
   };
 
   f32x4 acc[MI][NJ];
@@ -352,83 +393,132 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // weight scales: one per wave and block (gate/up: one each)
-  int sblk0, sblk1 = 0;
-  if constexpr (GATED) {
-    sblk0 = nb * kb;
-    sblk1 = (p.I / kFp8Block + nb) * kb;
-  } else {
-    sblk0 = min(nb * BN + nh * (BN / WN), p.N - 1) / kFp8Block * kb;
+  // the tile's weight scales: its two 128-row blocks (gate/up: the gate and the up block)
+  for (int i = tid; i < kb; i += 64 * NW) {
+    const int last = (p.N - 1) / kFp8Block;
+    const int b0 = GATED ? nb : min(nb * (BN / kFp8Block), last);
+    const int b1 = GATED ? p.I / kFp8Block + nb : min(nb * (BN / kFp8Block) + 1, last);
+    wsc[0][i] = ws[b0 * kb + i];
+    wsc[1][i] = ws[b1 * kb + i];
   }
-  auto frag = [&](const uint8_t* base, int r) {
-    const int sw = a_swz(r);
-    const i32x4 x = *reinterpret_cast<const i32x4*>(base + r * 128 + (((2 * g) ^ sw) * 16));
-    const i32x4 y = *reinterpret_cast<const i32x4*>(base + r * 128 + (((2 * g + 1) ^ sw) * 16));
+  const float* wsw = wsc[GATED ? 0 : nh * (BN / WN) / kFp8Block];
+  __syncthreads();
+  // A row's swizzle depends on its low 4 bits only: one address per operand and unit, the
+  // subtiles at constant offsets.
+  auto frag = [&](const uint8_t* base, int o0, int o1) {
+    const i32x4 x = *reinterpret_cast<const i32x4*>(base + o0);
+    const i32x4 y = *reinterpret_cast<const i32x4*>(base + o1);
     return fp8x32{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   };
-  auto compute = [&](const TileStage<BM, BN>& S, float w0, float w1) {
-    fp8x32 bf[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) bf[j] = frag(S.b, nh * (BN / WN) + j * 16 + l16);
-    const int r0 = mh * (BM / WM) + l16;
-    fp8x32 af = frag(S.a, r0);
-    float sa = S.s[r0];
-    f32x4 d[NJ];
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      fp8x32 an = af;
-      float sn = 0.f;
-      if (i + 1 < MI) {
-        an = frag(S.a, r0 + (i + 1) * 16);
-        sn = S.s[r0 + (i + 1) * 16];
-      }
-      f32x4 dn[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) dn[j] = mfma_e4m3(bf[j], af, f32x4{0.f, 0.f, 0.f, 0.f});
-      if (i > 0) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[i - 1][j][r] = fmaf(GATED && j >= 2 ? s1 : s0, d[j][r], acc[i - 1][j][r]);
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) d[j] = dn[j];
-      s0 = sa * w0;
-      s1 = sa * w1;
-      af = an;
-      sa = sn;
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        acc[MI - 1][j][r] = fmaf(GATED && j >= 2 ? s1 : s0, d[j][r], acc[MI - 1][j][r]);
+  const int r0 = mh * RW + l16, rb = nh * (BN / WN) + l16;
+  const int u0 = ((2 * g) ^ a_swz(l16)) * 16, u1 = ((2 * g + 1) ^ a_swz(l16)) * 16;
+  auto frag_a = [&](int c, int i) {
+    return frag(st[c & 1].a + i * 2048, r0 * 128 + u0, r0 * 128 + u1);
+  };
+  auto frag_b = [&](int c, int j) {
+    return frag(st[c & 1].b + j * 2048, rb * 128 + u0, rb * 128 + u1);
   };
 
-  issue(0, st[0]);
-  float w0 = ws[sblk0], w1 = GATED ? ws[sblk1] : 0.f;
-  for (int c = 0; c < kb; ++c) {
-    TileStage<BM, BN>& S = st[c & 1];
-    MOE_DMA_SYNC(0);
-    const int cn = min(c + 1, kb - 1);
-    const float n0 = ws[sblk0 + cn], n1 = GATED ? ws[sblk1 + cn] : 0.f;
-    if (c + 1 < kb) {
-      issue(c + 1, st[(c + 1) & 1]);
-    } else if (K % kFp8Block) {  // zeros past K in the short last block
-      const int u0 = K % kFp8Block / 16, nu = 8 - u0;
-      for (int i = tid; i < (BM + BN) * nu; i += 64 * NW) {
-        const int r = i / nu, u = u0 + i - r * nu, lr = r < BM ? r : r - BM;
-        *reinterpret_cast<i32x4*>((r < BM ? S.a : S.b) + lr * 128 + ((u ^ a_swz(lr)) * 16)) =
-            i32x4{0, 0, 0, 0};
-      }
-      __syncthreads();
+  // Zeros past K in the short last block (every wave's copies have landed).
+  auto zero_tail = [&](TileStage<BM, BN>& S) {
+    const int u0 = K % kFp8Block / 16, nu = 8 - u0;
+    for (int i = tid; i < (BM + BN) * nu; i += 64 * NW) {
+      const int r = i / nu, u = u0 + i - r * nu, lr = r < BM ? r : r - BM;
+      *reinterpret_cast<i32x4*>((r < BM ? S.a : S.b) + lr * 128 + ((u ^ a_swz(lr)) * 16)) =
+          i32x4{0, 0, 0, 0};
     }
-    compute(S, w0, w1);
+    __syncthreads();
+  };
+
+  // Fragments live across blocks: the weights', the next row subtile's, and the NJ
+  // results not yet folded in with their scale.
+  fp8x32 bf[NJ], af;
+  float sa, s0 = 0.f, s1 = 0.f;
+  f32x4 d[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // The zeroing of a short last block comes once its copies have landed, before it is read.
+  auto whole = [&](int c) {
+    if (c + 1 == kb && K % kFp8Block) zero_tail(st[c & 1]);
+  };
+  issue_s(0);
+  issue_b(0);
+  issue_a(0, 0);
+  issue_a(0, 1);
+  float w0 = wsw[0], w1 = GATED ? wsc[1][0] : 0.f;
+  if (kb > 1) {
+    if (!quad) issue_s(1);
+    issue_b(1);
+    issue_a(1, 0);
+    issue_a(1, 1);
+    MOE_DMA_SYNC(CPA + CPB);
+  } else {
+    MOE_DMA_SYNC(0);
+  }
+  whole(0);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) bf[j] = frag_b(0, j);
+  af = frag_a(0, 0);
+  sa = scale_of(0, r0);
+  for (int c = 0; c < kb; ++c) {
+    const int cn = min(c + 1, kb - 1);
+    const float n0 = wsw[cn], n1 = GATED ? wsc[1][cn] : 0.f;
+    const bool more = c + 1 < kb;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const fp8x32 a = af;
+      const float f0 = sa * w0, f1 = GATED ? sa * w1 : 0.f;
+      // every wave has read what the next copies overwrite (the waits on this wave's own LDS
+      // reads come before its barrier)
+      if (i == 1 && c + 2 < kb) {
+        MOE_LDS_SYNC();
+        if (quad && (c & 3) == 1 && s_first(c >> 2) + 4 < kb) issue_s((c >> 2) + 1);
+        issue_b(c + 2);
+      }
+      if (i == MI / 2 && c + 2 < kb) {
+        if (MI > 2) MOE_LDS_SYNC();
+        issue_a(c + 2, 0);
+      }
+      if (i + 1 < MI) {
+        af = frag_a(c, i + 1);
+        sa = scale_of(c, r0 + (i + 1) * 16);
+      } else if (more) {
+        // the next block has landed (the one behind it may still be on its way)
+        if (c + 2 < kb) {
+          MOE_DMA_SYNC(CPB + CPA / 2);
+          if (!quad) issue_s(c + 2);
+          issue_a(c + 2, 1);
+        } else {
+          MOE_DMA_SYNC(0);
+        }
+        whole(c + 1);
+        af = frag_a(c + 1, 0);
+        sa = scale_of(c + 1, r0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        f32x4& o = acc[i == 0 ? MI - 1 : i - 1][j];
+        const float f = GATED && j >= NJ / 2 ? s1 : s0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = fmaf(f, d[j][r], o[r]);
+        pin(o);
+        d[j] = mfma_e4m3(bf[j], a, f32x4{0.f, 0.f, 0.f, 0.f});
+        pin(d[j]);
+        if (i + 1 == MI && more) bf[j] = frag_b(c + 1, j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      s0 = f0;
+      s1 = f1;
+    }
     w0 = n0;
     w1 = n1;
   }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[MI - 1][j][r] = fmaf(GATED && j >= NJ / 2 ? s1 : s0, d[j][r], acc[MI - 1][j][r]);
 
   // acc[i][j][r]: row mh*(BM/WM) + 16i + l16, weight row nh*64 + 16j + 4g + r of the tile
   const int rl = mh * (BM / WM) + l16;
