@@ -51,6 +51,23 @@ __device__ __forceinline__ int fp8_pack4(float a, float b, float c, float d, con
   return s.finite ? w : 0x7f7f7f7f;
 }
 
+// Two fp32 values -> packed bf16, nearest-even (NaN quiet): one instruction.
+__device__ __forceinline__ uint32_t bf16_pack2(float a, float b) {
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// SiLU(g) * u = g * u / (1 + e^-g).  e^-g = 2^t with t = -g log2(e) in two parts (the second,
+// under 2^-24 of the first, enters as 2^lo = 1 + lo ln 2), so its relative error stays at a
+// few 2^-24 for every g; the hardware's 2^x and 1/x are good to one ulp.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  const float t = g * -1.44269504f;
+  const float lo = fmaf(g, -1.44269504f, -t) + g * -1.92596299e-8f;
+  const float z = __builtin_amdgcn_exp2f(t);
+  const float den = 1.0f + fmaf(z, lo * 0.69314718f, z);
+  return g * __builtin_amdgcn_rcpf(den) * u;
+}
+
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // The `tile`-th tile of BM rows, experts in ascending order, found by one

@@ -101,7 +101,19 @@ __device__ __forceinline__ const uint8_t* slot_base(const uint8_t* base, int64_t
   return base + (size_t)slot * stride;
 }
 
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// Four consecutive outputs of a row, of which the first `left` exist; 8-byte aligned where
+// `vec` (rows of a multiple of 4).
+__device__ __forceinline__ void store4(uint16_t* dst, const f32x4& v, int left, bool vec) {
+  const uint2 b = {bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3])};
+  if (vec) {
+    if (left > 0) *reinterpret_cast<uint2*>(dst) = b;
+  } else {
+    if (left > 0) dst[0] = (uint16_t)b.x;
+    if (left > 1) dst[1] = (uint16_t)(b.x >> 16);
+    if (left > 2) dst[2] = (uint16_t)b.y;
+    if (left > 3) dst[3] = (uint16_t)(b.y >> 16);
+  }
+}
 
 // Tiles of 16 rows x 64 weight rows; the 4 waves split K (blocks w, w+4, ...)
 // and their sums meet in LDS in wave order.
@@ -209,18 +221,7 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
     const f32x4 v = total(wave);
     const int col = n0 + wave * 16 + 4 * g;
     if (have) {
-      uint16_t* dst = p.y + (size_t)(t.row0 + i16) * p.N + col;
-      if (p.N % 4 == 0) {
-        if (col < p.N) {
-          const uint32_t b0 = f32_to_bf16_rne(v[0]), b1 = f32_to_bf16_rne(v[1]);
-          const uint32_t b2 = f32_to_bf16_rne(v[2]), b3 = f32_to_bf16_rne(v[3]);
-          *reinterpret_cast<uint2*>(dst) = uint2{b0 | (b1 << 16), b2 | (b3 << 16)};
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (col + r < p.N) dst[r] = f32_to_bf16_rne(v[r]);
-      }
+      store4(p.y + (size_t)(t.row0 + i16) * p.N + col, v, p.N - col, p.N % 4 == 0);
     }
   }
 }
@@ -567,18 +568,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
       uint16_t* dst = p.y + (size_t)(row0 + rl + i * 16) * p.N + col0;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const uint32_t b0 = f32_to_bf16_rne(acc[i][j][0]), b1 = f32_to_bf16_rne(acc[i][j][1]);
-        const uint32_t b2 = f32_to_bf16_rne(acc[i][j][2]), b3 = f32_to_bf16_rne(acc[i][j][3]);
-        const int col = col0 + j * 16;
-        if (p.N % 4 == 0) {
-          if (col < p.N)
-            *reinterpret_cast<uint2*>(dst + j * 16) = uint2{b0 | (b1 << 16), b2 | (b3 << 16)};
-        } else {
-          if (col < p.N) dst[j * 16] = (uint16_t)b0;
-          if (col + 1 < p.N) dst[j * 16 + 1] = (uint16_t)b1;
-          if (col + 2 < p.N) dst[j * 16 + 2] = (uint16_t)b2;
-          if (col + 3 < p.N) dst[j * 16 + 3] = (uint16_t)b3;
-        }
+        store4(dst + j * 16, acc[i][j], p.N - col0 - j * 16, p.N % 4 == 0);
       }
     }
   }
