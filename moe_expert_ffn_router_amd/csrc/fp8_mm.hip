@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   constexpr int NW = WM * WN, MI = BM / WM / 16, NJ = BN / WN / 16;
   constexpr int COLS = GATED ? BN / 2 : BN;    // output columns
   constexpr int CPA = BM / 8 / NW, CPB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
-  static_assert(NJ == 4 && BM % 64 == 0 && BM / 64 <= NW, "wave shape");
+  static_assert(NJ == 4 && BM % 64 == 0 && BM / 64 <= NW && MI > 2 && CPA / 2 <= NJ, "wave shape");
   static_assert(!GATED || COLS == kFp8Block, "gate/up: one scale block of h per tile");
   __shared__ TileStage<BM, BN> st[2];
   __shared__ __attribute__((aligned(16))) float sc[2][BM * 4];  // [row][4 blocks]
@@ -357,20 +357,21 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
     return u < (uint32_t)(K % kFp8Block) ? 0u : u;
   };
   auto is_short = [&](int c) { return c + 1 == kb && K % kFp8Block != 0; };
-  auto issue_a = [&](int c, int half) {
+  // copies [q0, q1) of block c
+  auto issue_a = [&](int c, int q0, int q1) {
     uint8_t* dst = st[c & 1].a;
     const uint8_t* src = ab + (size_t)c * kFp8Block;
     const bool cut = is_short(c);
 #pragma unroll
-    for (int q = half * (CPA / 2); q < (half + 1) * (CPA / 2); ++q)
+    for (int q = q0; q < q1; ++q)
       dma16(src, cut ? ao[q] - back(a_row(q) + (lane >> 3)) : ao[q], dst + a_row(q) * 128);
   };
-  auto issue_b = [&](int c) {
+  auto issue_b = [&](int c, int q0, int q1) {
     uint8_t* dst = st[c & 1].b + wave * CPB * 1024;
     const uint8_t* src = wb + (size_t)c * kFp8Block;
     const bool cut = is_short(c);
 #pragma unroll
-    for (int q = 0; q < CPB; ++q)
+    for (int q = q0; q < q1; ++q)
       dma16(src, cut ? wo[q] - back((wave * CPB + q) * 8 + (lane >> 3)) : wo[q], dst + q * 1024);
   };
   // the rows' scales of blocks [s_first(f), s_first(f) + 4) as group f; fewer than four blocks
@@ -443,15 +444,13 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
     if (c + 1 == kb && K % kFp8Block) zero_tail(st[c & 1]);
   };
   issue_s(0);
-  issue_b(0);
-  issue_a(0, 0);
-  issue_a(0, 1);
+  issue_b(0, 0, CPB);
+  issue_a(0, 0, CPA);
   float w0 = wsw[0], w1 = GATED ? wsc[1][0] : 0.f;
   if (kb > 1) {
     if (!quad) issue_s(1);
-    issue_b(1);
-    issue_a(1, 0);
-    issue_a(1, 1);
+    issue_b(1, 0, CPB);
+    issue_a(1, 0, CPA);
     MOE_DMA_SYNC(CPA + CPB);
   } else {
     MOE_DMA_SYNC(0);
@@ -474,12 +473,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
       if (i == 1 && c + 2 < kb) {
         MOE_LDS_SYNC();
         if (quad && (c & 3) == 1 && s_first(c >> 2) + 4 < kb) issue_s((c >> 2) + 1);
-        issue_b(c + 2);
       }
-      if (i == MI / 2 && c + 2 < kb) {
-        if (MI > 2) MOE_LDS_SYNC();
-        issue_a(c + 2, 0);
-      }
+      if (i == MI / 2 && c + 2 < kb) MOE_LDS_SYNC();
       if (i + 1 < MI) {
         af = frag_a(c, i + 1);
         sa = scale_of(c, r0 + (i + 1) * 16);
@@ -488,7 +483,6 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
         if (c + 2 < kb) {
           MOE_DMA_SYNC(CPB + CPA / 2);
           if (!quad) issue_s(c + 2);
-          issue_a(c + 2, 1);
         } else {
           MOE_DMA_SYNC(0);
         }
@@ -507,6 +501,12 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
         d[j] = mfma_e4m3(bf[j], a, f32x4{0.f, 0.f, 0.f, 0.f});
         pin(d[j]);
         if (i + 1 == MI && more) bf[j] = frag_b(c + 1, j);
+        // the freed pieces' copies, spread over the MFMAs
+        if (c + 2 < kb) {
+          if (i == 1) issue_b(c + 2, j * CPB / NJ, (j + 1) * CPB / NJ);
+          if (i == MI / 2 && j < CPA / 2) issue_a(c + 2, j, j + 1);
+          if (i + 1 == MI && j < CPA / 2) issue_a(c + 2, CPA / 2 + j, CPA / 2 + j + 1);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       s0 = f0;
