@@ -10,10 +10,11 @@
 // s) has the slot c + s of the partial arrays: going down the batch every
 // piece raises c or s, so slots are unique and fewer than chunks + S.  Each
 // lane sums the probabilities of its experts over its rows (fp32, at most
-// R / 4 terms), the groups are added in LDS, and the ids are counted with
-// integer LDS atomics (their order does not matter).  A second kernel, one
-// workgroup per sequence, adds a sequence's pieces in double in chunk order
-// and forms the loss.  A batch of one chunk is finished by the first kernel.
+// R / 4 terms), the waves are added in LDS, and the ids are counted with
+// integer LDS atomics (their order does not matter).  A second kernel
+// adds a sequence's pieces in double in chunk order, a workgroup per sequence and
+// 16 experts, and a third forms the loss.  A batch of one chunk is finished by the
+// first kernel.
 #include "fp8_common.h"
 
 namespace moe {
@@ -28,6 +29,7 @@ struct BalArgs {
   float* part_p;  // [slots][E]
   int* part_c;    // [slots][E]
   int* part_n;    // [slots]
+  double* part_d; // [S][slices of kSlice experts]
   int* n_tokens;
   int* counts;
   float* probs;
@@ -59,16 +61,22 @@ __device__ __forceinline__ void seq_rows(const int* seq, int s, int T, int& lo, 
   hi = hi < lo ? lo : hi > T ? T : hi;
 }
 
-// The first sequence that ends behind row t (S if none does).
-__device__ __forceinline__ int first_seq(const int* seq, int S, int t) {
+// The first sequence that ends behind row t (S if none does), found by a whole wave: each
+// step reads 64 evenly spaced offsets and keeps the interval between two of them (S <= 64:
+// one step, so one memory latency).
+__device__ __forceinline__ int first_seq(const int* seq, int S, int t, int lane) {
   if (!seq) return 0;
-  int a = 0, b = S;
-  while (a < b) {
-    const int m = (a + b) >> 1;
-    if (seq[m + 1] > t) b = m;
-    else a = m + 1;
+  int lo = 0, n = S;  // the answer lies in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 63) >> 6;
+    const int i = lane * step;
+    const bool past = i < n && seq[lo + min(i + step, n)] <= t;  // the lane's last sequence ends by t
+    const int k = __popcll(__ballot(past));
+    const int d = min(k * step, n);
+    lo += d;
+    n = step == 1 ? 0 : min(step, n - d);
   }
-  return a;
+  return lo;
 }
 
 // Maximum and sum over the LPR lanes of a group, in every lane of it.
@@ -130,6 +138,17 @@ __device__ __forceinline__ void load_row(const V* __restrict__ row, int E, int s
   }
 }
 
+// e^d for d <= 0: 2^t with t = d log2(e), what t's rounding and the constant's lost (lo, under
+// 2^-23 |t|) entered as 2^lo = 1 + lo ln 2: relative error (|d| + 3) 2^-24 with the rounding of
+// d itself.  -inf gives 0 (lo is NaN there and clamped), NaN stays.
+__device__ __forceinline__ float exp_neg(float d) {
+  const float t = d * 1.44269504f;
+  const float lo =
+      __builtin_amdgcn_fmed3f(fmaf(d, 1.92596299e-8f, fmaf(d, 1.44269504f, -t)), -1.0f, 1.0f);
+  const float z = __builtin_amdgcn_exp2f(t);
+  return fmaf(z, lo * 0.69314718f, z);
+}
+
 // Logits of a row -> its softmax, over the group's lanes.  Experts past E and
 // -inf logits get 0; a row of nothing but -inf gets zeros.
 template <int LPR, int VPL>
@@ -142,7 +161,7 @@ __device__ __forceinline__ void row_softmax(float (&x)[VPL]) {
   float z = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    x[i] = expf(x[i] - m);
+    x[i] = exp_neg(x[i] - m);
     z += x[i];
   }
   z = group_sum<LPR>(z);
@@ -153,48 +172,104 @@ __device__ __forceinline__ void row_softmax(float (&x)[VPL]) {
 
 constexpr int kMaxChunk = 128;  // rows of a chunk at most
 
-// The rows [lo, hi) of a sequence inside one chunk: probability sums into
-// acc[0..E), counts into hist[0..E), counting rows into *nv (all LDS).
-template <int NW, int LPR, int VPL, bool VEC>
-__device__ __forceinline__ void balance_piece(const BalArgs& a, int lo, int hi, float* acc,
-                                              int* hist, int* nv) {
+// U rows of a group, NG rows apart from row t on: loads in flight together, with the rows'
+// mask bytes beside them (a masked row is read and dropped: waiting for its mask first
+// would double the latency).
+template <int NG, int U, int LPR, int VPL, bool VEC>
+struct Rows {
+  float x[U][VPL];
+  bool live[U];
+  __device__ __forceinline__ void load(const BalArgs& a, int t, int hi, int sub) {
+    uint8_t m[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      live[u] = t + u * NG < hi;
+      m[u] = a.mask && live[u] ? a.mask[t + u * NG] : 1;
+      load_row<LPR, VPL, VEC>(a.logits + (size_t)(t + u * NG) * a.E, a.E, sub, live[u], -INFINITY,
+                              x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) live[u] = live[u] && m[u];
+  }
+};
+
+// A thread's first assignments of the chunk (i = tid, tid + NT of its rows * k): row and id,
+// -1 where the row is masked; and the mask of row tid.
+template <int NT>
+struct Ids {
+  static constexpr int P = 2;
+  int row[P], id[P];
+  bool on;
+  __device__ __forceinline__ void load(const BalArgs& a, int t0, int t1, int tid) {
+    const int n = (t1 - t0) * a.k;
+    uint8_t m[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const int i = tid + q * NT;
+      row[q] = i < n ? t0 + i / a.k : -1;
+      id[q] = i < n ? a.ids[(size_t)t0 * a.k + i] : -1;
+      m[q] = i < n && a.mask ? a.mask[row[q]] : 1;
+    }
+    on = t0 + tid < t1 && (!a.mask || a.mask[t0 + tid]);
+#pragma unroll
+    for (int q = 0; q < P; ++q) id[q] = m[q] ? id[q] : -1;
+  }
+};
+
+// The rows [lo, hi) of a sequence inside the chunk [t0, t1): probability sums of the wave into
+// its row of acc, counts into hist, counting rows into *nv (all LDS; finished by a barrier).
+// `first` and `ids` hold what was loaded ahead: the chunk's first rows (this piece's if it
+// starts the chunk) and its first assignments.
+template <int NW, int U, int LPR, int VPL, bool VEC, typename R>
+__device__ __forceinline__ void balance_piece(const BalArgs& a, int t0, int t1, int lo, int hi,
+                                              const R& first, const Ids<64 * NW>& ids,
+                                              float (*acc)[kMaxE], int* hist, int* nv) {
   constexpr int NT = 64 * NW, GPW = 64 / LPR, NG = NW * GPW;
-  constexpr int U = VPL >= 16 ? 2 : VPL == 8 ? 2 : 4;  // rows in flight per group
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int sub = lane % LPR, grp = wave * GPW + lane / LPR;
+  const bool ahead = lo == t0;
   for (int i = tid; i < a.E; i += NT) hist[i] = 0;
   if (tid == 0) *nv = 0;
   __syncthreads();
+  // counts, and the number of counting rows (a chunk has at most kMaxChunk <= NT rows)
+#pragma unroll
+  for (int q = 0; q < Ids<NT>::P; ++q)
+    if ((unsigned)ids.id[q] < (unsigned)a.E && ids.row[q] >= lo && ids.row[q] < hi)
+      atomicAdd(&hist[ids.id[q]], 1);
+  for (int i = tid + Ids<NT>::P * NT; i < (t1 - t0) * a.k; i += NT) {
+    const int t = t0 + i / a.k;
+    const int id = a.ids[(size_t)t0 * a.k + i];
+    if ((unsigned)id < (unsigned)a.E && t >= lo && t < hi && (!a.mask || a.mask[t]))
+      atomicAdd(&hist[id], 1);
+  }
+  const uint64_t counting = __ballot(ids.on && t0 + tid >= lo && t0 + tid < hi);
+  if (lane == 0 && counting) atomicAdd(nv, (int)__popcll(counting));
   float sum[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) sum[i] = 0.0f;
-  for (int t0 = lo + grp; t0 - grp < hi; t0 += NG * U) {
-    float x[U][VPL];
-    bool live[U];
+  auto take = [&](const R& r, int t) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = t0 + u * NG;
-      live[u] = t < hi && (!a.mask || a.mask[t]);
-      load_row<LPR, VPL, VEC>(a.logits + (size_t)t * a.E, a.E, sub, live[u], -INFINITY, x[u]);
-    }
+      const bool in = t + u * NG < hi && r.live[u];
+      float p[VPL];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      row_softmax<LPR, VPL>(x[u]);
+      for (int i = 0; i < VPL; ++i) p[i] = in ? r.x[u][i] : -INFINITY;
+      row_softmax<LPR, VPL>(p);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum[i] += x[u][i];
+      for (int i = 0; i < VPL; ++i) sum[i] += p[i];
     }
+  };
+  int t = lo + grp;
+  if (ahead) {
+    take(first, t);
+    t += NG * U;
   }
-  // counts, and the number of counting rows
-  const int rows = hi - lo;
-  const int* ids = a.ids + (size_t)lo * a.k;
-  for (int i = tid; i < rows * a.k; i += NT) {
-    const int t = lo + i / a.k;
-    const int id = ids[i];
-    if ((unsigned)id < (unsigned)a.E && (!a.mask || a.mask[t])) atomicAdd(&hist[id], 1);
+  for (; t - grp < hi; t += NG * U) {
+    R r;
+    r.load(a, t, hi, sub);
+    take(r, t);
   }
-  for (int i = tid; i < rows; i += NT)
-    if (!a.mask || a.mask[lo + i]) atomicAdd(nv, 1);
-  // the groups of a wave, then the waves in order
+  // the groups of a wave
   if constexpr (LPR == 16) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -202,134 +277,195 @@ __device__ __forceinline__ void balance_piece(const BalArgs& a, int lo, int hi, 
       sum[i] += __shfl_xor(sum[i], 32, 64);
     }
   }
-  for (int w = 0; w < NW; ++w) {
-    if (wave == w && lane < LPR) {
+  if (lane < LPR) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = expert_of<LPR, VEC>(sub, i);
-        if (e < a.E) acc[e] = w == 0 ? sum[i] : acc[e] + sum[i];
-      }
+    for (int i = 0; i < VPL; ++i) {
+      const int e = expert_of<LPR, VEC>(sub, i);
+      if (e < a.E) acc[wave][e] = sum[i];
     }
-    __syncthreads();
   }
+  __syncthreads();
 }
 
-// loss of one sequence from its counts and sums (device layout), by one wave.
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
 
+// loss of one sequence from its counts and sums.
 __device__ __forceinline__ float loss_of(double dot, int E, int k, int n) {
   return n > 0 ? (float)(dot * (double)E / ((double)k * (double)n * (double)n)) : 0.0f;
 }
 
 template <int NW, int LPR, int VPL, bool VEC, bool FINAL>
 __global__ __launch_bounds__(64 * NW) void balance_partial_kernel(BalArgs a) {
-  __shared__ float acc[kMaxE];
+  __shared__ float acc[NW][kMaxE];
   __shared__ int hist[kMaxE];
+  __shared__ double wdot[NW];
   __shared__ int nv;
-  constexpr int NT = 64 * NW;
-  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int NT = 64 * NW, NG = NW * 64 / LPR;
+  constexpr int U = VPL == 4 ? 4 : VPL == 16 && NW == 16 ? 1 : 2;  // rows in flight per group
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = (int)blockIdx.x;
   const int t0 = c * a.R, t1 = FINAL ? a.T : min(a.T, t0 + a.R);
-  for (int s = FINAL ? 0 : first_seq(a.seq, a.S, t0); s < a.S; ++s) {
+  Rows<NG, U, LPR, VPL, VEC> first;
+  first.load(a, t0 + wave * (64 / LPR) + lane / LPR, t1, lane % LPR);
+  Ids<NT> ids;
+  ids.load(a, t0, t1, tid);
+  for (int s = FINAL ? 0 : first_seq(a.seq, a.S, t0, lane); s < a.S; ++s) {
     int lo, hi;
     seq_rows(a.seq, s, a.T, lo, hi);
     if (!FINAL && lo >= t1) break;
     lo = max(lo, t0);
     hi = min(hi, t1);
     if (FINAL || hi > lo) {
-      balance_piece<NW, LPR, VPL, VEC>(a, lo, hi, acc, hist, &nv);
+      balance_piece<NW, U, LPR, VPL, VEC>(a, t0, t1, lo, hi, first, ids, acc, hist, &nv);
       const int n = nv;
       const size_t o = FINAL ? (size_t)s * a.E : (size_t)(c + s) * a.E;
       float* po = FINAL ? a.probs : a.part_p;
       int* co = FINAL ? a.counts : a.part_c;
-      for (int i = tid; i < a.E; i += NT) {
-        po[o + i] = acc[i];
-        co[o + i] = hist[i];
+      double dot = 0.0;
+      for (int i = tid; i < a.E; i += NT) {  // the waves in order
+        float p = acc[0][i];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) p += acc[w][i];
+        const int h = hist[i];
+        po[o + i] = p;
+        co[o + i] = h;
+        if constexpr (FINAL) dot += (double)p * (double)h;
       }
       if (tid == 0) (FINAL ? a.n_tokens[s] : a.part_n[c + s]) = n;
       if constexpr (FINAL) {
-        if (tid < 64) {
-          double dot = 0.0;
-          for (int i = lane; i < a.E; i += 64) dot += (double)acc[i] * (double)hist[i];
-          dot = wave_sum_f64(dot);
-          if (lane == 0) a.loss[s] = loss_of(dot, a.E, a.k, n);
+        dot = wave_sum_f64(dot);
+        if (lane == 0) wdot[wave] = dot;
+        __syncthreads();
+        if (tid == 0) {
+          double d = 0.0;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) d += wdot[w];
+          a.loss[s] = loss_of(d, a.E, a.k, n);
         }
       }
-      __syncthreads();  // acc, hist and nv are reused by the next piece
+      __syncthreads();  // acc, hist, wdot and nv are reused by the next piece
     }
   }
 }
 
-// One workgroup per sequence: its pieces' sums in chunk order (thread =
-// (expert, one of W interleaved chunk lanes), the lanes then added in order).
-constexpr int kFinNT = 1024;
-__global__ __launch_bounds__(kFinNT) void balance_final_kernel(BalArgs a) {
-  __shared__ double sp[kFinNT];
-  __shared__ int sc[kFinNT];
-  __shared__ double wdot[kFinNT / 64];
-  __shared__ int sn;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int s = (int)blockIdx.x;
+// The pieces of a sequence in chunk order, one workgroup per sequence and kSlice experts: thread
+// = (expert, one of kRedLanes interleaved chunk lanes), U chunks in flight, the lanes then
+// added in a fixed order.  Each slice leaves its share of the loss's sum.
+constexpr int kSlice = 16, kRedLanes = 64;
+__global__ __launch_bounds__(kSlice * kRedLanes) void balance_reduce_kernel(BalArgs a) {
+  constexpr int NT = kSlice * kRedLanes, NW = NT / 64, U = 8;
+  __shared__ double sp[NW][kSlice];
+  __shared__ int sc[NW][kSlice], sn[NW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nsl = (a.E + kSlice - 1) / kSlice;
+  const int s = (int)blockIdx.x / nsl, sl = (int)blockIdx.x - s * nsl;
   int lo, hi;
   seq_rows(a.seq, s, a.T, lo, hi);
   const int c0 = lo / a.R, c1 = hi > lo ? (hi - 1) / a.R + 1 : c0;
-  const int W = kFinNT / a.E;  // E <= 1024
-  const int e = tid % a.E, cl = tid / a.E;
+  const int e = sl * kSlice + tid % kSlice, cl = tid / kSlice;
   double p = 0.0;
   int c = 0;
-  if (cl < W)
-    for (int i = c0 + cl; i < c1; i += W) {
-      const size_t o = (size_t)(i + s) * a.E + e;
-      p += (double)a.part_p[o];
-      c += a.part_c[o];
-    }
-  sp[tid] = p;
-  sc[tid] = c;
-  if (tid == 0) sn = 0;
-  __syncthreads();
-  int n = 0;
-  for (int i = c0 + tid; i < c1; i += kFinNT) n += a.part_n[i + s];
-  if (n) atomicAdd(&sn, n);
-  double dot = 0.0;
-  if (tid < a.E) {
-    for (int w = 1; w < W; ++w) {
-      p += sp[w * a.E + tid];
-      c += sc[w * a.E + tid];
-    }
-    const float pf = (float)p;
-    a.probs[(size_t)s * a.E + tid] = pf;
-    a.counts[(size_t)s * a.E + tid] = c;
-    dot = p * (double)c;
-  }
-  dot = wave_sum_f64(dot);
-  if (lane == 0) wdot[tid >> 6] = dot;
-  __syncthreads();
-  if (tid == 0) {
-    double d = 0.0;
+  for (int i = c0 + cl; i < c1; i += kRedLanes * U) {
+    float pv[U];
+    int cv[U];
 #pragma unroll
-    for (int w = 0; w < kFinNT / 64; ++w) d += wdot[w];
-    a.n_tokens[s] = sn;
-    a.loss[s] = loss_of(d, a.E, a.k, sn);
+    for (int u = 0; u < U; ++u) {
+      const bool ok = i + u * kRedLanes < c1 && e < a.E;
+      const size_t o = (size_t)(i + u * kRedLanes + s) * a.E + e;
+      pv[u] = ok ? a.part_p[o] : 0.0f;
+      cv[u] = ok ? a.part_c[o] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      p += (double)pv[u];
+      c += cv[u];
+    }
+  }
+  int n = 0;
+  if (sl == 0)
+    for (int i = c0 + tid; i < c1; i += NT) n += a.part_n[i + s];
+#pragma unroll
+  for (int o = 16; o < 64; o *= 2) {  // the wave's four chunk lanes
+    p += __shfl_xor(p, o, 64);
+    c += __shfl_xor(c, o, 64);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o, 64);
+  if (lane < kSlice) {
+    sp[wave][lane] = p;
+    sc[wave][lane] = c;
+  }
+  if (lane == 0) sn[wave] = n;
+  __syncthreads();
+  if (wave == 0) {
+    double dot = 0.0;
+    if (lane < kSlice && e < a.E) {
+#pragma unroll
+      for (int w = 1; w < NW; ++w) {
+        p += sp[w][lane];
+        c += sc[w][lane];
+      }
+      a.probs[(size_t)s * a.E + e] = (float)p;
+      a.counts[(size_t)s * a.E + e] = c;
+      dot = p * (double)c;
+    }
+    dot = wave_sum_f64(dot);
+    if (lane == 0) {
+      a.part_d[(size_t)s * nsl + sl] = dot;
+      if (sl == 0) {
+#pragma unroll
+        for (int w = 1; w < NW; ++w) n += sn[w];
+        a.n_tokens[s] = n;
+      }
+    }
   }
 }
 
-// Gradient: a group of LPR lanes per row, R rows per workgroup of 4 waves.
+// One wave per sequence: the slices' shares (at most 64) -> the loss.
+__global__ __launch_bounds__(256) void balance_loss_kernel(BalArgs a) {
+  const int lane = threadIdx.x & 63, s = (int)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (s >= a.S) return;
+  const int nsl = (a.E + kSlice - 1) / kSlice;
+  const double d = wave_sum_f64(lane < nsl ? a.part_d[(size_t)s * nsl + lane] : 0.0);
+  if (lane == 0) a.loss[s] = loss_of(d, a.E, a.k, a.n_tokens[s]);
+}
+
+// Gradient: a group of LPR lanes per row, kBwdRows rows per workgroup of 4 waves (65536 x 512:
+// 50.8 us with 16, 53.1 with 32, 59.3 with 64 rows).
+constexpr int kBwdRows = 16;
 template <int LPR, int VPL, bool VEC>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
   constexpr int GPW = 64 / LPR, NG = 4 * GPW;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int sub = lane % LPR, grp = wave * GPW + lane / LPR;
+  __shared__ __attribute__((aligned(16))) float extra[NG][LPR * VPL];
+  for (int i = tid; i < NG * LPR * VPL; i += 256) (&extra[0][0])[i] = 0.0f;
+  __syncthreads();
   const int t0 = (int)blockIdx.x * a.R, t1 = min(a.T, t0 + a.R);
   int s = -1, lo = 0, hi = 0;
   float ac[VPL];  // a_s c_se of the current sequence
 #pragma unroll
   for (int i = 0; i < VPL; ++i) ac[i] = 0.0f;
-  int s_next = first_seq(a.seq, a.S, t0);
+  // what a row needs is read whether or not it turns out to count (lane j < k of the group holds
+  // assignment j)
+  int s_next = first_seq(a.seq, a.S, t0, lane);
   for (int t = t0 + grp; t - grp < t1; t += NG) {
+    const bool in = t < t1;
+    const uint8_t m = a.mask && in ? a.mask[t] : 1;
+    float p[VPL];
+    load_row<LPR, VPL, VEC>(a.logits + (size_t)t * a.E, a.E, sub, in, -INFINITY, p);
+    int id = -1;
+    float w = 0.0f, wd = 0.0f;
+    if (a.dw && in && sub < a.k) {
+      const size_t o = (size_t)t * a.k + sub;
+      id = a.ids[o];
+      w = a.w[o];
+      wd = a.dw[o];
+    }
     // the row's sequence (per group; every lane of the group agrees)
     while (s_next < a.S && t >= hi) {
       s = s_next++;
@@ -343,20 +479,13 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
         for (int i = 0; i < VPL; ++i) ac[i] = as * (float)c[i];
       }
     }
-    const bool inside = t < t1 && s >= 0 && t >= lo && t < hi;
-    const bool live = inside && (!a.mask || a.mask[t]);
-    float p[VPL];
-    load_row<LPR, VPL, VEC>(a.logits + (size_t)t * a.E, a.E, sub, live, -INFINITY, p);
-    // routing weights: lane j < k of the group holds assignment j
-    int id = -1;
-    float w = 0.0f, wd = 0.0f;
-    if (a.dw && live && sub < a.k) {
-      const size_t o = (size_t)t * a.k + sub;
-      id = a.ids[o];
-      if ((unsigned)id >= (unsigned)a.E) id = -1;
-      w = id < 0 ? 0.0f : a.w[o];
-      wd = id < 0 ? 0.0f : w * a.dw[o];
-    }
+    const bool inside = in && s >= 0 && t >= lo && t < hi;
+    const bool live = inside && m;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = live ? p[i] : -INFINITY;
+    if (!live || (unsigned)id >= (unsigned)a.E) id = -1;
+    w = id < 0 ? 0.0f : w;
+    wd = id < 0 ? 0.0f : w * wd;
     const float D = group_sum<LPR>(wd);
     const float add = a.renorm ? wd - w * D : wd;
     row_softmax<LPR, VPL>(p);
@@ -367,6 +496,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) p[i] *= ac[i] - dot;
     if (a.dw) {
+      // the weights' share, through a row of LDS that is zero between rows: the first lane of
+      // every id adds up that id's terms in order
+      float mine = 0.0f;
+      bool lead = id >= 0;
       for (int j = 0; j < a.k; ++j) {
         int idj;
         float v;
@@ -377,9 +510,18 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
           idj = __shfl(id, (lane & ~15) + j, 64);
           v = __shfl(add, (lane & ~15) + j, 64);
         }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) p[i] += expert_of<LPR, VEC>(sub, i) == idj ? v : 0.0f;
+        if (id == idj) {
+          mine += v;
+          lead = lead && j >= sub;
+        }
       }
+      if (lead) extra[grp][id] = mine;
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) p[i] += extra[grp][expert_of<LPR, VEC>(sub, i)];
+      __builtin_amdgcn_wave_barrier();
+      if (lead) extra[grp][id] = 0.0f;
+      __builtin_amdgcn_wave_barrier();
     }
     if (inside) {
       float* out = a.d_logits + (size_t)t * a.E;
@@ -433,7 +575,7 @@ int chunk_rows(int T) {
 }
 
 struct BalWs {
-  size_t p, c, n, total;
+  size_t p, c, n, d, total;
 };
 BalWs bal_ws(int T, int E, int S) {
   const size_t slots = (size_t)(T + chunk_rows(T) - 1) / chunk_rows(T) + (size_t)S;
@@ -442,7 +584,8 @@ BalWs bal_ws(int T, int E, int S) {
   w.p = 0;
   w.c = up(slots * E * 4);
   w.n = w.c + up(slots * E * 4);
-  w.total = w.n + up(slots * 4);
+  w.d = w.n + up(slots * 4);
+  w.total = w.d + up((size_t)S * ((E + kSlice - 1) / kSlice) * 8);
   return w;
 }
 
@@ -501,6 +644,7 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, in
   a.part_p = reinterpret_cast<float*>(w + L.p);
   a.part_c = reinterpret_cast<int*>(w + L.c);
   a.part_n = reinterpret_cast<int*>(w + L.n);
+  a.part_d = reinterpret_cast<double*>(w + L.d);
   a.n_tokens = n_tokens;
   a.counts = counts;
   a.probs = probs;
@@ -518,7 +662,9 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, in
     using Q = decltype(r);
     balance_partial_kernel<4, Q::lpr, Q::vpl, Q::vec, false><<<chunks, 256, 0, s>>>(a);
   });
-  balance_final_kernel<<<(unsigned)S, kFinNT, 0, s>>>(a);
+  const unsigned slices = (unsigned)((E + kSlice - 1) / kSlice);
+  balance_reduce_kernel<<<(unsigned)S * slices, kSlice * kRedLanes, 0, s>>>(a);
+  balance_loss_kernel<<<((unsigned)S + 3) / 4, 256, 0, s>>>(a);
   return check_launch(who);
 }
 
@@ -553,7 +699,7 @@ extern "C" int moe_route_backward(const float* logits, int32_t T, int32_t E, int
   a.d_loss = d_loss;
   a.d_logits = d_logits;
   a.T = T; a.E = E; a.k = k; a.S = S; a.renorm = renorm;
-  a.R = 32;
+  a.R = kBwdRows;
   const unsigned blocks = (unsigned)((T + a.R - 1) / a.R);
   with_row_shape(E, [&](auto r) {
     using Q = decltype(r);

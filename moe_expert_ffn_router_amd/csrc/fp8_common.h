@@ -70,46 +70,59 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// The `tile`-th tile of BM rows, experts in ascending order, found by one
-// whole wave: lane l owns the experts [l * per, l * per + per).
+// Row tiles of BM rows over the experts' segments, experts in ascending order, looked up by
+// one whole wave: lane l owns the experts [l * per, l * per + per) and loads their counts
+// and offsets together.
 struct RowTile {
   int e, row0, rows;
 };
 template <int BM>
-__device__ __forceinline__ bool row_tile(const int* __restrict__ counts,
-                                         const int* __restrict__ offsets, int E, int tile, int lane,
-                                         RowTile& t) {
-  const int per = (E + 63) >> 6;  // at most 16
-  const int first = lane * per;
-  int n[kMaxE / 64], mine = 0;
+struct RowTiles {
+  int n[kMaxE / 64], o[kMaxE / 64], first, mine, upto;
+
+  __device__ __forceinline__ int load(const int* __restrict__ counts,
+                                      const int* __restrict__ offsets, int E, int lane) {
+    const int per = (E + 63) >> 6;  // at most 16
+    first = lane * per;
 #pragma unroll
-  for (int i = 0; i < kMaxE / 64; ++i) {
-    const int c = i < per && first + i < E ? counts[first + i] : 0;
-    n[i] = c > 0 ? c : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < kMaxE / 64; ++i) mine += (n[i] + BM - 1) / BM;
-  const int upto = wave_incl_scan(mine);
-  const uint64_t owner = __ballot(tile >= upto - mine && tile < upto);
-  if (!owner) return false;
-  const int ol = (int)__builtin_ctzll(owner);
-  int left = tile - (upto - mine), e = first, rows = 0;
-#pragma unroll
-  for (int i = 0; i < kMaxE / 64; ++i) {
-    const int tiles = (n[i] + BM - 1) / BM;
-    if (rows == 0 && left >= 0 && left < tiles) {
-      e = first + i;
-      rows = n[i] - left * BM;
-      mine = left * BM;  // rows of the expert before this tile
+    for (int i = 0; i < kMaxE / 64; ++i) {
+      const bool ok = i < per && first + i < E;
+      n[i] = ok ? counts[first + i] : 0;
+      o[i] = ok ? offsets[first + i] : 0;
     }
-    left -= tiles;
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 64; ++i) {
+      n[i] = n[i] > 0 ? n[i] : 0;
+      mine += (n[i] + BM - 1) / BM;
+    }
+    upto = wave_incl_scan(mine);
+    return __builtin_amdgcn_readlane(upto, 63);  // tiles in all
   }
-  t.e = __builtin_amdgcn_readlane(e, ol);
-  const int r = __builtin_amdgcn_readlane(rows, ol);
-  t.row0 = offsets[t.e] + __builtin_amdgcn_readlane(mine, ol);
-  t.rows = r < BM ? r : BM;
-  return true;
-}
+
+  // tile < load()'s result
+  __device__ __forceinline__ RowTile at(int tile) const {
+    const uint64_t owner = __ballot(tile >= upto - mine && tile < upto);
+    const int ol = (int)__builtin_ctzll(owner);
+    int left = tile - (upto - mine), e = first, rows = 0, row0 = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 64; ++i) {
+      const int tiles = (n[i] + BM - 1) / BM;
+      if (rows == 0 && left >= 0 && left < tiles) {
+        e = first + i;
+        rows = n[i] - left * BM;
+        row0 = o[i] + left * BM;
+      }
+      left -= tiles;
+    }
+    RowTile t;
+    t.e = __builtin_amdgcn_readlane(e, ol);
+    const int r = __builtin_amdgcn_readlane(rows, ol);
+    t.row0 = __builtin_amdgcn_readlane(row0, ol);
+    t.rows = r < BM ? r : BM;
+    return t;
+  }
+};
 
 // Upper bound on the row tiles of A rows over E experts (host).
 inline int64_t row_tiles_bound(int64_t A, int64_t E, int64_t BM) {

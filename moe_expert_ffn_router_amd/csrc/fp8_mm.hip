@@ -127,7 +127,9 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   RowTile t;
   if (p.counts) {
-    if (!row_tile<16>(p.counts, p.offsets, p.E, tile, lane, t)) return;  // uniform per block
+    RowTiles<16> tiles;
+    if (tile >= tiles.load(p.counts, p.offsets, p.E, lane)) return;  // uniform per block
+    t = tiles.at(tile);
     dbg_segment(t.row0, t.rows, p.M);
   } else {
     t.e = 0;
@@ -250,25 +252,17 @@ struct TileStage {
 // m-tiles that consecutive workgroups of one XCD share weights over
 constexpr int kPanel = 4;
 
-// Workgroup -> (row tile, column block).  Hardware block b runs on XCD b % 8.
-// Dense: the tiles in panels of kPanel row tiles, column block by column block,
-// cut into eight contiguous ranges.  Grouped: the number of tiles is only bounded
-// on the host and the ones that hold rows come first, so whole panels go to the
-// XCDs in turn.
-__device__ __forceinline__ bool tile_of(const Fp8Args& p, int b, int& tile, int& nb) {
-  const int nnb = p.nnb;
-  if (p.counts) {
-    const int S = kPanel * nnb, x = b & 7, j = b >> 3;
-    const int sl = j / S, r = j - sl * S;
-    tile = (sl * 8 + x) * kPanel + r % kPanel;
-    nb = r / kPanel;
-    return true;
-  }
-  const int G = p.mt * nnb, per = (G + 7) >> 3;
+// Workgroup -> (row tile, column block) among mt x nnb tiles.  Hardware block b runs on
+// XCD b % 8: the tiles, in panels of kPanel row tiles that go column block by column
+// block, are cut into eight contiguous ranges of equal length.  (Grouped products know
+// mt on the device only: the grid is sized from a bound, and the workgroups behind the
+// ranges have nothing to do.)
+__device__ __forceinline__ bool tile_of(int b, int mt, int nnb, int& tile, int& nb) {
+  const int G = mt * nnb, per = (G + 7) >> 3;
   const int v = (b & 7) * per + (b >> 3);
   if ((b >> 3) >= per || v >= G) return false;
   const int panel = v / (kPanel * nnb), r = v - panel * (kPanel * nnb);
-  const int rows = min(kPanel, p.mt - panel * kPanel);
+  const int rows = min(kPanel, mt - panel * kPanel);
   nb = r / rows;
   tile = panel * kPanel + r - nb * rows;
   return true;
@@ -281,32 +275,32 @@ __device__ __forceinline__ bool tile_of(const Fp8Args& p, int b, int& tile, int&
     asm volatile("s_barrier" ::: "memory");                              \
   } while (0)
 
-template <int BM, int BN, int WM, int WN, bool GATED>
-__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
+// LDS of a tile: its stages, the rows' scales, the tile's two rows of weight scales, and
+// (gate/up) the rows' largest h per wave column.
+template <int BM, int BN, int WN, bool GATED>
+struct TileLds {
+  TileStage<BM, BN> st[2];
+  __attribute__((aligned(16))) float sc[2][BM * 4];  // [row][4 blocks]
+  float wsc[2][65536 / kFp8Block];
+  float row_max[GATED ? WN : 1][GATED ? BM : 1];
+};
+
+// A tile of at most BM rows in LDS laid out for LM >= BM.
+template <int BM, int BN, int WM, int WN, bool GATED, int LM>
+__device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const RowTile& t, int nb,
+                                              TileLds<LM, BN, WN, GATED>& lds) {
   constexpr int NW = WM * WN, MI = BM / WM / 16, NJ = BN / WN / 16;
   constexpr int COLS = GATED ? BN / 2 : BN;    // output columns
   constexpr int CPA = BM / 8 / NW, CPB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
   static_assert(NJ == 4 && BM % 64 == 0 && BM / 64 <= NW && MI > 2 && CPA / 2 <= NJ, "wave shape");
   static_assert(!GATED || COLS == kFp8Block, "gate/up: one scale block of h per tile");
-  __shared__ TileStage<BM, BN> st[2];
-  __shared__ __attribute__((aligned(16))) float sc[2][BM * 4];  // [row][4 blocks]
-  __shared__ float wsc[2][65536 / kFp8Block];  // the tile's two rows of weight scales
-  __shared__ float row_max[GATED ? WN : 1][GATED ? BM : 1];
+  auto& st = lds.st;
+  auto& sc = lds.sc;
+  auto& wsc = lds.wsc;
+  auto& row_max = lds.row_max;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int mh = wave / WN, nh = wave % WN;
-  int tile, nb;
-  if (!tile_of(p, (int)blockIdx.x, tile, nb)) return;
-  RowTile t;
-  if (p.counts) {
-    if (!row_tile<BM>(p.counts, p.offsets, p.E, tile, lane, t)) return;  // uniform per block
-    dbg_segment(t.row0, t.rows, p.M);
-    if (t.rows <= 0) return;
-  } else {
-    t.e = 0;
-    t.row0 = tile * BM;
-    t.rows = min(BM, p.M - t.row0);
-  }
   const int row0 = __builtin_amdgcn_readfirstlane(t.row0);
   const int rows = __builtin_amdgcn_readfirstlane(t.rows);
   const int e = __builtin_amdgcn_readfirstlane(t.e);
@@ -422,7 +416,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   };
 
   // Zeros past K in the short last block (every wave's copies have landed).
-  auto zero_tail = [&](TileStage<BM, BN>& S) {
+  auto zero_tail = [&](TileStage<LM, BN>& S) {
     const int u0 = K % kFp8Block / 16, nu = 8 - u0;
     for (int i = tid; i < (BM + BN) * nu; i += 64 * NW) {
       const int r = i / nu, u = u0 + i - r * nu, lr = r < BM ? r : r - BM;
@@ -574,18 +568,37 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   }
 }
 
+// Tiles of up to BM rows; one of at most half takes half the rows per wave (the last tile of an
+// expert's rows).
+template <int BM, int BN, int WM, int WN, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
+  __shared__ TileLds<BM, BN, WN, GATED> lds;
+  int tile, nb;
+  RowTile t;
+  if (p.counts) {
+    RowTiles<BM> tiles;
+    const int mt = tiles.load(p.counts, p.offsets, p.E, threadIdx.x & 63);
+    if (!tile_of((int)blockIdx.x, mt, p.nnb, tile, nb)) return;  // uniform per block
+    t = tiles.at(tile);
+    dbg_segment(t.row0, t.rows, p.M);
+    if (t.rows <= 0) return;
+  } else {
+    if (!tile_of((int)blockIdx.x, p.mt, p.nnb, tile, nb)) return;
+    t.e = 0;
+    t.row0 = tile * BM;
+    t.rows = min(BM, p.M - t.row0);
+  }
+  if (t.rows <= BM / 2) fp8_tile_body<BM / 2, BN, WM, WN, GATED, BM>(p, t, nb, lds);
+  else fp8_tile_body<BM, BN, WM, WN, GATED, BM>(p, t, nb, lds);
+}
+
 template <int BM, int BN, int WM, int WN, bool GATED>
 int launch_tiles(Fp8Args p, hipStream_t s, const char* who) {
   constexpr int COLS = GATED ? BN / 2 : BN;
   p.nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
-  int64_t blocks;
-  if (p.counts) {
-    const int64_t bound = row_tiles_bound(p.M, p.E, BM);
-    blocks = (bound + 8 * kPanel - 1) / (8 * kPanel) * (8 * kPanel) * p.nnb;
-  } else {
-    p.mt = (p.M + BM - 1) / BM;
-    blocks = ((int64_t)p.mt * p.nnb + 7) / 8 * 8;
-  }
+  const int64_t mt = p.counts ? row_tiles_bound(p.M, p.E, BM) : ((int64_t)p.M + BM - 1) / BM;
+  const int64_t blocks = (mt * p.nnb + 7) / 8 * 8;
+  p.mt = (int)mt;
   if (blocks > ((int64_t)1 << 31) - 1)
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   fp8_tile_kernel<BM, BN, WM, WN, GATED><<<(unsigned)blocks, 64 * WM * WN, 0, s>>>(p);
