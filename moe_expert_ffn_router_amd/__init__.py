@@ -150,8 +150,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr() if t.numel() else None
 
 
+# The current stream's handle without building a Stream object (2.9 us a call, measured; this
+# is 0.1 us); torch builds without the function go the long way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, int):
         return stream
