@@ -18,7 +18,8 @@ constexpr int kFp8Block = 128;  // columns (and weight rows) of one scale
 // any split of the 128 codes over the groups works that is the same for both.
 // C: lane (g, i) element r is C[4g + r][i].
 __device__ __forceinline__ f32x4 mfma_e4m3(fp8x32 a, fp8x32 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+  // scale operands that are the constant 0 select the instruction without scales
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
 // Keeps a value at this point of the program: without it the compiler moves an MFMA
@@ -57,15 +58,13 @@ __device__ __forceinline__ uint32_t bf16_pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// SiLU(g) * u = g * u / (1 + e^-g).  e^-g = 2^t with t = -g log2(e) in two parts (the second,
-// under 2^-24 of the first, enters as 2^lo = 1 + lo ln 2), so its relative error stays at a
-// few 2^-24 for every g; the hardware's 2^x and 1/x are good to one ulp.
+// SiLU(g) * u = g * u / (1 + e^-g), with e^-g = 2^(-g log2(e)) on the hardware's 2^x and 1/x
+// (one ulp each).  The exponent's rounding makes e^-g off by |g| 2^-24 relative: enough for
+// a value that goes to 4 significant bits next (16 instead of 30 us of a 4096-token gate/up
+// product's 240 us).
 __device__ __forceinline__ float swiglu(float g, float u) {
-  const float t = g * -1.44269504f;
-  const float lo = fmaf(g, -1.44269504f, -t) + g * -1.92596299e-8f;
-  const float z = __builtin_amdgcn_exp2f(t);
-  const float den = 1.0f + fmaf(z, lo * 0.69314718f, z);
-  return g * __builtin_amdgcn_rcpf(den) * u;
+  const float z = __builtin_amdgcn_exp2f(g * -1.44269504f);
+  return g * __builtin_amdgcn_rcpf(1.0f + z) * u;
 }
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }

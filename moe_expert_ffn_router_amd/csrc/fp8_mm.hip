@@ -236,12 +236,16 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
 // MI activation fragments past them; each MFMA starts from zero and its result
 // is folded into the accumulators one row subtile later, so the fold's
 // multiply-adds run under the next MFMAs.
-//   The copies bound this kernel (a block's 64 KB take longer to arrive than
-// to multiply), so a stage is refilled piece by piece as it is read rather than
-// as a whole at its end: the weights once every wave holds its fragments (row
-// subtile 1), the first half of each wave's rows at subtile MI/2, the second at
-// the last.  Every piece then has at least one block's time to arrive, and the
-// waits leave the pieces issued since outstanding.
+//   The copies bound this kernel (a block's 64 KB take as long to arrive as to
+// multiply), so they never stop: a stage is refilled piece by piece as it is
+// read rather than as a whole at its end - the weights once every wave holds its
+// fragments (row subtile 1), the first half of each wave's rows at subtile MI/2,
+// the second at the last - and the waits leave the pieces issued since
+// outstanding.  Every piece has at least one block's time to arrive.  A
+// workgroup owns its compute unit (LDS, registers) and works through a list of
+// tiles as one sequence of blocks: the next tile's first two blocks are copied
+// during the last two of the current one, so its look-up, launch and first loads
+// hide behind MFMAs and the epilogue.
 // ---------------------------------------------------------------------------
 template <int BM, int BN>
 struct TileStage {
@@ -249,156 +253,201 @@ struct TileStage {
   uint8_t b[BN * 128];  // weights, same layout
 };
 
+constexpr int kListTiles = 32;  // tiles of one workgroup at most
+constexpr int kXcds = 8, kXcdCus = 32;
+
+template <int BM, int BN, int WN, bool GATED>
+struct TileLds {
+  TileStage<BM, BN> st[2];
+  __attribute__((aligned(16))) float sc[3][BM * 4];  // rows' scales: [group of 4 blocks % 3][row][4]
+  float wsc[2][2][65536 / kFp8Block];  // [tile % 2]: its two rows of weight scales
+  __attribute__((aligned(16))) int list[kListTiles][4];  // slot, first row, rows, column block
+  int src[BM];  // gathered activation rows of the next tile
+  float row_max[GATED ? WN : 1][GATED ? BM : 1];  // largest |h| per wave column
+};
+
 // m-tiles that consecutive workgroups of one XCD share weights over
 constexpr int kPanel = 4;
 
-// Workgroup -> (row tile, column block) among mt x nnb tiles.  Hardware block b runs on
-// XCD b % 8: the tiles, in panels of kPanel row tiles that go column block by column
-// block, are cut into eight contiguous ranges of equal length.  (Grouped products know
-// mt on the device only: the grid is sized from a bound, and the workgroups behind the
-// ranges have nothing to do.)
-__device__ __forceinline__ bool tile_of(int b, int mt, int nnb, int& tile, int& nb) {
-  const int G = mt * nnb, per = (G + 7) >> 3;
-  const int v = (b & 7) * per + (b >> 3);
-  if ((b >> 3) >= per || v >= G) return false;
+// Tile v of mt x nnb: in panels of kPanel row tiles that go column block by column block.
+__device__ __forceinline__ void panel_tile(int v, int mt, int nnb, int& tile, int& nb) {
   const int panel = v / (kPanel * nnb), r = v - panel * (kPanel * nnb);
   const int rows = min(kPanel, mt - panel * kPanel);
   nb = r / rows;
   tile = panel * kPanel + r - nb * rows;
-  return true;
 }
 
-// Waits for this wave's LDS reads, then a barrier that no memory access moves across.
+// Waits for this wave's LDS accesses, then a barrier that no memory access moves across.
 #define MOE_LDS_SYNC()                                                   \
   do {                                                                   \
     __builtin_amdgcn_s_waitcnt(::moe::waitcnt_vm_lgkm0(63));             \
     asm volatile("s_barrier" ::: "memory");                              \
   } while (0)
 
-// LDS of a tile: its stages, the rows' scales, the tile's two rows of weight scales, and
-// (gate/up) the rows' largest h per wave column.
-template <int BM, int BN, int WN, bool GATED>
-struct TileLds {
-  TileStage<BM, BN> st[2];
-  __attribute__((aligned(16))) float sc[2][BM * 4];  // [row][4 blocks]
-  float wsc[2][65536 / kFp8Block];
-  float row_max[GATED ? WN : 1][GATED ? BM : 1];
-};
-
-// A tile of at most BM rows in LDS laid out for LM >= BM.
-template <int BM, int BN, int WM, int WN, bool GATED, int LM>
-__device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const RowTile& t, int nb,
-                                              TileLds<LM, BN, WN, GATED>& lds) {
+// Needs at least two blocks of K.
+template <int BM, int BN, int WM, int WN, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   constexpr int NW = WM * WN, MI = BM / WM / 16, NJ = BN / WN / 16;
   constexpr int COLS = GATED ? BN / 2 : BN;    // output columns
   constexpr int CPA = BM / 8 / NW, CPB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
+  constexpr int RW = BM / WM, HALF = RW / 2;           // rows of a wave row, and of half of one
   static_assert(NJ == 4 && BM % 64 == 0 && BM / 64 <= NW && MI > 2 && CPA / 2 <= NJ, "wave shape");
   static_assert(!GATED || COLS == kFp8Block, "gate/up: one scale block of h per tile");
+  __shared__ TileLds<BM, BN, WN, GATED> lds;
   auto& st = lds.st;
-  auto& sc = lds.sc;
-  auto& wsc = lds.wsc;
-  auto& row_max = lds.row_max;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int mh = wave / WN, nh = wave % WN;
-  const int row0 = __builtin_amdgcn_readfirstlane(t.row0);
-  const int rows = __builtin_amdgcn_readfirstlane(t.rows);
-  const int e = __builtin_amdgcn_readfirstlane(t.e);
   const int K = p.K, kb = (K + kFp8Block - 1) / kFp8Block;
-  const uint8_t* w = slot_base(p.w, p.w_stride, p, e);
-  const float* ws = reinterpret_cast<const float*>(slot_base(p.ws, p.ws_stride, p, e));
 
-  // activation row of local row lr: rows past the tile read its last one
-  auto source = [&](int lr) -> uint32_t {
-    const int r = min(lr, rows - 1);
-    if (p.row_of) return (uint32_t)(dbg_clamp(p.row_of[row0 + r], p.M, kDbgSorted) / p.k);
-    return (uint32_t)r;
-  };
-  const uint8_t* ab = p.row_of ? p.a : p.a + (size_t)row0 * K;
-  const uint8_t* sb = reinterpret_cast<const uint8_t*>(p.row_of ? p.a_scale
-                                                                : p.a_scale + (size_t)row0 * kb);
-  const uint8_t* wb = GATED ? w : w + (size_t)nb * BN * K;
+  // This workgroup's tiles.  Hardware block b runs on XCD b % 8: the tiles are cut into
+  // eight contiguous ranges, and an XCD's workgroups take its range in turn.  (Grouped
+  // products know the number of tiles here only; the host sized the grid from a bound.)
+  int mine;
+  {
+    const int x = (int)blockIdx.x % kXcds, i0 = (int)blockIdx.x / kXcds;
+    const int W = (int)gridDim.x / kXcds;
+    RowTiles<BM> tiles;
+    const int mt = p.counts ? tiles.load(p.counts, p.offsets, p.E, lane) : p.mt;
+    const int G = mt * p.nnb, per = (G + kXcds - 1) / kXcds;
+    const int end = min(per, G - x * per);
+    mine = i0 < end ? (end - i0 + W - 1) / W : 0;
+    mine = __builtin_amdgcn_readfirstlane(min(mine, kListTiles));
+    if (mine == 0) return;  // uniform
+    for (int q = wave; q < mine; q += NW) {
+      int tile, nb;
+      panel_tile(x * per + i0 + q * W, mt, p.nnb, tile, nb);
+      RowTile t;
+      if (p.counts) {
+        t = tiles.at(tile);
+        dbg_segment(t.row0, t.rows, p.M);
+      } else {
+        t.e = 0;
+        t.row0 = tile * BM;
+        t.rows = min(BM, p.M - t.row0);
+      }
+      const int slot = p.slot_of ? dbg_clamp(p.slot_of[t.e], p.E, kDbgSlot) : t.e;
+      if (lane == 0) *reinterpret_cast<i32x4*>(lds.list[q]) = i32x4{slot, t.row0, t.rows, nb};
+    }
+    __syncthreads();
+  }
+  auto entry = [&](int q, int f) { return __builtin_amdgcn_readfirstlane(lds.list[q][f]); };
+
+  // -- copies -----------------------------------------------------------------------
+  // Cursor: tile cr, block cc, with the tile's addresses.
+  int cr = 0, cc = 0, cgrp = 0;  // cgrp: scale group counter % 3
+  const uint8_t *ab, *sb, *wb;
   uint32_t ao[CPA], wo[CPB], so = 0;
-  const uint32_t unit = (uint32_t)(lane & 7);
+  // The lane's part of the addresses is recomputed per tile: hoisted out of the loop it would
+  // cost registers that the accumulators need.
+  auto fresh_lane = [&]() {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
   // local row that copy q of this wave starts at: the first CPA / 2 cover the first halves of
   // the waves' row groups, the others the second halves
-  constexpr int RW = BM / WM, HALF = RW / 2;
   auto a_row = [&](int q) {
     const int x = (wave * (CPA / 2) + q % (CPA / 2)) * 8;
     return x / HALF * RW + x % HALF + (q < CPA / 2 ? 0 : HALF);
   };
-#pragma unroll
-  for (int q = 0; q < CPA; ++q) {
-    const int lr = a_row(q) + (lane >> 3);
-    ao[q] = source(lr) * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
-  }
-#pragma unroll
-  for (int q = 0; q < CPB; ++q) {
-    const int lr = (wave * CPB + q) * 8 + (lane >> 3);
-    int wr;
-    if constexpr (GATED) {  // a wave's 64 weight rows: 32 gate rows, then their up rows
-      const int col = nb * COLS + (lr >> 6) * 32 + (lr & 31);
-      wr = (lr & 32) ? p.I + col : col;
-    } else {
-      wr = min(lr, p.N - 1 - nb * BN);
+  // the activation rows of tile q, gathered ones through LDS (issue_src)
+  auto issue_src = [&](int q) {
+    if (wave < BM / 64) {
+      const int r = min(wave * 64 + lane, max(entry(q, 2), 1) - 1);
+      dma4(reinterpret_cast<const uint8_t*>(p.row_of + entry(q, 1)), (uint32_t)r * 4u,
+           lds.src + wave * 64);
     }
-    wo[q] = (uint32_t)wr * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
-  }
-  if (wave < BM / 64) so = source(wave * 64 + lane) * (uint32_t)kb * 4u;
-  // a short last block: units past K re-read its first
-  auto back = [&](int lr) -> uint32_t {
-    const uint32_t u = (unit ^ a_swz(lr)) * 16;
-    return u < (uint32_t)(K % kFp8Block) ? 0u : u;
   };
-  auto is_short = [&](int c) { return c + 1 == kb && K % kFp8Block != 0; };
-  // copies [q0, q1) of block c
-  auto issue_a = [&](int c, int q0, int q1) {
-    uint8_t* dst = st[c & 1].a;
-    const uint8_t* src = ab + (size_t)c * kFp8Block;
-    const bool cut = is_short(c);
+  auto point_at = [&](int q) {
+    const int slot = entry(q, 0), row0 = entry(q, 1), rows = entry(q, 2), nb = entry(q, 3);
+    const int ln = fresh_lane();
+    const uint32_t unit = (uint32_t)(ln & 7);
+    // rows past the tile read its last one
+    auto source = [&](int lr) -> uint32_t {
+      if (p.row_of) return (uint32_t)(dbg_clamp(lds.src[lr], p.M, kDbgSorted) / p.k);
+      return (uint32_t)min(lr, max(rows, 1) - 1);
+    };
+    ab = p.row_of ? p.a : p.a + (size_t)row0 * K;
+    sb = reinterpret_cast<const uint8_t*>(p.row_of ? p.a_scale : p.a_scale + (size_t)row0 * kb);
+    wb = p.w + (size_t)slot * p.w_stride + (GATED ? 0 : (size_t)nb * BN * K);
 #pragma unroll
-    for (int q = q0; q < q1; ++q)
-      dma16(src, cut ? ao[q] - back(a_row(q) + (lane >> 3)) : ao[q], dst + a_row(q) * 128);
-  };
-  auto issue_b = [&](int c, int q0, int q1) {
-    uint8_t* dst = st[c & 1].b + wave * CPB * 1024;
-    const uint8_t* src = wb + (size_t)c * kFp8Block;
-    const bool cut = is_short(c);
+    for (int i = 0; i < CPA; ++i) {
+      const int lr = a_row(i) + (ln >> 3);
+      ao[i] = source(lr) * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
+    }
 #pragma unroll
-    for (int q = q0; q < q1; ++q)
-      dma16(src, cut ? wo[q] - back((wave * CPB + q) * 8 + (lane >> 3)) : wo[q], dst + q * 1024);
-  };
-  // the rows' scales of blocks [s_first(f), s_first(f) + 4) as group f; fewer than four blocks
-  // in all: one at a time, each a group
-  const bool quad = kb >= 4;
-  auto s_first = [&](int f) { return quad ? min(4 * f, kb - 4) : f; };
-  auto issue_s = [&](int f) {
-    if (wave >= BM / 64) return;
-    float* dst = sc[f & 1] + wave * 64 * (quad ? 4 : 1);
-    if (quad) dma16(sb, so + (uint32_t)s_first(f) * 4u, dst);
-    else dma4(sb, so + (uint32_t)f * 4u, dst);
-  };
-  auto scale_of = [&](int c, int r) {
-    const int f = quad ? c >> 2 : c;
-    return quad ? sc[f & 1][r * 4 + c - s_first(f)] : sc[f & 1][r];
-  };
-
-  f32x4 acc[MI][NJ];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // the tile's weight scales: its two 128-row blocks (gate/up: the gate and the up block)
-  for (int i = tid; i < kb; i += 64 * NW) {
+    for (int i = 0; i < CPB; ++i) {
+      const int lr = (wave * CPB + i) * 8 + (ln >> 3);
+      int wr;
+      if constexpr (GATED) {  // a wave's 64 weight rows: 32 gate rows, then their up rows
+        const int col = nb * COLS + (lr >> 6) * 32 + (lr & 31);
+        wr = (lr & 32) ? p.I + col : col;
+      } else {
+        wr = min(lr, p.N - 1 - nb * BN);
+      }
+      wo[i] = (uint32_t)wr * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
+    }
+    if (wave < BM / 64) so = source(wave * 64 + ln) * (uint32_t)kb * 4u;
+    // the tile's two rows of weight scales (gate/up: the gate and the up block)
     const int last = (p.N - 1) / kFp8Block;
     const int b0 = GATED ? nb : min(nb * (BN / kFp8Block), last);
     const int b1 = GATED ? p.I / kFp8Block + nb : min(nb * (BN / kFp8Block) + 1, last);
-    wsc[0][i] = ws[b0 * kb + i];
-    wsc[1][i] = ws[b1 * kb + i];
-  }
-  const float* wsw = wsc[GATED ? 0 : nh * (BN / WN) / kFp8Block];
-  __syncthreads();
+    const uint8_t* ws = p.ws + (size_t)slot * p.ws_stride;
+    for (int i = wave; i < 2 * ((kb + 63) >> 6); i += NW)
+      dma4(ws + (size_t)(i & 1 ? b1 : b0) * kb * 4,
+           (uint32_t)min((i >> 1) * 64 + ln, kb - 1) * 4u, &lds.wsc[q & 1][i & 1][(i >> 1) * 64]);
+  };
+  // a short last block: units past K re-read its first
+  auto back = [&](int row) -> uint32_t {
+    const int ln = fresh_lane();
+    const uint32_t u = (uint32_t)((ln & 7) ^ a_swz(row + (ln >> 3))) * 16;
+    return u < (uint32_t)(K % kFp8Block) ? 0u : u;
+  };
+  auto is_short = [&](int c) { return c + 1 == kb && K % kFp8Block != 0; };
+  // copies [q0, q1) of the cursor's block into stage s
+  auto issue_a = [&](int s, int q0, int q1) {
+    const uint8_t* src = ab + (size_t)cc * kFp8Block;
+    const bool cut = is_short(cc);
+#pragma unroll
+    for (int q = q0; q < q1; ++q)
+      dma16(src, cut ? ao[q] - back(a_row(q)) : ao[q], st[s].a + a_row(q) * 128);
+  };
+  auto issue_b = [&](int s, int q0, int q1) {
+    uint8_t* dst = st[s].b + wave * CPB * 1024;
+    const uint8_t* src = wb + (size_t)cc * kFp8Block;
+    const bool cut = is_short(cc);
+#pragma unroll
+    for (int q = q0; q < q1; ++q)
+      dma16(src, cut ? wo[q] - back((wave * CPB + q) * 8) : wo[q], dst + q * 1024);
+  };
+  // The rows' scales in groups of four blocks, the last one ending with K (fewer than four
+  // blocks in all: one by one).  Three groups may be in use at once, where the middle one is
+  // a single block.
+  const bool quad = kb >= 4;
+  auto opens = [&](int c) { return !quad || (c & 3) == 0; };
+  auto s_first = [&](int c) { return quad ? min(c & ~3, kb - 4) : c; };
+  auto next3 = [](int v) { return v == 2 ? 0 : v + 1; };
+  auto issue_s = [&]() {
+    if (wave >= BM / 64) return;
+    float* dst = lds.sc[cgrp] + wave * 64 * (quad ? 4 : 1);
+    const uint32_t off = so + (uint32_t)s_first(cc) * 4u;
+    if (quad) dma16(sb, off, dst);
+    else dma4(sb, off, dst);
+  };
+  // Moves the cursor on by one block; true where that opens a tile.  Behind the last tile it
+  // stays: the loop's last two turns copy a block that nobody reads, rather than carry
+  // branches through all the others.
+  auto advance = [&]() {
+    if (cc + 1 == kb && cr + 1 == mine) return false;
+    const bool fresh = cc + 1 == kb;
+    cc = fresh ? 0 : cc + 1;
+    cr += fresh;
+    if (opens(cc)) cgrp = next3(cgrp);
+    return fresh;
+  };
+
+  // -- compute ----------------------------------------------------------------------
   // A row's swizzle depends on its low 4 bits only: one address per operand and unit, the
   // subtiles at constant offsets.
   auto frag = [&](const uint8_t* base, int o0, int o1) {
@@ -408,81 +457,93 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const RowTile& t
   };
   const int r0 = mh * RW + l16, rb = nh * (BN / WN) + l16;
   const int u0 = ((2 * g) ^ a_swz(l16)) * 16, u1 = ((2 * g + 1) ^ a_swz(l16)) * 16;
-  auto frag_a = [&](int c, int i) {
-    return frag(st[c & 1].a + i * 2048, r0 * 128 + u0, r0 * 128 + u1);
+  auto frag_a = [&](int s, int i) {
+    return frag(st[s].a + i * 2048, r0 * 128 + u0, r0 * 128 + u1);
   };
-  auto frag_b = [&](int c, int j) {
-    return frag(st[c & 1].b + j * 2048, rb * 128 + u0, rb * 128 + u1);
+  auto frag_b = [&](int s, int j) {
+    return frag(st[s].b + j * 2048, rb * 128 + u0, rb * 128 + u1);
   };
-
-  // Zeros past K in the short last block (every wave's copies have landed).
-  auto zero_tail = [&](TileStage<LM, BN>& S) {
-    const int u0 = K % kFp8Block / 16, nu = 8 - u0;
-    for (int i = tid; i < (BM + BN) * nu; i += 64 * NW) {
-      const int r = i / nu, u = u0 + i - r * nu, lr = r < BM ? r : r - BM;
-      *reinterpret_cast<i32x4*>((r < BM ? S.a : S.b) + lr * 128 + ((u ^ a_swz(lr)) * 16)) =
+  auto scale_of = [&](int grp, int c, int r) {
+    return quad ? lds.sc[grp][r * 4 + c - s_first(c)] : lds.sc[grp][r];
+  };
+  // Zeros past K in a short last block: once its copies have landed, before it is read.
+  auto whole = [&](int s, int c) {
+    if (!is_short(c)) return;
+    const int z0 = K % kFp8Block / 16, nz = 8 - z0;
+    for (int i = tid; i < (BM + BN) * nz; i += 64 * NW) {
+      const int r = i / nz, u = z0 + i - r * nz, lr = r < BM ? r : r - BM;
+      *reinterpret_cast<i32x4*>((r < BM ? st[s].a : st[s].b) + lr * 128 + ((u ^ a_swz(lr)) * 16)) =
           i32x4{0, 0, 0, 0};
     }
-    __syncthreads();
+    MOE_LDS_SYNC();
   };
 
-  // Fragments live across blocks: the weights', the next row subtile's, and the NJ
-  // results not yet folded in with their scale.
-  fp8x32 bf[NJ], af;
-  float sa, s0 = 0.f, s1 = 0.f;
-  f32x4 d[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // The zeroing of a short last block comes once its copies have landed, before it is read.
-  auto whole = [&](int c) {
-    if (c + 1 == kb && K % kFp8Block) zero_tail(st[c & 1]);
-  };
-  issue_s(0);
-  issue_b(0, 0, CPB);
-  issue_a(0, 0, CPA);
-  float w0 = wsw[0], w1 = GATED ? wsc[1][0] : 0.f;
-  if (kb > 1) {
-    if (!quad) issue_s(1);
-    issue_b(1, 0, CPB);
-    issue_a(1, 0, CPA);
-    MOE_DMA_SYNC(CPA + CPB);
-  } else {
+  // The first two blocks.
+  if (p.row_of) {
+    issue_src(0);
     MOE_DMA_SYNC(0);
   }
-  whole(0);
+  point_at(0);
+  issue_s();
+  issue_b(0, 0, CPB);
+  issue_a(0, 0, CPA);
+  advance();  // kb >= 2: the same tile
+  if (opens(cc)) issue_s();
+  issue_b(1, 0, CPB);
+  issue_a(1, 0, CPA);
+  MOE_DMA_SYNC(CPA + CPB);
+  if (p.row_of && mine > 1) issue_src(1);
+  whole(0, 0);
+
+  f32x4 acc[MI][NJ], d[NJ];
+  fp8x32 bf[NJ], af;
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
+  const int wrow = GATED ? 0 : nh * (BN / WN) / kFp8Block;
+  int r = 0, c = 0, grp = 0;  // tile, block and scale group being multiplied
+  int rows = entry(0, 2);
+  float w0 = lds.wsc[0][wrow][0], w1 = GATED ? lds.wsc[0][1][0] : 0.f;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) bf[j] = frag_b(0, j);
   af = frag_a(0, 0);
-  sa = scale_of(0, r0);
-  for (int c = 0; c < kb; ++c) {
-    const int cn = min(c + 1, kb - 1);
-    const float n0 = wsw[cn], n1 = GATED ? wsc[1][cn] : 0.f;
-    const bool more = c + 1 < kb;
+  float sa = scale_of(0, 0, r0), s0 = 0.f, s1 = 0.f;
+  for (int s = 0;; s ^= 1) {
+    const bool last = c + 1 == kb;
+    const int cn = last ? 0 : c + 1, rn = last ? r + 1 : r;
+    const int gn = opens(cn) ? next3(grp) : grp;
+    const float n0 = lds.wsc[rn & 1][wrow][cn], n1 = GATED ? lds.wsc[rn & 1][1][cn] : 0.f;
+    const bool fresh = advance();
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const fp8x32 a = af;
       const float f0 = sa * w0, f1 = GATED ? sa * w1 : 0.f;
-      // every wave has read what the next copies overwrite (the waits on this wave's own LDS
-      // reads come before its barrier)
-      if (i == 1 && c + 2 < kb) {
+      // Every wave has read what the next copies overwrite (the waits on this wave's own LDS
+      // reads come before its barrier).
+      if (i == 1) {
         MOE_LDS_SYNC();
-        if (quad && (c & 3) == 1 && s_first(c >> 2) + 4 < kb) issue_s((c >> 2) + 1);
+        if (fresh) point_at(cr);
+        if (opens(cc)) issue_s();
       }
-      if (i == MI / 2 && c + 2 < kb) MOE_LDS_SYNC();
+      if (i == MI / 2) {
+        MOE_LDS_SYNC();
+        if (fresh && p.row_of && cr + 1 < mine) issue_src(cr + 1);
+      }
       if (i + 1 < MI) {
-        af = frag_a(c, i + 1);
-        sa = scale_of(c, r0 + (i + 1) * 16);
-      } else if (more) {
-        // the next block has landed (the one behind it may still be on its way)
-        if (c + 2 < kb) {
-          MOE_DMA_SYNC(CPB + CPA / 2);
-          if (!quad) issue_s(c + 2);
-        } else {
-          MOE_DMA_SYNC(0);
-        }
-        whole(c + 1);
-        af = frag_a(c + 1, 0);
-        sa = scale_of(c + 1, r0);
+        af = frag_a(s, i + 1);
+        sa = scale_of(grp, c, r0 + (i + 1) * 16);
+      } else {
+        // the next block has landed; the one behind it may still be on its way
+        MOE_DMA_SYNC(CPB + CPA / 2);
+        whole(s ^ 1, cn);
+        af = frag_a(s ^ 1, 0);
+        sa = scale_of(gn, cn, r0);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -490,17 +551,15 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const RowTile& t
         f32x4& o = acc[i == 0 ? MI - 1 : i - 1][j];
         const float f = GATED && j >= NJ / 2 ? s1 : s0;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = fmaf(f, d[j][r], o[r]);
+        for (int q = 0; q < 4; ++q) o[q] = fmaf(f, d[j][q], o[q]);
         pin(o);
         d[j] = mfma_e4m3(bf[j], a, f32x4{0.f, 0.f, 0.f, 0.f});
         pin(d[j]);
-        if (i + 1 == MI && more) bf[j] = frag_b(c + 1, j);
+        if (i + 1 == MI) bf[j] = frag_b(s ^ 1, j);
         // the freed pieces' copies, spread over the MFMAs
-        if (c + 2 < kb) {
-          if (i == 1) issue_b(c + 2, j * CPB / NJ, (j + 1) * CPB / NJ);
-          if (i == MI / 2 && j < CPA / 2) issue_a(c + 2, j, j + 1);
-          if (i + 1 == MI && j < CPA / 2) issue_a(c + 2, CPA / 2 + j, CPA / 2 + j + 1);
-        }
+        if (i == 1) issue_b(s, j * CPB / NJ, (j + 1) * CPB / NJ);
+        if (i == MI / 2 && j < CPA / 2) issue_a(s, j, j + 1);
+        if (i + 1 == MI && j < CPA / 2) issue_a(s, CPA / 2 + j, CPA / 2 + j + 1);
         __builtin_amdgcn_sched_barrier(0);
       }
       s0 = f0;
@@ -508,88 +567,67 @@ __device__ __forceinline__ void fp8_tile_body(const Fp8Args& p, const RowTile& t
     }
     w0 = n0;
     w1 = n1;
-  }
+    if (last) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      acc[MI - 1][j][r] = fmaf(GATED && j >= NJ / 2 ? s1 : s0, d[j][r], acc[MI - 1][j][r]);
-
-  // acc[i][j][r]: row mh*(BM/WM) + 16i + l16, weight row nh*64 + 16j + 4g + r of the tile
-  const int rl = mh * (BM / WM) + l16;
-  if constexpr (GATED) {
-    // h in place of the gate sums, its largest magnitude per row over the waves' 32 columns
-    float hm[MI];
+        for (int q = 0; q < 4; ++q)
+          acc[MI - 1][j][q] = fmaf(GATED && j >= NJ / 2 ? s1 : s0, d[j][q], acc[MI - 1][j][q]);
+      // acc[i][j][q]: row r0 + 16i, weight row nh*64 + 16j + 4g + q of the tile
+      const int row0 = entry(r, 1), nb = entry(r, 3);
+      if constexpr (GATED) {
+        // h in place of the gate sums; its largest magnitude per row over the waves' columns
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      uint32_t m = 0;
+        for (int i = 0; i < MI; ++i) {
+          uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          acc[i][j][r] = swiglu(acc[i][j][r], acc[i][j + 2][r]);
-          m = umax(m, __float_as_uint(acc[i][j][r]) & 0x7fffffffu);
+            for (int q = 0; q < 4; ++q) {
+              acc[i][j][q] = swiglu(acc[i][j][q], acc[i][j + 2][q]);
+              m = umax(m, __float_as_uint(acc[i][j][q]) & 0x7fffffffu);
+            }
+          m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+          m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+          if (g == 0) lds.row_max[nh][r0 + i * 16] = __uint_as_float(m);
         }
-      m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-      m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      hm[i] = __uint_as_float(m);
-      if (g == 0) row_max[nh][rl + i * 16] = hm[i];
-    }
-    __syncthreads();
-    uint8_t* hc = st[0].a;  // the tile's codes [BM][128], written out by whole rows
+        MOE_LDS_SYNC();
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      uint32_t m = 0;
+        for (int i = 0; i < MI; ++i) {
+          uint32_t m = 0;
 #pragma unroll
-      for (int q = 0; q < WN; ++q) m = umax(m, __float_as_uint(row_max[q][rl + i * 16]));
-      const Fp8Scale s = fp8_block_scale(m);
+          for (int q = 0; q < WN; ++q) m = umax(m, __float_as_uint(lds.row_max[q][r0 + i * 16]));
+          const Fp8Scale sc = fp8_block_scale(m);
+          if (r0 + i * 16 < rows) {
+            const size_t row = (size_t)(row0 + r0 + i * 16);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<int*>(hc + (rl + i * 16) * 128 + nh * 32 + j * 16 + 4 * g) =
-            fp8_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], s);
-      if (nh == 0 && g == 0 && rl + i * 16 < rows)
-        p.hs[(size_t)(row0 + rl + i * 16) * (p.I / kFp8Block) + nb] = s.scale;
-    }
-    __syncthreads();
-    for (int i = tid; i < rows * 8; i += 64 * NW)
-      *reinterpret_cast<i32x4*>(p.hq + (size_t)(row0 + (i >> 3)) * p.I + nb * COLS + (i & 7) * 16) =
-          *reinterpret_cast<const i32x4*>(hc + i * 16);
-  } else {
-    const int col0 = nb * BN + nh * (BN / WN) + 4 * g;
+            for (int j = 0; j < 2; ++j)
+              *reinterpret_cast<int*>(p.hq + row * p.I + nb * COLS + nh * 32 + j * 16 + 4 * g) =
+                  fp8_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], sc);
+            if (nh == 0 && g == 0) p.hs[row * (p.I / kFp8Block) + nb] = sc.scale;
+          }
+        }
+      } else {
+        const int col0 = nb * BN + nh * (BN / WN) + 4 * g;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (rl + i * 16 >= rows) continue;
-      uint16_t* dst = p.y + (size_t)(row0 + rl + i * 16) * p.N + col0;
+        for (int i = 0; i < MI; ++i) {
+          if (r0 + i * 16 >= rows) continue;
+          uint16_t* dst = p.y + (size_t)(row0 + r0 + i * 16) * p.N + col0;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        store4(dst + j * 16, acc[i][j], p.N - col0 - j * 16, p.N % 4 == 0);
+          for (int j = 0; j < NJ; ++j)
+            store4(dst + j * 16, acc[i][j], p.N - col0 - j * 16, p.N % 4 == 0);
+        }
       }
+      if (rn == mine) break;
+      clear();
+      s0 = s1 = 0.f;
+      rows = entry(rn, 2);
     }
+    r = rn;
+    c = cn;
+    grp = gn;
   }
-}
-
-// Tiles of up to BM rows; one of at most half takes half the rows per wave (the last tile of an
-// expert's rows).
-template <int BM, int BN, int WM, int WN, bool GATED>
-__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
-  __shared__ TileLds<BM, BN, WN, GATED> lds;
-  int tile, nb;
-  RowTile t;
-  if (p.counts) {
-    RowTiles<BM> tiles;
-    const int mt = tiles.load(p.counts, p.offsets, p.E, threadIdx.x & 63);
-    if (!tile_of((int)blockIdx.x, mt, p.nnb, tile, nb)) return;  // uniform per block
-    t = tiles.at(tile);
-    dbg_segment(t.row0, t.rows, p.M);
-    if (t.rows <= 0) return;
-  } else {
-    if (!tile_of((int)blockIdx.x, p.mt, p.nnb, tile, nb)) return;
-    t.e = 0;
-    t.row0 = tile * BM;
-    t.rows = min(BM, p.M - t.row0);
-  }
-  if (t.rows <= BM / 2) fp8_tile_body<BM / 2, BN, WM, WN, GATED, BM>(p, t, nb, lds);
-  else fp8_tile_body<BM, BN, WM, WN, GATED, BM>(p, t, nb, lds);
+  MOE_DMA_SYNC(0);  // copies still on their way into this workgroup's LDS
 }
 
 template <int BM, int BN, int WM, int WN, bool GATED>
@@ -597,11 +635,14 @@ int launch_tiles(Fp8Args p, hipStream_t s, const char* who) {
   constexpr int COLS = GATED ? BN / 2 : BN;
   p.nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
   const int64_t mt = p.counts ? row_tiles_bound(p.M, p.E, BM) : ((int64_t)p.M + BM - 1) / BM;
-  const int64_t blocks = (mt * p.nnb + 7) / 8 * 8;
-  p.mt = (int)mt;
-  if (blocks > ((int64_t)1 << 31) - 1)
+  const int64_t per = (mt * p.nnb + kXcds - 1) / kXcds;  // tiles of an XCD
+  // one workgroup per compute unit, more where its list would overflow
+  int64_t W = per < kXcdCus ? per : kXcdCus;
+  if (W * kListTiles < per) W = (per + kListTiles - 1) / kListTiles;
+  if (mt * p.nnb > ((int64_t)1 << 31) - 1)
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-  fp8_tile_kernel<BM, BN, WM, WN, GATED><<<(unsigned)blocks, 64 * WM * WN, 0, s>>>(p);
+  p.mt = (int)mt;
+  fp8_tile_kernel<BM, BN, WM, WN, GATED><<<(unsigned)(W * kXcds), 64 * WM * WN, 0, s>>>(p);
   return check_launch(who);
 }
 
@@ -698,7 +739,7 @@ extern "C" int moe_fp8_matmul(const uint8_t* a, const float* a_scale, int32_t M,
   p.E = E; p.M = M; p.N = N; p.K = K;
   p.y = y;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (M <= 32 * (int64_t)E) return launch_rows16<false>(p, s, who);
+  if (M <= 32 * (int64_t)E || K <= kFp8Block) return launch_rows16<false>(p, s, who);
   return launch_tiles<256, 256, 2, 4, false>(p, s, who);
 }
 
@@ -756,8 +797,10 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   p.h = reinterpret_cast<float*>(wb + B.h);
   p.hq = wb + B.hq;
   p.hs = reinterpret_cast<float*>(wb + B.hs);
-  // the tile kernel addresses the gathered activation rows with 32-bit offsets
-  const bool tiles = A > 32 * (int64_t)W->E && (int64_t)T * H < ((int64_t)1 << 32);
+  // the tile kernel addresses the gathered activation rows with 32-bit offsets and needs two
+  // blocks of K
+  const bool tiles = A > 32 * (int64_t)W->E && (int64_t)T * H < ((int64_t)1 << 32) &&
+                     H > kFp8Block && I > kFp8Block;
   int st;
   if (tiles) {
     st = launch_tiles<256, 256, 2, 4, true>(p, s, who);

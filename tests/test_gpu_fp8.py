@@ -313,8 +313,10 @@ def _ffn_reference(x, k, offsets, sorted_idx, parts, H, I):
         g, u, dg, du = gu[:, :I], gu[:, I:], dgu[:, :I], dgu[:, I:]
         act = OFF.silu(g)
         h = act * u
-        # |silu'| <= 1.1; expf, the division and two products: 8 roundings
-        dh = 1.1 * dg * np.abs(u) + np.abs(act) * du + 1.1 * dg * du + 8 * EPS * np.abs(h)
+        # |silu'| <= 1.1; 2^x and 1/x of one ulp, a sum and two products: 8 roundings; the
+        # exponent's product with log2(e) and that constant: e^-g off by 2 |g| eps
+        dh = (1.1 * dg * np.abs(u) + np.abs(act) * du + 1.1 * dg * du
+              + (8 + 2 * np.abs(g)) * EPS * np.abs(h))
         hc, hs = O8.quantize(h)
         hq = O8.rows_value(hc, hs)
         off = np.zeros_like(h)
