@@ -234,8 +234,8 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
 // rows' scales likewise, four blocks at a time.  A wave owns MI x NJ subtiles of
 // 16 x 16: it keeps the block's NJ weight fragments in registers and streams its
 // MI activation fragments past them; each MFMA starts from zero and its result
-// is folded into the accumulators one row subtile later, so the fold's
-// multiply-adds run under the next MFMAs.
+// is folded into the accumulators two MFMAs later, so the fold's multiply-adds
+// run under the MFMAs between.
 //   The copies bound this kernel (a block's 64 KB take as long to arrive as to
 // multiply), so they never stop: a stage is refilled piece by piece as it is
 // read rather than as a whole at its end - the weights once every wave holds its
@@ -284,8 +284,8 @@ __device__ __forceinline__ void panel_tile(int v, int mt, int nnb, int& tile, in
     asm volatile("s_barrier" ::: "memory");                              \
   } while (0)
 
-// Needs at least two blocks of K.
-template <int BM, int BN, int WM, int WN, bool GATED>
+// Needs at least two blocks of K; QUAD: at least four.
+template <int BM, int BN, int WM, int WN, bool GATED, bool QUAD>
 __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   constexpr int NW = WM * WN, MI = BM / WM / 16, NJ = BN / WN / 16;
   constexpr int COLS = GATED ? BN / 2 : BN;    // output columns
@@ -424,15 +424,15 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   // The rows' scales in groups of four blocks, the last one ending with K (fewer than four
   // blocks in all: one by one).  Three groups may be in use at once, where the middle one is
   // a single block.
-  const bool quad = kb >= 4;
-  auto opens = [&](int c) { return !quad || (c & 3) == 0; };
-  auto s_first = [&](int c) { return quad ? min(c & ~3, kb - 4) : c; };
+  constexpr int PER = QUAD ? 4 : 1;
+  auto opens = [&](int c) { return !QUAD || (c & 3) == 0; };
+  auto s_first = [&](int c) { return QUAD ? min(c & ~3, kb - 4) : c; };
   auto next3 = [](int v) { return v == 2 ? 0 : v + 1; };
   auto issue_s = [&]() {
     if (wave >= BM / 64) return;
-    float* dst = lds.sc[cgrp] + wave * 64 * (quad ? 4 : 1);
+    float* dst = lds.sc[cgrp] + wave * 64 * PER;
     const uint32_t off = so + (uint32_t)s_first(cc) * 4u;
-    if (quad) dma16(sb, off, dst);
+    if (QUAD) dma16(sb, off, dst);
     else dma4(sb, off, dst);
   };
   // Moves the cursor on by one block; true where that opens a tile.  Behind the last tile it
@@ -463,8 +463,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   auto frag_b = [&](int s, int j) {
     return frag(st[s].b + j * 2048, rb * 128 + u0, rb * 128 + u1);
   };
-  auto scale_of = [&](int grp, int c, int r) {
-    return quad ? lds.sc[grp][r * 4 + c - s_first(c)] : lds.sc[grp][r];
+  auto scale_of = [&](int grp, int c, int i) {
+    return *(lds.sc[grp] + (c - s_first(c)) + r0 * PER + i * 16 * PER);
   };
   // Zeros past K in a short last block: once its copies have landed, before it is read.
   auto whole = [&](int s, int c) {
@@ -495,137 +495,154 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   if (p.row_of && mine > 1) issue_src(1);
   whole(0, 0);
 
-  f32x4 acc[MI][NJ], d[NJ];
+  f32x4 acc[MI][NJ], d[2];  // d: the last two results, not folded in yet
   fp8x32 bf[NJ], af;
-  auto clear = [&]() {
+  float sa;
+  const int wrow = GATED ? 0 : nh * (BN / WN) / kFp8Block;
+  int s = 0, grp = 0;  // stage and scale group of the block being multiplied
+  // its weight and first activation fragments
+  auto first_frags = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bf[j] = frag_b(s, j);
+    af = frag_a(s, 0);
+    sa = scale_of(grp, c, 0);
+  };
+  first_frags(0);
+  // Every wave has read what the next copies overwrite (the waits on this wave's own LDS reads
+  // come before its barrier): the weights' place, the first and the second halves of the rows.
+  // At the second, the next block has landed; the one behind it may still be on its way.
+  auto free_b = [&](bool fresh) {
+    MOE_LDS_SYNC();
+    if (fresh) point_at(cr);
+    if (opens(cc)) issue_s();
+  };
+  auto free_a = [&](bool fresh) {
+    MOE_LDS_SYNC();
+    if (fresh && p.row_of && cr + 1 < mine) issue_src(cr + 1);
+  };
+  auto landed = [&](int cn) {
+    MOE_DMA_SYNC(CPB + CPA / 2);
+    whole(s ^ 1, cn);
+  };
+  for (int r = 0; r < mine; ++r) {
+    const int rows = entry(r, 2), row0 = entry(r, 1), nb = entry(r, 3);
+    if (mh * RW >= rows) {  // no rows for this wave: its share of the copies and the barriers
+      for (int c = 0; c < kb; ++c) {
+        const int cn = c + 1 == kb ? 0 : c + 1;
+        const bool fresh = advance();
+        free_b(fresh);
+        issue_b(s, 0, CPB);
+        free_a(fresh);
+        issue_a(s, 0, CPA / 2);
+        landed(cn);
+        issue_a(s, CPA / 2, CPA);
+        s ^= 1;
+        if (opens(cn)) grp = next3(grp);
+      }
+      if (GATED) MOE_LDS_SYNC();  // the other waves' exchange of row maxima
+      first_frags(0);
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    d[0] = d[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float w0 = lds.wsc[r & 1][wrow][0], w1 = GATED ? lds.wsc[r & 1][1][0] : 0.f;
+    float s1 = 0.f;  // scale of the previous row subtile's last two results
+    for (int c = 0; c < kb; ++c) {
+      const int cn = c + 1 == kb ? 0 : c + 1;
+      const int gn = opens(cn) ? next3(grp) : grp;
+      const float n0 = lds.wsc[r & 1][wrow][cn], n1 = GATED ? lds.wsc[r & 1][1][cn] : 0.f;
+      const bool fresh = advance();
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  };
-  clear();
-  const int wrow = GATED ? 0 : nh * (BN / WN) / kFp8Block;
-  int r = 0, c = 0, grp = 0;  // tile, block and scale group being multiplied
-  int rows = entry(0, 2);
-  float w0 = lds.wsc[0][wrow][0], w1 = GATED ? lds.wsc[0][1][0] : 0.f;
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) bf[j] = frag_b(0, j);
-  af = frag_a(0, 0);
-  float sa = scale_of(0, 0, r0), s0 = 0.f, s1 = 0.f;
-  for (int s = 0;; s ^= 1) {
-    const bool last = c + 1 == kb;
-    const int cn = last ? 0 : c + 1, rn = last ? r + 1 : r;
-    const int gn = opens(cn) ? next3(grp) : grp;
-    const float n0 = lds.wsc[rn & 1][wrow][cn], n1 = GATED ? lds.wsc[rn & 1][1][cn] : 0.f;
-    const bool fresh = advance();
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const fp8x32 a = af;
-      const float f0 = sa * w0, f1 = GATED ? sa * w1 : 0.f;
-      // Every wave has read what the next copies overwrite (the waits on this wave's own LDS
-      // reads come before its barrier).
-      if (i == 1) {
-        MOE_LDS_SYNC();
-        if (fresh) point_at(cr);
-        if (opens(cc)) issue_s();
-      }
-      if (i == MI / 2) {
-        MOE_LDS_SYNC();
-        if (fresh && p.row_of && cr + 1 < mine) issue_src(cr + 1);
-      }
-      if (i + 1 < MI) {
-        af = frag_a(s, i + 1);
-        sa = scale_of(grp, c, r0 + (i + 1) * 16);
-      } else {
-        // the next block has landed; the one behind it may still be on its way
-        MOE_DMA_SYNC(CPB + CPA / 2);
-        whole(s ^ 1, cn);
-        af = frag_a(s ^ 1, 0);
-        sa = scale_of(gn, cn, r0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        f32x4& o = acc[i == 0 ? MI - 1 : i - 1][j];
-        const float f = GATED && j >= NJ / 2 ? s1 : s0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = fmaf(f, d[j][q], o[q]);
-        pin(o);
-        d[j] = mfma_e4m3(bf[j], a, f32x4{0.f, 0.f, 0.f, 0.f});
-        pin(d[j]);
-        if (i + 1 == MI) bf[j] = frag_b(s ^ 1, j);
-        // the freed pieces' copies, spread over the MFMAs
-        if (i == 1) issue_b(s, j * CPB / NJ, (j + 1) * CPB / NJ);
-        if (i == MI / 2 && j < CPA / 2) issue_a(s, j, j + 1);
-        if (i + 1 == MI && j < CPA / 2) issue_a(s, CPA / 2 + j, CPA / 2 + j + 1);
+      for (int i = 0; i < MI; ++i) {
+        const fp8x32 a = af;
+        const float f0 = sa * w0, f1 = GATED ? sa * w1 : f0;
+        if (i == 1) free_b(fresh);
+        if (i == MI / 2) free_a(fresh);
+        if (i + 1 < MI) {
+          af = frag_a(s, i + 1);
+          sa = scale_of(grp, c, i + 1);
+        } else {
+          landed(cn);
+          af = frag_a(s ^ 1, 0);
+          sa = scale_of(gn, cn, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          // the result of two MFMAs ago
+          f32x4& o = j >= 2 ? acc[i][j - 2] : acc[i == 0 ? MI - 1 : i - 1][j + 2];
+          const float f = j >= 2 ? f0 : s1;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = fmaf(f, d[j & 1][q], o[q]);
+          pin(o);
+          d[j & 1] = mfma_e4m3(bf[j], a, f32x4{0.f, 0.f, 0.f, 0.f});
+          pin(d[j & 1]);
+          if (i + 1 == MI) bf[j] = frag_b(s ^ 1, j);
+          // the freed pieces' copies, spread over the MFMAs
+          if (i == 1) issue_b(s, j * CPB / NJ, (j + 1) * CPB / NJ);
+          if (i == MI / 2 && j < CPA / 2) issue_a(s, j, j + 1);
+          if (i + 1 == MI && j < CPA / 2) issue_a(s, CPA / 2 + j, CPA / 2 + j + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        s1 = f1;
       }
-      s0 = f0;
-      s1 = f1;
+      w0 = n0;
+      w1 = n1;
+      s ^= 1;
+      grp = gn;
     }
-    w0 = n0;
-    w1 = n1;
-    if (last) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          acc[MI - 1][j][q] = fmaf(GATED && j >= NJ / 2 ? s1 : s0, d[j][q], acc[MI - 1][j][q]);
-      // acc[i][j][q]: row r0 + 16i, weight row nh*64 + 16j + 4g + q of the tile
-      const int row0 = entry(r, 1), nb = entry(r, 3);
-      if constexpr (GATED) {
-        // h in place of the gate sums; its largest magnitude per row over the waves' columns
+      for (int q = 0; q < 4; ++q) acc[MI - 1][j + 2][q] = fmaf(s1, d[j][q], acc[MI - 1][j + 2][q]);
+    // acc[i][j][q]: row er + 16i, weight row nh*64 + 16j + 4eg + q of the tile
+    const int el = fresh_lane(), eg = el >> 4, er = mh * RW + (el & 15);
+    if constexpr (GATED) {
+      // h in place of the gate sums; its largest magnitude per row over the waves' columns
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          uint32_t m = 0;
+      for (int i = 0; i < MI; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[i][j][q] = swiglu(acc[i][j][q], acc[i][j + 2][q]);
+            m = umax(m, __float_as_uint(acc[i][j][q]) & 0x7fffffffu);
+          }
+        m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+        m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+        if (eg == 0) lds.row_max[nh][er + i * 16] = __uint_as_float(m);
+      }
+      MOE_LDS_SYNC();
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < WN; ++q) m = umax(m, __float_as_uint(lds.row_max[q][er + i * 16]));
+        const Fp8Scale sc = fp8_block_scale(m);
+        if (er + i * 16 < rows) {
+          const size_t row = (size_t)(row0 + er + i * 16);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              acc[i][j][q] = swiglu(acc[i][j][q], acc[i][j + 2][q]);
-              m = umax(m, __float_as_uint(acc[i][j][q]) & 0x7fffffffu);
-            }
-          m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-          m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-          if (g == 0) lds.row_max[nh][r0 + i * 16] = __uint_as_float(m);
-        }
-        MOE_LDS_SYNC();
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int q = 0; q < WN; ++q) m = umax(m, __float_as_uint(lds.row_max[q][r0 + i * 16]));
-          const Fp8Scale sc = fp8_block_scale(m);
-          if (r0 + i * 16 < rows) {
-            const size_t row = (size_t)(row0 + r0 + i * 16);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<int*>(p.hq + row * p.I + nb * COLS + nh * 32 + j * 16 + 4 * g) =
-                  fp8_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], sc);
-            if (nh == 0 && g == 0) p.hs[row * (p.I / kFp8Block) + nb] = sc.scale;
-          }
-        }
-      } else {
-        const int col0 = nb * BN + nh * (BN / WN) + 4 * g;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          if (r0 + i * 16 >= rows) continue;
-          uint16_t* dst = p.y + (size_t)(row0 + r0 + i * 16) * p.N + col0;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            store4(dst + j * 16, acc[i][j], p.N - col0 - j * 16, p.N % 4 == 0);
+            *reinterpret_cast<int*>(p.hq + row * p.I + nb * COLS + nh * 32 + j * 16 + 4 * eg) =
+                fp8_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], sc);
+          if (nh == 0 && eg == 0) p.hs[row * (p.I / kFp8Block) + nb] = sc.scale;
         }
       }
-      if (rn == mine) break;
-      clear();
-      s0 = s1 = 0.f;
-      rows = entry(rn, 2);
+    } else {
+      const int col0 = nb * BN + nh * (BN / WN) + 4 * eg;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (er + i * 16 >= rows) continue;
+        uint16_t* dst = p.y + (size_t)(row0 + er + i * 16) * p.N + col0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          store4(dst + j * 16, acc[i][j], p.N - col0 - j * 16, p.N % 4 == 0);
+      }
     }
-    r = rn;
-    c = cn;
-    grp = gn;
   }
   MOE_DMA_SYNC(0);  // copies still on their way into this workgroup's LDS
 }
@@ -642,7 +659,11 @@ int launch_tiles(Fp8Args p, hipStream_t s, const char* who) {
   if (mt * p.nnb > ((int64_t)1 << 31) - 1)
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   p.mt = (int)mt;
-  fp8_tile_kernel<BM, BN, WM, WN, GATED><<<(unsigned)(W * kXcds), 64 * WM * WN, 0, s>>>(p);
+  const unsigned grid = (unsigned)(W * kXcds);
+  if (p.K > 3 * kFp8Block)
+    fp8_tile_kernel<BM, BN, WM, WN, GATED, true><<<grid, 64 * WM * WN, 0, s>>>(p);
+  else
+    fp8_tile_kernel<BM, BN, WM, WN, GATED, false><<<grid, 64 * WM * WN, 0, s>>>(p);
   return check_launch(who);
 }
 
