@@ -667,6 +667,233 @@ int launch_tiles(Fp8Args p, hipStream_t s, const char* who) {
   return check_launch(who);
 }
 
+// ---------------------------------------------------------------------------
+// Smaller tiles for products that cannot fill the chip with 256-row ones (few
+// rows per expert, few tiles): BM x BN on WM x WN waves over a ring of stages
+// of one K block each, S - 1 blocks in flight, one barrier per block.  Bound by
+// the bytes it can keep in flight (weights of experts with few rows) or by the
+// blocks' latency (small dense products).
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WN, int S, bool GATED>
+struct RingLds {
+  TileStage<BM, BN> st[S];
+  float sc[S][BM];  // the rows' scales
+  float wsc[2][65536 / kFp8Block];
+  float row_max[GATED ? WN : 1][GATED ? BM : 1];
+};
+
+template <int BM, int BN, int WM, int WN, int S, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_ring_kernel(Fp8Args p) {
+  constexpr int NW = WM * WN, MI = BM / WM / 16, NJ = BN / WN / 16, RW = BM / WM, CW = BN / WN;
+  constexpr int COLS = GATED ? BN / 2 : BN;
+  constexpr int CPA = BM / 8 / NW, CPB = BN / 8 / NW;  // 1 KB copies (8 rows) per wave
+  constexpr int COPIES = CPA + CPB + 1;                // per wave and block
+  static_assert(BM == 64 && (NJ == 4 || !GATED) && S >= 3 && S <= 4, "ring shape");
+  static_assert(!GATED || COLS == kFp8Block, "gate/up: one scale block of h per tile");
+  __shared__ RingLds<BM, BN, WN, S, GATED> lds;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mh = wave / WN, nh = wave % WN;
+  const int K = p.K, kb = (K + kFp8Block - 1) / kFp8Block;
+
+  // Hardware block b runs on XCD b % 8: the tiles are cut into eight contiguous ranges (grouped
+  // products know their number here only; the grid was sized from a bound)
+  RowTile t;
+  int nb;
+  {
+    RowTiles<BM> tiles;
+    const int mt = p.counts ? tiles.load(p.counts, p.offsets, p.E, lane) : p.mt;
+    const int G = mt * p.nnb, per = (G + kXcds - 1) / kXcds;
+    const int i = (int)blockIdx.x / kXcds, v = (int)blockIdx.x % kXcds * per + i;
+    if (i >= per || v >= G) return;  // uniform per block
+    int tile;
+    panel_tile(v, mt, p.nnb, tile, nb);
+    if (p.counts) {
+      t = tiles.at(tile);
+      dbg_segment(t.row0, t.rows, p.M);
+      if (t.rows <= 0) return;
+    } else {
+      t.e = 0;
+      t.row0 = tile * BM;
+      t.rows = min(BM, p.M - t.row0);
+    }
+  }
+  const int row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  const int rows = __builtin_amdgcn_readfirstlane(t.rows);
+  const int e = __builtin_amdgcn_readfirstlane(t.e);
+  const uint8_t* w = slot_base(p.w, p.w_stride, p, e);
+  const float* ws = reinterpret_cast<const float*>(slot_base(p.ws, p.ws_stride, p, e));
+  // rows past the tile read its last one
+  auto source = [&](int lr) -> uint32_t {
+    const int r = min(lr, rows - 1);
+    if (p.row_of) return (uint32_t)(dbg_clamp(p.row_of[row0 + r], p.M, kDbgSorted) / p.k);
+    return (uint32_t)r;
+  };
+  const uint8_t* ab = p.row_of ? p.a : p.a + (size_t)row0 * K;
+  const uint8_t* sb = reinterpret_cast<const uint8_t*>(p.row_of ? p.a_scale
+                                                                : p.a_scale + (size_t)row0 * kb);
+  const uint8_t* wb = GATED ? w : w + (size_t)nb * BN * K;
+  const uint32_t unit = (uint32_t)(lane & 7);
+  uint32_t ao[CPA], wo[CPB];
+#pragma unroll
+  for (int q = 0; q < CPA; ++q) {
+    const int lr = (wave * CPA + q) * 8 + (lane >> 3);
+    ao[q] = source(lr) * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
+  }
+#pragma unroll
+  for (int q = 0; q < CPB; ++q) {
+    const int lr = (wave * CPB + q) * 8 + (lane >> 3);
+    int wr;
+    if constexpr (GATED) {  // a wave's 64 weight rows: 32 gate rows, then their up rows
+      const int col = nb * COLS + (lr >> 6) * 32 + (lr & 31);
+      wr = (lr & 32) ? p.I + col : col;
+    } else {
+      wr = min(lr, p.N - 1 - nb * BN);
+    }
+    wo[q] = (uint32_t)wr * (uint32_t)K + ((unit ^ a_swz(lr)) * 16);
+  }
+  const uint32_t so = source(lane) * (uint32_t)kb * 4u;
+  {  // the tile's weight scales (gate/up: the gate and the up block)
+    const int last = (p.N - 1) / kFp8Block;
+    const int b0 = GATED ? nb : min(nb * BN / kFp8Block, last);
+    const int b1 = GATED ? p.I / kFp8Block + nb : min(nb * BN / kFp8Block + 1, last);
+    for (int i = tid; i < kb; i += 64 * NW) {
+      lds.wsc[0][i] = ws[b0 * kb + i];
+      lds.wsc[1][i] = ws[b1 * kb + i];
+    }
+    __syncthreads();
+  }
+  // a short last block: units past K re-read its first
+  auto back = [&](int lr) -> uint32_t {
+    const uint32_t u = (unit ^ a_swz(lr)) * 16;
+    return u < (uint32_t)(K % kFp8Block) ? 0u : u;
+  };
+  auto issue = [&](int c, int s) {
+    const bool cut = c + 1 == kb && K % kFp8Block != 0;
+    const uint8_t* as = ab + (size_t)c * kFp8Block;
+    const uint8_t* bs = wb + (size_t)c * kFp8Block;
+#pragma unroll
+    for (int q = 0; q < CPB; ++q) {
+      const int n = wave * CPB + q;
+      dma16(bs, cut ? wo[q] - back(n * 8 + (lane >> 3)) : wo[q], lds.st[s].b + n * 1024);
+    }
+#pragma unroll
+    for (int q = 0; q < CPA; ++q) {
+      const int n = wave * CPA + q;
+      dma16(as, cut ? ao[q] - back(n * 8 + (lane >> 3)) : ao[q], lds.st[s].a + n * 1024);
+    }
+    dma4(sb, so + (uint32_t)c * 4u, lds.sc[s]);  // every wave the same 64: equal waits for all
+  };
+
+  const int r0 = mh * RW + l16, rb = nh * CW + l16;
+  const int u0 = ((2 * g) ^ a_swz(l16)) * 16, u1 = ((2 * g + 1) ^ a_swz(l16)) * 16;
+  auto frag = [&](const uint8_t* base, int r) {
+    const i32x4 x = *reinterpret_cast<const i32x4*>(base + r * 128 + u0);
+    const i32x4 y = *reinterpret_cast<const i32x4*>(base + r * 128 + u1);
+    return fp8x32{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
+  const float* wsw = lds.wsc[GATED ? 0 : nh * CW / kFp8Block];
+  f32x4 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < S - 1 && c < kb; ++c) issue(c, c);
+  for (int c = 0, s = 0; c < kb; ++c, s = s + 1 == S ? 0 : s + 1) {
+    // block c has landed, the blocks issued since may be on their way; every wave is done with
+    // block c - 1, whose stage the next copies take
+    const int behind = min(S - 2, kb - 1 - c);
+    if (behind == 2) MOE_DMA_SYNC(2 * COPIES);
+    else if (behind == 1) MOE_DMA_SYNC(COPIES);
+    else MOE_DMA_SYNC(0);
+    if (c + S - 1 < kb) issue(c + S - 1, s == 0 ? S - 1 : s - 1);
+    TileStage<BM, BN>& T = lds.st[s];
+    if (c + 1 == kb && K % kFp8Block) {  // zeros past K in the short last block
+      const int z0 = K % kFp8Block / 16, nz = 8 - z0;
+      for (int i = tid; i < (BM + BN) * nz; i += 64 * NW) {
+        const int r = i / nz, u = z0 + i - r * nz, lr = r < BM ? r : r - BM;
+        *reinterpret_cast<i32x4*>((r < BM ? T.a : T.b) + lr * 128 + ((u ^ a_swz(lr)) * 16)) =
+            i32x4{0, 0, 0, 0};
+      }
+      MOE_LDS_SYNC();
+    }
+    const float w0 = wsw[c], w1 = GATED ? lds.wsc[1][c] : 0.f;
+    fp8x32 bf[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) bf[j] = frag(T.b, rb + j * 16);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const fp8x32 af = frag(T.a, r0 + i * 16);
+      const float sa = lds.sc[s][r0 + i * 16];
+      const float f0 = sa * w0, f1 = GATED ? sa * w1 : f0;
+      f32x4 d[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) d[j] = mfma_e4m3(bf[j], af, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[i][j][q] = fmaf(GATED && j >= NJ / 2 ? f1 : f0, d[j][q], acc[i][j][q]);
+    }
+  }
+  // acc[i][j][q]: row r0 + 16i, weight row nh*CW + 16j + 4g + q of the tile
+  if constexpr (GATED) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc[i][j][q] = swiglu(acc[i][j][q], acc[i][j + 2][q]);
+          m = umax(m, __float_as_uint(acc[i][j][q]) & 0x7fffffffu);
+        }
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+      m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+      if (g == 0) lds.row_max[nh][r0 + i * 16] = __uint_as_float(m);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int q = 0; q < WN; ++q) m = umax(m, __float_as_uint(lds.row_max[q][r0 + i * 16]));
+      const Fp8Scale sc = fp8_block_scale(m);
+      if (r0 + i * 16 < rows) {
+        const size_t row = (size_t)(row0 + r0 + i * 16);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<int*>(p.hq + row * p.I + nb * COLS + nh * 32 + j * 16 + 4 * g) =
+              fp8_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], sc);
+        if (nh == 0 && g == 0) p.hs[row * (p.I / kFp8Block) + nb] = sc.scale;
+      }
+    }
+  } else {
+    const int col0 = nb * BN + nh * CW + 4 * g;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (r0 + i * 16 >= rows) continue;
+      uint16_t* dst = p.y + (size_t)(row0 + r0 + i * 16) * p.N + col0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        store4(dst + j * 16, acc[i][j], p.N - col0 - j * 16, p.N % 4 == 0);
+    }
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int S, bool GATED>
+int launch_ring(Fp8Args p, hipStream_t s, const char* who) {
+  constexpr int COLS = GATED ? BN / 2 : BN;
+  p.nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
+  const int64_t mt = p.counts ? row_tiles_bound(p.M, p.E, BM) : ((int64_t)p.M + BM - 1) / BM;
+  const int64_t blocks = (mt * p.nnb + kXcds - 1) / kXcds * kXcds;
+  if (blocks > ((int64_t)1 << 31) - 1)
+    return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+  p.mt = (int)mt;
+  fp8_ring_kernel<BM, BN, WM, WN, S, GATED><<<(unsigned)blocks, 64 * WM * WN, 0, s>>>(p);
+  return check_launch(who);
+}
+
 template <bool GATED>
 int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
   const int cols = GATED ? 32 : 64;
@@ -676,6 +903,51 @@ int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   fp8_rows16_kernel<GATED><<<(unsigned)(nnb * tiles), 256, 0, s>>>(p);
   return check_launch(who);
+}
+
+// ---------------------------------------------------------------------------
+// Which kernel: by what fills the chip and how often weights are read again (times in us, E4M3
+// weights resident in HBM; R = rows per expert, M / E).
+//  * 16-row tiles read an expert's weights once per 16 rows: up to 4 rows per expert on average,
+//    or 32 rows in all (M = 32, N = 4096, K = 7168: 21.3 against 27.2 on 64 x 64 tiles, M = 128:
+//    38.1 against 27.9; FFN of 512 experts of 4096 x 1024: R = 1 1192 against 1189 on 64 x 256
+//    tiles, R = 16 1754 against 1324; of 64 experts of 2048 x 1024: R = 8 87 against 92).
+//  * 64 x 64 tiles while at most two of them fall on a compute unit (N = 4096, K = 7168: M = 512
+//    36 against 47 on 64 x 256 tiles, M = 777 67 against 48).
+//  * 64 x 256 tiles while at most two of them fall on a compute unit (N = 4096, K = 7168: M = 1024
+//    51 against 95 on 256 x 256 tiles, M = 2048 95 against 96), or for up to 64 rows per expert
+//    (FFN of 64 experts of 2048 x 1024: R = 32 101 against 106, R = 64 113 against 113, R = 96 154
+//    against 117; of 256 experts of 7168 x 2048: R = 64 2359 against 2741, R = 128 3577 against 2723).
+//  * 256 x 256 tiles otherwise (two K blocks at least).
+// The last three address gathered activation rows with 32-bit offsets.
+// ---------------------------------------------------------------------------
+constexpr int64_t kTwoPerCu = 2 * kXcds * kXcdCus;
+
+bool few_rows(int64_t M, int64_t E) { return M <= 4 * E || M <= 32; }
+
+int launch_product(const Fp8Args& p, hipStream_t s, const char* who) {
+  const int64_t M = p.M, E = p.E;
+  const int64_t rt = row_tiles_bound(M, E, 64);
+  if (few_rows(M, E)) return launch_rows16<false>(p, s, who);
+  if (rt * ((p.N + 63) / 64) <= kTwoPerCu) return launch_ring<64, 64, 2, 2, 4, false>(p, s, who);
+  if (rt * ((p.N + 255) / 256) <= kTwoPerCu || M <= 64 * E || p.K <= kFp8Block)
+    return launch_ring<64, 256, 2, 4, 3, false>(p, s, who);
+  return launch_tiles<256, 256, 2, 4, false>(p, s, who);
+}
+
+// gate/up into hq and hs
+int launch_gateup(const Fp8Args& p, bool offsets32, hipStream_t s, const char* who) {
+  const int64_t M = p.M, E = p.E;
+  if (few_rows(M, E) || !offsets32) {
+    const int st = launch_rows16<true>(p, s, who);
+    if (st) return st;
+    launch_quantize<float>(p.h, p.M, p.I, p.hq, p.hs, s);
+    return check_launch(who);
+  }
+  if (row_tiles_bound(M, E, 64) * (p.I / kFp8Block) <= kTwoPerCu || M <= 64 * E ||
+      p.K <= kFp8Block)
+    return launch_ring<64, 256, 2, 4, 3, true>(p, s, who);
+  return launch_tiles<256, 256, 2, 4, true>(p, s, who);
 }
 
 // FFN workspace: xq, its scales, h (fp32), hq, its scales.
@@ -759,9 +1031,7 @@ extern "C" int moe_fp8_matmul(const uint8_t* a, const float* a_scale, int32_t M,
   p.offsets = offsets;
   p.E = E; p.M = M; p.N = N; p.K = K;
   p.y = y;
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (M <= 32 * (int64_t)E || K <= kFp8Block) return launch_rows16<false>(p, s, who);
-  return launch_tiles<256, 256, 2, 4, false>(p, s, who);
+  return launch_product(p, reinterpret_cast<hipStream_t>(stream), who);
 }
 
 extern "C" size_t moe_expert_ffn_fp8_workspace(const moe_experts* W, int32_t T, int32_t k) {
@@ -818,19 +1088,8 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   p.h = reinterpret_cast<float*>(wb + B.h);
   p.hq = wb + B.hq;
   p.hs = reinterpret_cast<float*>(wb + B.hs);
-  // the tile kernel addresses the gathered activation rows with 32-bit offsets and needs two
-  // blocks of K
-  const bool tiles = A > 32 * (int64_t)W->E && (int64_t)T * H < ((int64_t)1 << 32) &&
-                     H > kFp8Block && I > kFp8Block;
-  int st;
-  if (tiles) {
-    st = launch_tiles<256, 256, 2, 4, true>(p, s, who);
-    if (st) return st;
-  } else {
-    st = launch_rows16<true>(p, s, who);
-    if (st) return st;
-    launch_quantize<float>(p.h, (int)A, I, p.hq, p.hs, s);
-  }
+  int st = launch_gateup(p, (int64_t)T * H < ((int64_t)1 << 32), s, who);
+  if (st) return st;
   Fp8Args d = p;
   d.a = wb + B.hq;
   d.a_scale = reinterpret_cast<const float*>(wb + B.hs);
@@ -839,5 +1098,5 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   d.ws = rec + L.w2s;
   d.N = H; d.K = I;
   d.y = y_perm;
-  return tiles ? launch_tiles<256, 256, 2, 4, false>(d, s, who) : launch_rows16<false>(d, s, who);
+  return launch_product(d, s, who);
 }
