@@ -8,6 +8,8 @@
 // lane's four results are consecutive output columns of one activation row,
 // whose scale it holds once, and the weight scale is the same for the whole
 // 16-row subtile.
+#include <type_traits>
+
 #include "fp8_common.h"
 #include "lds_copy.h"
 
@@ -15,12 +17,11 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------------------
-// bf16 / fp32 rows -> E4M3.  A thread holds 8 consecutive columns, 16 lanes
+// bf16 rows -> E4M3.  A thread holds 8 consecutive columns, 16 lanes
 // (one DPP row) a 128-block; short blocks leave lanes without columns.
 // ---------------------------------------------------------------------------
-template <typename SRC>
-__global__ __launch_bounds__(256) void fp8_quantize_kernel(const SRC* __restrict__ x, int T, int K,
-                                                           uint8_t* __restrict__ codes,
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t* __restrict__ x, int T,
+                                                           int K, uint8_t* __restrict__ codes,
                                                            float* __restrict__ scales) {
   const int kb = (K + kFp8Block - 1) / kFp8Block;
   const int64_t n = (int64_t)T * kb * 16;  // 8-column units, rows padded to whole blocks
@@ -31,20 +32,12 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const SRC* __restrict
     const int col = b * kFp8Block + (int)(u & 15) * 8;
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (col < K) {
-      const SRC* p = x + row * K + col;
-      if constexpr (sizeof(SRC) == 2) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint4 v = *reinterpret_cast<const uint4*>(x + row * K + col);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f[2 * q] = __uint_as_float(w[q] << 16);
-          f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
-        }
-      } else {
-        const float4 v0 = reinterpret_cast<const float4*>(p)[0];
-        const float4 v1 = reinterpret_cast<const float4*>(p)[1];
-        f[0] = v0.x; f[1] = v0.y; f[2] = v0.z; f[3] = v0.w;
-        f[4] = v1.x; f[5] = v1.y; f[6] = v1.z; f[7] = v1.w;
+      for (int q = 0; q < 4; ++q) {
+        f[2 * q] = __uint_as_float(w[q] << 16);
+        f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
       }
     }
     uint32_t am = 0;
@@ -64,12 +57,12 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const SRC* __restrict
   }
 }
 
-template <typename SRC>
-void launch_quantize(const SRC* x, int T, int K, uint8_t* codes, float* scales, hipStream_t s) {
+void launch_quantize(const uint16_t* x, int T, int K, uint8_t* codes, float* scales,
+                     hipStream_t s) {
   const int64_t n = (int64_t)T * ((K + kFp8Block - 1) / kFp8Block) * 16;
   const int64_t blocks = (n + 255) / 256;
-  fp8_quantize_kernel<SRC><<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, s>>>(
-      x, T, K, codes, scales);
+  fp8_quantize_kernel<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, s>>>(x, T, K, codes,
+                                                                                  scales);
 }
 
 // ---------------------------------------------------------------------------
@@ -115,13 +108,60 @@ __device__ __forceinline__ void store4(uint16_t* dst, const f32x4& v, int left, 
   }
 }
 
-// Tiles of 16 rows x 64 weight rows; the 4 waves split K (blocks w, w+4, ...)
-// and their sums meet in LDS in wave order.
-template <bool GATED>
-__global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
-  constexpr int NSUB = 4, U = 2, COLS = GATED ? 32 : 64;
-  __shared__ f32x4 red[4][NSUB][64];
-  const int nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
+// Activations of the 16-row kernel: codes with their scales, or rows that it quantises as it
+// reads them (bf16 x, fp32 h), which saves the quantising launch where few rows are read.
+enum { kSrcCodes, kSrcBf16, kSrcF32 };
+
+// A lane's 32 consecutive values [col, col + 32) of a row -> codes, and the scale of the
+// row's 128-block, which the lanes i16, i16 + 16, i16 + 32, i16 + 48 hold together.
+template <typename SRC>
+struct RawRow {
+  i32x4 v[sizeof(SRC) * 2];
+};
+template <typename SRC>
+__device__ __forceinline__ void load_raw(const SRC* row, int col, int K, bool live, RawRow<SRC>& r) {
+  constexpr int N = sizeof(SRC) * 2, PER = 16 / sizeof(SRC);  // 16-byte pieces, values of one
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const i32x4 zero = {0, 0, 0, 0};
+    r.v[q] = live && col + q * PER < K ? *reinterpret_cast<const i32x4*>(row + col + q * PER) : zero;
+  }
+}
+template <typename SRC>
+__device__ __forceinline__ fp8x32 quantize_raw(const RawRow<SRC>& r, float& scale) {
+  auto at = [&](int i) -> float {
+    if constexpr (sizeof(SRC) == 2) {
+      const uint32_t w = (uint32_t)r.v[i / 8][(i % 8) / 2];
+      return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    } else {
+      return __int_as_float(r.v[i / 4][i % 4]);
+    }
+  };
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) am = umax(am, __float_as_uint(at(i)) & 0x7fffffffu);
+  am = umax(am, (uint32_t)__shfl_xor((int)am, 16, 64));
+  am = umax(am, (uint32_t)__shfl_xor((int)am, 32, 64));
+  const Fp8Scale s = fp8_block_scale(am);
+  scale = s.scale;
+  fp8x32 c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = fp8_pack4(at(4 * i), at(4 * i + 1), at(4 * i + 2), at(4 * i + 3), s);
+  return c;
+}
+
+// Tiles of 16 rows, for few rows: bound by the weight bytes, which go from memory straight to
+// registers, U blocks of K in flight per wave.  A wave takes NSUB subtiles of 16 weight rows
+// (gate/up: half gate rows, half their up rows).  SPLIT = NW: the NW waves share the subtiles
+// and split K (blocks w, w + NW, ...), their sums meet in LDS in wave order; SPLIT = 1: each
+// has subtiles of its own over the whole K.
+template <int SRC, bool GATED, int NSUB, int NW, int SPLIT, int U>
+__global__ __launch_bounds__(64 * NW) void fp8_rows16_kernel(Fp8Args p) {
+  constexpr int OUT = GATED ? NSUB / 2 : NSUB;          // output subtiles of a wave
+  constexpr int COLS = OUT * 16 * (SPLIT == 1 ? NW : 1);  // output columns of a workgroup
+  static_assert(SPLIT == 1 || (SPLIT == NW && NW >= OUT), "split");
+  __shared__ f32x4 red[SPLIT == 1 ? 1 : NW][NSUB][64];
+  const int nnb = p.nnb;
   const int tile = (int)blockIdx.x / nnb, nb = (int)blockIdx.x - tile * nnb;
   const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -139,16 +179,13 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
   const int K = p.K, kb = (K + kFp8Block - 1) / kFp8Block;
   const uint8_t* w = slot_base(p.w, p.w_stride, p, t.e);
   const float* ws = reinterpret_cast<const float*>(slot_base(p.ws, p.ws_stride, p, t.e));
-  const int n0 = nb * COLS;
+  const int n0 = nb * COLS + (SPLIT == 1 ? wave * OUT * 16 : 0);
   uint32_t wo[NSUB];
   int so[NSUB];
 #pragma unroll
   for (int j = 0; j < NSUB; ++j) {
-    int base;
-    if constexpr (GATED) base = (j < 2 ? n0 : p.I + n0) + (j & 1) * 16;
-    else base = n0 + j * 16;
-    const int row = min(base + i16, p.N - 1);
-    wo[j] = (uint32_t)row * (uint32_t)K;
+    const int base = GATED ? (j < OUT ? n0 : p.I + n0) + j % OUT * 16 : n0 + j * 16;
+    wo[j] = (uint32_t)min(base + i16, p.N - 1) * (uint32_t)K;
     so[j] = min(base, p.N - 1) / kFp8Block * kb;
   }
   const bool have = i16 < t.rows;
@@ -157,19 +194,20 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
     const int r = t.row0 + i16;
     arow = p.row_of ? (size_t)(dbg_clamp(p.row_of[r], p.M, kDbgSorted) / p.k) : (size_t)r;
   }
-  const uint8_t* ap = p.a + arow * K;
-  const float* asp = p.a_scale + arow * kb;
+  using Raw = std::conditional_t<SRC == kSrcF32, float, uint16_t>;
 
   f32x4 acc[NSUB];
 #pragma unroll
   for (int j = 0; j < NSUB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const i32x4 zero = {0, 0, 0, 0};
-  for (int c0 = wave; c0 < kb; c0 += 4 * U) {
-    i32x4 wf[U][NSUB][2], af[U][2];
+  for (int c0 = SPLIT == 1 ? 0 : wave; c0 < kb; c0 += SPLIT * U) {
+    i32x4 wf[U][NSUB][2];
+    RawRow<uint8_t> af[U];
+    RawRow<Raw> raw[U];
     float sa[U], sw[U][NSUB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + 4 * u;
+      const int c = c0 + SPLIT * u;
       const int col = c * kFp8Block + 32 * g;  // K a multiple of 16: 16-byte units are whole
       const bool ok0 = c < kb && col < K, ok1 = c < kb && col + 16 < K;
 #pragma unroll
@@ -178,14 +216,22 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
         wf[u][j][1] = ok1 ? *reinterpret_cast<const i32x4*>(w + wo[j] + col + 16) : zero;
         sw[u][j] = c < kb ? ws[so[j] + c] : 0.0f;
       }
-      af[u][0] = ok0 && have ? *reinterpret_cast<const i32x4*>(ap + col) : zero;
-      af[u][1] = ok1 && have ? *reinterpret_cast<const i32x4*>(ap + col + 16) : zero;
-      sa[u] = c < kb && have ? asp[c] : 0.0f;
+      if constexpr (SRC == kSrcCodes) {
+        load_raw<uint8_t>(p.a + arow * K, col, K, have && c < kb, af[u]);
+        sa[u] = c < kb && have ? p.a_scale[arow * kb + c] : 0.0f;
+      } else {
+        load_raw<Raw>(reinterpret_cast<const Raw*>(p.a) + arow * K, col, K, have && c < kb, raw[u]);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const fp8x32 b = {af[u][0][0], af[u][0][1], af[u][0][2], af[u][0][3],
-                        af[u][1][0], af[u][1][1], af[u][1][2], af[u][1][3]};
+      fp8x32 b;
+      if constexpr (SRC == kSrcCodes) {
+        const i32x4 x = af[u].v[0], y = af[u].v[1];
+        b = fp8x32{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      } else {
+        b = quantize_raw<Raw>(raw[u], sa[u]);
+      }
 #pragma unroll
       for (int j = 0; j < NSUB; ++j) {
         const i32x4 x = wf[u][j][0], y = wf[u][j][1];
@@ -197,34 +243,38 @@ __global__ __launch_bounds__(256) void fp8_rows16_kernel(Fp8Args p) {
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < NSUB; ++j) red[wave][j][lane] = acc[j];
-  __syncthreads();
-  auto total = [&](int j) {
-    f32x4 v = red[0][j][lane];
-#pragma unroll
-    for (int q = 1; q < 4; ++q) {
-      const f32x4 x = red[q][j][lane];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += x[r];
-    }
-    return v;
-  };
-  if constexpr (GATED) {
-    if (wave < 2) {
-      const f32x4 gv = total(wave), uv = total(wave + 2);
-      const int col = n0 + wave * 16 + 4 * g;
-      if (have && col < p.I)
+  // output subtile j (gate/up: from its gate and up sums) of row i16, columns 4g..4g+3
+  auto put = [&](int j, const f32x4& v, const f32x4& u) {
+    const int col = n0 + j * 16 + 4 * g;
+    if (!have) return;
+    if constexpr (GATED) {
+      if (col < p.I)
         *reinterpret_cast<float4*>(p.h + (size_t)(t.row0 + i16) * p.I + col) =
-            float4{swiglu(gv[0], uv[0]), swiglu(gv[1], uv[1]), swiglu(gv[2], uv[2]),
-                   swiglu(gv[3], uv[3])};
-    }
-  } else {
-    const f32x4 v = total(wave);
-    const int col = n0 + wave * 16 + 4 * g;
-    if (have) {
+            float4{swiglu(v[0], u[0]), swiglu(v[1], u[1]), swiglu(v[2], u[2]), swiglu(v[3], u[3])};
+    } else {
       store4(p.y + (size_t)(t.row0 + i16) * p.N + col, v, p.N - col, p.N % 4 == 0);
     }
+  };
+  if constexpr (SPLIT == 1) {
+#pragma unroll
+    for (int j = 0; j < OUT; ++j) put(j, acc[j], acc[GATED ? j + OUT : j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NSUB; ++j) red[wave][j][lane] = acc[j];
+    __syncthreads();
+    if (wave >= OUT) return;
+    auto total = [&](int j) {
+      f32x4 v = red[0][j][lane];
+#pragma unroll
+      for (int q = 1; q < NW; ++q) {
+        const f32x4 x = red[q][j][lane];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += x[r];
+      }
+      return v;
+    };
+    const f32x4 v = total(wave);
+    put(wave, v, GATED ? total(wave + OUT) : v);
   }
 }
 
@@ -894,15 +944,30 @@ int launch_ring(Fp8Args p, hipStream_t s, const char* who) {
   return check_launch(who);
 }
 
-template <bool GATED>
-int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
-  const int cols = GATED ? 32 : 64;
-  const int64_t nnb = ((GATED ? p.I : p.N) + cols - 1) / cols;
-  const int64_t tiles = p.counts ? row_tiles_bound(p.M, p.E, 16) : ((int64_t)p.M + 15) / 16;
-  if (nnb * tiles > ((int64_t)1 << 31) - 1)
+template <int SRC, bool GATED, int NSUB, int NW, int SPLIT, int U>
+int launch_rows16_as(Fp8Args p, int64_t tiles, hipStream_t s, const char* who) {
+  const int cols = (GATED ? NSUB / 2 : NSUB) * 16 * (SPLIT == 1 ? NW : 1);
+  p.nnb = ((GATED ? p.I : p.N) + cols - 1) / cols;
+  if (p.nnb * tiles > ((int64_t)1 << 31) - 1)
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-  fp8_rows16_kernel<GATED><<<(unsigned)(nnb * tiles), 256, 0, s>>>(p);
+  fp8_rows16_kernel<SRC, GATED, NSUB, NW, SPLIT, U>
+      <<<(unsigned)(p.nnb * tiles), 64 * NW, 0, s>>>(p);
   return check_launch(who);
+}
+
+// FFN of 8 tokens, 256 experts of 2048 x 512: 46.8 us with one block of K in flight per wave, 49.5
+// with two, 54.4 with four (registers); the down product's K of 4 blocks split over the waves 55.7.
+// Fewer than two workgroups per compute unit take single subtiles and 8 waves along K
+// (1 x 7168 x 2048: 5.9 against 8.0 us).
+template <int SRC, bool GATED>
+int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
+  const int64_t tiles = p.counts ? row_tiles_bound(p.M, p.E, 16) : ((int64_t)p.M + 15) / 16;
+  const int kb = (p.K + kFp8Block - 1) / kFp8Block;
+  const int wide = GATED ? 32 : 64, n = GATED ? p.I : p.N;
+  if (tiles * ((n + wide - 1) / wide) < 2 * kXcds * kXcdCus)
+    return launch_rows16_as<SRC, GATED, GATED ? 2 : 1, 8, 8, 2>(p, tiles, s, who);
+  if (kb <= 8) return launch_rows16_as<SRC, GATED, 4, 4, 1, 1>(p, tiles, s, who);
+  return launch_rows16_as<SRC, GATED, 4, 4, 4, 1>(p, tiles, s, who);
 }
 
 // ---------------------------------------------------------------------------
@@ -928,42 +993,38 @@ bool few_rows(int64_t M, int64_t E) { return M <= 4 * E || M <= 32; }
 int launch_product(const Fp8Args& p, hipStream_t s, const char* who) {
   const int64_t M = p.M, E = p.E;
   const int64_t rt = row_tiles_bound(M, E, 64);
-  if (few_rows(M, E)) return launch_rows16<false>(p, s, who);
+  if (few_rows(M, E)) return launch_rows16<kSrcCodes, false>(p, s, who);
   if (rt * ((p.N + 63) / 64) <= kTwoPerCu) return launch_ring<64, 64, 2, 2, 4, false>(p, s, who);
   if (rt * ((p.N + 255) / 256) <= kTwoPerCu || M <= 64 * E || p.K <= kFp8Block)
     return launch_ring<64, 256, 2, 4, 3, false>(p, s, who);
   return launch_tiles<256, 256, 2, 4, false>(p, s, who);
 }
 
-// gate/up into hq and hs
-int launch_gateup(const Fp8Args& p, bool offsets32, hipStream_t s, const char* who) {
+// gate/up into hq and hs, from rows that fit 32-bit offsets
+int launch_gateup(const Fp8Args& p, hipStream_t s, const char* who) {
   const int64_t M = p.M, E = p.E;
-  if (few_rows(M, E) || !offsets32) {
-    const int st = launch_rows16<true>(p, s, who);
-    if (st) return st;
-    launch_quantize<float>(p.h, p.M, p.I, p.hq, p.hs, s);
-    return check_launch(who);
-  }
   if (row_tiles_bound(M, E, 64) * (p.I / kFp8Block) <= kTwoPerCu || M <= 64 * E ||
       p.K <= kFp8Block)
     return launch_ring<64, 256, 2, 4, 3, true>(p, s, who);
   return launch_tiles<256, 256, 2, 4, true>(p, s, who);
 }
 
-// FFN workspace: xq, its scales, h (fp32), hq, its scales.
+// FFN workspace: h (fp32) on the 16-row path; xq, its scales, hq and its scales on the others.
+// The size covers both.
 struct Fp8FfnWs {
-  size_t xq, xs, h, hq, hs, total;
+  size_t h, xq, xs, hq, hs, total;
 };
 Fp8FfnWs fp8_ffn_ws(int64_t T, int64_t k, int64_t H, int64_t I) {
   auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
   const int64_t A = T * k;
   Fp8FfnWs w;
+  w.h = 0;
   w.xq = 0;
   w.xs = w.xq + up(T * H);
-  w.h = w.xs + up(T * (H / kFp8Block) * 4);
-  w.hq = w.h + up(A * I * 4);
+  w.hq = w.xs + up(T * (H / kFp8Block) * 4);
   w.hs = w.hq + up(A * I);
-  w.total = w.hs + up(A * (I / kFp8Block) * 4) + 256;
+  w.total = w.hs + up(A * (I / kFp8Block) * 4);
+  if (w.total < up(A * I * 4)) w.total = up(A * I * 4);
   return w;
 }
 
@@ -987,7 +1048,7 @@ extern "C" int moe_fp8_quantize(const uint16_t* x, int32_t T, int32_t K, uint8_t
   if (!x || !codes || !scales) return set_error(MOE_ERR_INVALID_ARG, "%s: null pointer", who);
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
     return set_error(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
-  launch_quantize<uint16_t>(x, T, K, codes, scales, reinterpret_cast<hipStream_t>(stream));
+  launch_quantize(x, T, K, codes, scales, reinterpret_cast<hipStream_t>(stream));
   return check_launch(who);
 }
 
@@ -1072,10 +1133,7 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   uint8_t* wb = static_cast<uint8_t*>(ws);
   const uint8_t* rec = static_cast<const uint8_t*>(W->base);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  launch_quantize<uint16_t>(x, T, H, wb + B.xq, reinterpret_cast<float*>(wb + B.xs), s);
   Fp8Args p{};
-  p.a = wb + B.xq;
-  p.a_scale = reinterpret_cast<const float*>(wb + B.xs);
   p.row_of = sorted_idx;
   p.k = k;
   p.w = rec + L.w13;
@@ -1085,18 +1143,29 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   p.counts = counts;
   p.offsets = offsets;
   p.E = W->E; p.M = (int)A; p.N = 2 * I; p.K = H; p.I = I;
-  p.h = reinterpret_cast<float*>(wb + B.h);
-  p.hq = wb + B.hq;
-  p.hs = reinterpret_cast<float*>(wb + B.hs);
-  int st = launch_gateup(p, (int64_t)T * H < ((int64_t)1 << 32), s, who);
-  if (st) return st;
-  Fp8Args d = p;
-  d.a = wb + B.hq;
-  d.a_scale = reinterpret_cast<const float*>(wb + B.hs);
+  Fp8Args d = p;  // down
   d.row_of = nullptr;
   d.w = rec + L.w2;
   d.ws = rec + L.w2s;
   d.N = H; d.K = I;
   d.y = y_perm;
+  if (few_rows(A, W->E) || (int64_t)T * H >= ((int64_t)1 << 32)) {
+    // two launches, which quantise x and h as they read them
+    p.a = reinterpret_cast<const uint8_t*>(x);
+    p.h = reinterpret_cast<float*>(wb + B.h);
+    const int st = launch_rows16<kSrcBf16, true>(p, s, who);
+    if (st) return st;
+    d.a = wb + B.h;
+    return launch_rows16<kSrcF32, false>(d, s, who);
+  }
+  launch_quantize(x, T, H, wb + B.xq, reinterpret_cast<float*>(wb + B.xs), s);
+  p.a = wb + B.xq;
+  p.a_scale = reinterpret_cast<const float*>(wb + B.xs);
+  p.hq = wb + B.hq;
+  p.hs = reinterpret_cast<float*>(wb + B.hs);
+  const int st = launch_gateup(p, s, who);
+  if (st) return st;
+  d.a = p.hq;
+  d.a_scale = p.hs;
   return launch_product(d, s, who);
 }
