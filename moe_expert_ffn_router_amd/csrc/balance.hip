@@ -79,6 +79,17 @@ __device__ __forceinline__ int first_seq(const int* seq, int S, int t, int lane)
   return lo;
 }
 
+// The same by one lane alone.
+__device__ __forceinline__ int seq_of_row(const int* seq, int S, int t) {
+  int a = 0, b = seq ? S : 0;
+  while (a < b) {
+    const int m = (a + b) >> 1;
+    if (seq[m + 1] > t) b = m;
+    else a = m + 1;
+  }
+  return a;
+}
+
 // Maximum and sum over the LPR lanes of a group, in every lane of it.
 template <int LPR>
 __device__ __forceinline__ float group_max(float x) {
@@ -171,6 +182,7 @@ __device__ __forceinline__ void row_softmax(float (&x)[VPL]) {
 }
 
 constexpr int kMaxChunk = 128;  // rows of a chunk at most
+constexpr int kOneKernelSeqs = 256;  // sequences that one workgroup writes out by itself
 
 // U rows of a group, NG rows apart from row t on: loads in flight together, with the rows'
 // mask bytes beside them (a masked row is read and dropped: waiting for its mask first
@@ -317,6 +329,10 @@ __global__ __launch_bounds__(64 * NW) void balance_partial_kernel(BalArgs a) {
     int lo, hi;
     seq_rows(a.seq, s, a.T, lo, hi);
     if (!FINAL && lo >= t1) break;
+    if (!FINAL && lo == hi) {  // a run of empty sequences: on to the one that holds row lo
+      s = max(s, first_seq(a.seq, a.S, lo, lane) - 1);
+      continue;
+    }
     lo = max(lo, t0);
     hi = min(hi, t1);
     if (FINAL || hi > lo) {
@@ -466,8 +482,11 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs a) {
       w = a.w[o];
       wd = a.dw[o];
     }
-    // the row's sequence (per group; every lane of the group agrees)
-    while (s_next < a.S && t >= hi) {
+    // the row's sequence (per group; every lane of the group agrees): the next one, or, behind
+    // empty ones, the one that a search finds
+    for (int step = 0; s_next < a.S && t >= hi; ++step) {
+      if (step == 1) s_next = max(s_next, seq_of_row(a.seq, a.S, t));
+      if (s_next >= a.S) break;
       s = s_next++;
       seq_rows(a.seq, s, a.T, lo, hi);
       if (t < hi && a.d_loss) {
@@ -650,7 +669,7 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, in
   a.probs = probs;
   a.loss = loss;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (T <= kMaxChunk) {  // one chunk: finished by the first kernel
+  if (T <= kMaxChunk && S <= kOneKernelSeqs) {  // one chunk: finished by the first kernel
     with_row_shape(E, [&](auto r) {
       using Q = decltype(r);
       balance_partial_kernel<16, Q::lpr, Q::vpl, Q::vec, true><<<1, 1024, 0, s>>>(a);

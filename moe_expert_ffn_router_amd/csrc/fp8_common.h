@@ -77,11 +77,11 @@ struct RowTile {
 };
 template <int BM>
 struct RowTiles {
-  int n[kMaxE / 64], o[kMaxE / 64], first, mine, upto;
+  int n[kMaxE / 64], o[kMaxE / 64], per, first, mine, upto;
 
   __device__ __forceinline__ int load(const int* __restrict__ counts,
                                       const int* __restrict__ offsets, int E, int lane) {
-    const int per = (E + 63) >> 6;  // at most 16
+    per = (E + 63) >> 6;  // at most 16
     first = lane * per;
 #pragma unroll
     for (int i = 0; i < kMaxE / 64; ++i) {

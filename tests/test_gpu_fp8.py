@@ -446,3 +446,115 @@ def test_expert_ffn_fp8_masked_rows_zero_and_nan():
     inv = c.layer.inv_idx[:c.T * c.k].cpu().numpy().reshape(c.T, c.k)
     assert np.all(y[inv[3]] == 0) and np.all(np.isnan(y[inv[7]]))
     assert np.all(np.isfinite(np.delete(y, inv[7], 0)))
+
+
+# ---- every kernel the size rules choose ------------------------------------
+def _check_all_rows(p, sample):
+    """Every output against the product in float64 on the device, within a bound that only a
+    misplaced, dropped or doubled term can pass; the sampled rows against the oracle's bound.
+
+    The crude bound: with at most one subnormal operand the product of the binades is at most 8
+    times the product itself, so a group's largest (mfma_cut's `top`) is at most 8 times the
+    group's magnitude sum; a pair of two subnormals has 2^-12, no more than any pair of normal
+    codes beside it.  Summed over the groups: 7 * 2^-13 * 8 mag."""
+    kb = -(-p.K // 128)
+    A = p.d[0].view(torch.float8_e4m3fn).double() * p.d[1].double().repeat_interleave(128, 1)[:, :p.K]
+    w, sw = p.d[2].view(torch.float8_e4m3fn), p.d[3].double()
+    segs = [(0, p.M, 0)] if not p.E else [(int(p.offsets[e]), int(p.offsets[e] + p.counts[e]), e)
+                                         for e in range(p.E) if p.counts[e]]
+    seen = torch.zeros(p.M, dtype=torch.bool, device=DEV)
+    for lo, hi, e in segs:
+        we, se = (w[e], sw[e]) if p.E else (w, sw)
+        W = we.double() * se.repeat_interleave(128, 0)[:p.N].repeat_interleave(128, 1)[:, :p.K]
+        y, mag = A[lo:hi] @ W.t(), A[lo:hi].abs() @ W.t().abs()
+        err = (p.y[lo:hi].double() - y).abs()
+        tol = 2.0 ** -8 * y.abs() + (7 * 2.0 ** -13 * 8 + (256 + kb + 20) * EPS) * mag
+        assert bool((err <= tol).all()), (e, torch.nonzero(err > tol)[:4].tolist())
+        seen[lo:hi] = True
+    assert bool((p.y[~seen] == MARK).all())
+    got = p.y.double().cpu().numpy()
+    for lo, hi, e in segs:
+        rows = [r for r in sample if lo <= r < hi]
+        if rows:
+            we, se = (p.w[e], p.sw[e]) if p.E else (p.w, p.sw)
+            y, mag = O8.matmul(p.a[rows], p.sa[rows], we, se)
+            tol = (2.0 ** -8 * np.abs(y) + (1 + 2.0 ** -8) *
+                   ((256 + kb + 20) * EPS * mag + O8.mfma_cut(p.a[rows], p.sa[rows], we, se)))
+            assert np.all(np.abs(got[rows] - y) <= tol)
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1100, 2500, 128), (1100, 2500, 272), (1100, 2500, 1040),              # 64 x 256 tiles
+    (8200, 2300, 144), (8200, 2300, 272), (8200, 2300, 384), (8200, 2300, 400),
+    (8200, 2300, 640), (8200, 2300, 1040), (16400, 2050, 512),             # 256 x 256, several a unit
+    (33, 65536, 16), (40, 48, 65536), (3, 33, 65536)])
+def test_matmul_tiles(M, N, K):
+    flush(f"[matmul tiles] M={M} N={N} K={K}")
+    p = Product(M, N, K, seed=M + K).upload()
+    p.call()
+    torch.cuda.synchronize()
+    _check_all_rows(p, sorted({0, M // 2, M - 1, min(M - 1, 8192)}))
+    ref = p.y.clone()
+    for s in (None, torch.cuda.Stream()):                                  # the same bits again
+        p.y.fill_(MARK)
+        torch.cuda.synchronize()
+        p.call(s)
+        torch.cuda.synchronize()
+        assert torch.equal(p.y, ref)
+
+
+@pytest.mark.parametrize("E,counts,N,K,tail", [
+    (6, [2000, 1, 0, 129, 128, 900], 1500, 640, 5), (3, [0, 4097, 30], 2048, 400, 0),
+    (16, [700, 3, 255, 256, 257, 0, 1500, 128, 129, 64, 65, 900, 1, 0, 511, 513], 1000, 272, 11),
+    (40, [60 + 7 * i for i in range(40)], 600, 512, 3), (9, [40, 64, 65, 0, 1, 128, 80, 70, 33], 3200, 1040, 2),
+    (300, [i % 23 for i in range(300)], 512, 256, 0), (300, [(i * 7) % 90 for i in range(300)], 700, 144, 1)])
+def test_matmul_grouped_tiles(E, counts, N, K, tail):
+    M = sum(counts) + tail
+    flush(f"[matmul tiles] grouped E={E} M={M} N={N} K={K}")
+    p = Product(M, N, K, E, counts, seed=E + K).upload()
+    p.call()
+    torch.cuda.synchronize()
+    off = p.offsets
+    _check_all_rows(p, sorted({int(r) for e in range(0, E, max(1, E // 6))
+                               for r in (off[e], off[e + 1] - 1) if 0 <= r < M - tail}))
+
+
+@pytest.mark.parametrize("T,H,I,E,k,zipf", [(4100, 256, 512, 4, 2, None), (2100, 384, 640, 5, 4, 1.0),
+                                            (4096, 512, 384, 8, 4, 1.4)])
+def test_expert_ffn_fp8_tiles(T, H, I, E, k, zipf):
+    """The 256-row gate/up tiles: sampled tokens' rows against the definition."""
+    flush(f"[ffn fp8 tiles] T={T} H={H} I={I} E={E} k={k}")
+    c = Layer(T, H, I, E, k, seed=T + I, zipf=zipf)
+    y = c.run()
+    ids, _ = OR.route(c.logits_np, k)
+    _, off, srt, _ = OP.permute(ids, E)
+    got = y[:T * k].double().cpu().numpy()
+    assert np.all(np.isfinite(got))
+    for e in range(E):                       # each expert's first, last and a few other rows
+        lo, hi = int(off[e]), int(off[e + 1])
+        if hi <= lo:
+            continue
+        rows = sorted({lo, hi - 1, (lo + hi) // 2, min(hi - 1, lo + 255), min(hi - 1, lo + 256),
+                       max(lo, hi - 130)})
+        sub = np.concatenate([[0] * (e + 1), [len(rows)] * (E - e)])
+        yy, tol = _ffn_reference(c.xv, k, sub, np.asarray(srt)[rows], lambda q: c._parts[q], H, I)
+        assert np.all(np.abs(got[rows] - yy) <= tol), e
+
+
+def test_two_products_at_once():
+    """Two products on two streams at the same time: each with the bits it has alone."""
+    ps = [Product(M, 2300, 640, seed=M).upload() for M in (8200, 7000)]
+    refs = []
+    for p in ps:
+        p.call()
+        torch.cuda.synchronize()
+        refs.append(p.y.clone())
+        p.y.fill_(MARK)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for p, s in zip(ps, streams):
+            p.call(s)
+    torch.cuda.synchronize()
+    for p, r in zip(ps, refs):
+        assert torch.equal(p.y, r)

@@ -309,3 +309,37 @@ def test_binding_refusals():
         moe.moe_balance_loss(*args, token_mask=d["lg"], seq_offsets=d["seq"])
     with pytest.raises(moe.MoeError):
         moe.moe_balance_loss(*args[:7], b.ws[:16], seq_offsets=d["seq"])
+
+
+@pytest.mark.parametrize("T,E,S", [(100, 16, 3000), (100, 300, 257), (5000, 16, 70000), (300, 100, 5000)])
+def test_many_empty_sequences(T, E, S):
+    """Far more sequences than rows: runs of empty ones are searched past, not walked."""
+    rng = np.random.default_rng(T + S)
+    seq = np.sort(rng.integers(0, T + 1, S + 1)).astype(np.int32)
+    seq[S // 3:S // 3 + S // 4] = seq[S // 3]          # one long run of empty sequences
+    seq = np.sort(seq)
+    b = Batch(T, E, 3, None, True, seed=S)
+    b.seq, b.S = seq, S
+    b.dl = rng.normal(size=S).astype(np.float32)
+    b.run()
+
+
+def test_largest_row_and_k():
+    b = Batch(400, 1024, 16, [0, 399], seed=21)
+    b.lg[7] = 0.0                                       # every expert equal
+    b.run()
+
+
+def test_two_calls_at_once():
+    """Two batches on two streams, each with its workspace: the results of each alone."""
+    bs = [Batch(T, 200, 4, [0, T // 3, T], True, seed=T).upload() for T in (3000, 2500)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for b, s in zip(bs, streams):
+            b.forward(s)
+            b.backward(s)
+    torch.cuda.synchronize()
+    for b in bs:
+        b.check_forward()
+        b.check_backward()
