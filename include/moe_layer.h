@@ -370,10 +370,12 @@ int moe_fp8_matmul(const uint8_t* a, const float* a_scale, int32_t M, const uint
                    moe_stream_t stream);
 
 /* moe_expert_ffn_fp8 — moe_expert_ffn over MOE_W_FP8_B128 records with both
- * operands of both products in E4M3 (half the MFMA work of moe_expert_ffn's
- * FP8 path, which keeps the bf16 activations to 2^-17 by splitting them in
- * two; here they carry E4M3's 4 significant bits):
- *   xq   = moe_fp8_quantize(x);   g, u = the rows' products with W13 (fp32)
+ * operands of both products in E4M3 (moe_expert_ffn's FP8 path keeps the bf16
+ * activations to 2^-17 by splitting them in two; here they carry E4M3's 4
+ * significant bits, and one product does):
+ *   xq   = moe_fp8_quantize(x);   g, u = the rows' products with W13, in fp32,
+ *          summed as in moe_fp8_matmul; where few tiles fall on a compute unit
+ *          without its cut, which would show there
  *   hq   = moe_fp8_quantize's rule applied to fp32 h = SiLU(g) * u
  *   y_perm = bf16(hq W2^T)
  * Arguments as for moe_expert_ffn (W->fmt must be MOE_W_FP8_B128, others

@@ -232,11 +232,15 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows16_kernel(Fp8Args p) {
       } else {
         b = quantize_raw<Raw>(raw[u], sa[u]);
       }
+      Decoded bd;
+      if constexpr (GATED) bd = decode_e4m3(b);
 #pragma unroll
       for (int j = 0; j < NSUB; ++j) {
         const i32x4 x = wf[u][j][0], y = wf[u][j][1];
         const fp8x32 a = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        const f32x4 d = mfma_e4m3(a, b, f32x4{0.f, 0.f, 0.f, 0.f});
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (GATED) d = mfma_decoded(decode_e4m3(a), bd, d);
+        else d = mfma_e4m3(a, b, d);
         const float s = sa[u] * sw[u][j];
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(s, d[r], acc[j][r]);
@@ -782,7 +786,9 @@ int launch_tiles(Fp8Args p, hipStream_t s, const char* who) {
 // rows per expert, few tiles): BM x BN on WM x WN waves over a ring of stages
 // of one K block each, S - 1 blocks in flight, one barrier per block.  Bound by
 // the bytes it can keep in flight (weights of experts with few rows) or by the
-// blocks' latency (small dense products).
+// blocks' latency (small dense products).  Gate/up: on the bf16 MFMA, as few values of h share
+// the cost of a rounding that moved (FFN of 64 experts of 2048 x 1024, 16 rows each: 105 us, on
+// the E4M3 MFMA 99).
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int WN, int S, bool GATED>
 struct RingLds {
@@ -928,17 +934,26 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_ring_kernel(Fp8Args p) {
       MOE_LDS_SYNC();
     }
     const float w0 = wsw[c], w1 = GATED ? lds.wsc[1][c] : 0.f;
-    fp8x32 bf[NJ];
+    using Frag = std::conditional_t<GATED, Decoded, fp8x32>;
+    auto operand = [&](const uint8_t* base, int r) -> Frag {
+      if constexpr (GATED) return decode_e4m3(frag(base, r));
+      else return frag(base, r);
+    };
+    Frag bf[NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) bf[j] = frag(T.b, rb + j * 16);
+    for (int j = 0; j < NJ; ++j) bf[j] = operand(T.b, rb + j * 16);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const fp8x32 af = frag(T.a, r0 + i * 16);
+      const Frag af = operand(T.a, r0 + i * 16);
       const float sa = lds.sc[s][r0 + i * 16];
       const float f0 = sa * w0, f1 = GATED ? sa * w1 : f0;
       f32x4 d[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) d[j] = mfma_e4m3(bf[j], af, f32x4{0.f, 0.f, 0.f, 0.f});
+      for (int j = 0; j < NJ; ++j) {
+        d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (GATED) d[j] = mfma_decoded(bf[j], af, d[j]);
+        else d[j] = mfma_e4m3(bf[j], af, d[j]);
+      }
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -1037,16 +1052,25 @@ int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
 //    or 32 rows in all (M = 32, N = 4096, K = 7168: 21.3 against 27.2 on 64 x 64 tiles, M = 128:
 //    38.1 against 27.9; FFN of 512 experts of 4096 x 1024: R = 1 1192 against 1189 on 64 x 256
 //    tiles, R = 16 1754 against 1324; of 64 experts of 2048 x 1024: R = 8 87 against 92).
+// Products of codes:
 //  * 64 x 64 tiles while at most two of them fall on a compute unit (N = 4096, K = 7168: M = 512
 //    36 against 47 on 64 x 256 tiles, M = 777 67 against 48).
 //  * 64 x 256 tiles while at most two of them fall on a compute unit (N = 4096, K = 7168: M = 1024
 //    51 against 95 on 256 x 256 tiles, M = 2048 95 against 96), or for up to 64 rows per expert
-//    (FFN of 64 experts of 2048 x 1024: R = 32 101 against 106, R = 64 113 against 113, R = 96 154
-//    against 117; of 256 experts of 7168 x 2048: R = 64 2359 against 2741, R = 128 3577 against 2723).
+//    (both products of 64 experts of 2048 x 1024: R = 32 101 against 106, R = 64 113 against 113,
+//    R = 96 154 against 117; of 256 experts of 7168 x 2048: R = 64 2359 against 2741, R = 128 3577
+//    against 2723).
 //  * 256 x 256 tiles otherwise (two K blocks at least).
-// The last three address gathered activation rows with 32-bit offsets.
+// Gate/up products, whose 64 x 256 tiles run on the bf16 MFMA (FFN times):
+//  * 64 x 256 tiles while at most one of them falls on a compute unit where the rows spread evenly
+//    over the experts (8 experts of 4096 x 1024: R = 256 86 against 98, R = 400 132 against 101;
+//    32 of 2048 x 768: R = 64 47 against 50, R = 128 77 against 57), or two for up to 32 rows per
+//    expert (64 of 2048 x 1024: R = 32 111 against 122, R = 48 117 against 115).
+//  * 256 x 256 tiles otherwise (512 experts of 4096 x 1024: R = 16 1345 against 1421, R = 64 1558
+//    against 1759; 256 of 7168 x 2048: R = 16 2173 against 2184, R = 64 2406 against 2520).
+// All but the 16-row tiles address gathered activation rows with 32-bit offsets.
 // ---------------------------------------------------------------------------
-constexpr int64_t kTwoPerCu = 2 * kXcds * kXcdCus;
+constexpr int64_t kCus = kXcds * kXcdCus, kTwoPerCu = 2 * kCus;
 
 bool few_rows(int64_t M, int64_t E) { return M <= 4 * E || M <= 32; }
 
@@ -1063,8 +1087,8 @@ int launch_product(const Fp8Args& p, hipStream_t s, const char* who) {
 // gate/up into hq and hs, from rows that fit 32-bit offsets
 int launch_gateup(const Fp8Args& p, hipStream_t s, const char* who) {
   const int64_t M = p.M, E = p.E;
-  if (row_tiles_bound(M, E, 64) * (p.I / kFp8Block) <= kTwoPerCu || M <= 64 * E ||
-      p.K <= kFp8Block)
+  const int64_t tiles = (M < E ? M : E) * ((M + 64 * E - 1) / (64 * E)) * (p.I / kFp8Block);
+  if (tiles <= (M <= 32 * E ? kTwoPerCu : kCus) || p.K <= kFp8Block)
     return launch_ring<64, 256, 2, 4, 3, true>(p, s, who);
   return launch_tiles<256, 256, 2, 4, true>(p, s, who);
 }

@@ -342,7 +342,7 @@ def _ffn_reference(x, k, offsets, sorted_idx, parts, H, I):
 class Layer:
     """A layer of FP8 records (narrow gate/up codes, any down codes), its batch and helper."""
 
-    def __init__(self, T, H, I, E, k, seed, zipf=None, T_max=None):
+    def __init__(self, T, H, I, E, k, seed, zipf=None, T_max=None, wide=False):
         rng = np.random.default_rng(seed)
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         wl = synth.Workload(f"fp8_{seed}", T=T, H=H, E=E, I=I, k=k, fmt="fp8_b128", seed=seed,
@@ -350,12 +350,13 @@ class Layer:
         self.wl = wl
         self.logits_np = synth.make_logits(wl)
         self.logits = torch.from_numpy(self.logits_np).to(DEV)
-        self.x, self.xv = _bf16(_narrow(rng, (T, H)))
+        self.x, self.xv = _bf16(rng.normal(size=(T, H)) if wide else _narrow(rng, (T, H)))
         lay = synth.record_layout("fp8_b128", H, I)
         rec = np.zeros((E, lay["stride"]), np.uint8)
         self._parts = []
         for e in range(E):
-            c13 = (torch.from_numpy(_narrow(rng, (2 * I, H))).to(torch.float8_e4m3fn)
+            v13 = np.clip(rng.normal(size=(2 * I, H)) * 40, -448, 448) / 8
+            c13 = (torch.from_numpy(v13 if wide else _narrow(rng, (2 * I, H))).to(torch.float8_e4m3fn)
                    .view(torch.uint8).numpy())
             c2 = _codes(rng, (H, I))
             s13 = (0.02 * (0.5 + rng.random((2 * I // 128, H // 128))) / np.sqrt(H)).astype(np.float32)
@@ -391,6 +392,18 @@ class Layer:
 def test_expert_ffn_fp8(T, H, I, E, k, zipf):
     flush(f"[ffn fp8] T={T} H={H} I={I} E={E} k={k}")
     c = Layer(T, H, I, E, k, seed=T + H + I, zipf=zipf)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("T,H,I,E,k,zipf", [
+    (1, 512, 128, 4, 2, None), (8, 2048, 512, 64, 8, None),      # 16-row tiles
+    (40, 512, 384, 8, 2, 1.2), (90, 2048, 256, 6, 4, None)])     # 64 x 256 tiles
+def test_expert_ffn_fp8_of_few_rows_keeps_every_product(T, H, I, E, k, zipf):
+    """Ordinary values, whose products span more than the E4M3 MFMA keeps: few rows take their
+    gate/up products exactly, with the tolerance of fp32 additions."""
+    flush(f"[ffn fp8, wide] T={T} H={H} I={I} E={E} k={k}")
+    c = Layer(T, H, I, E, k, seed=T + H + I + 1, zipf=zipf, wide=True)
     c.run()
     c.check()
 
