@@ -994,14 +994,29 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_ring_kernel(Fp8Args p) {
       }
     }
   } else {
-    const int col0 = nb * BN + nh * CW + 4 * g;
+    const int col0 = nh * CW + 4 * g, left = p.N - nb * BN;
+    uint16_t* dst = p.y + (size_t)row0 * p.N + nb * BN;
+    if (p.N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      if (r0 + i * 16 >= rows) continue;
-      uint16_t* dst = p.y + (size_t)(row0 + r0 + i * 16) * p.N + col0;
+      for (int i = 0; i < MI; ++i) {
+        if (r0 + i * 16 >= rows) continue;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        store4(dst + j * 16, acc[i][j], p.N - col0 - j * 16, p.N % 4 == 0);
+        for (int j = 0; j < NJ; ++j)
+          store4(dst + (size_t)(r0 + i * 16) * p.N + col0 + j * 16, acc[i][j], left - col0 - j * 16,
+                 true);
+      }
+    } else {  // rows that are not aligned: through LDS, so that a wave writes whole rows
+      uint16_t(*out)[BN + 8] = reinterpret_cast<uint16_t(*)[BN + 8]>(lds.st);
+      static_assert(sizeof(lds.st) >= BM * sizeof(out[0]), "output tile");
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          store4(&out[r0 + i * 16][col0 + j * 16], acc[i][j], 4, true);
+      __syncthreads();
+      for (int r = wave; r < rows; r += NW)
+        for (int c = lane; c < min(BN, left); c += 64) dst[(size_t)r * p.N + c] = out[r][c];
     }
   }
 }
@@ -1016,6 +1031,164 @@ int launch_ring(Fp8Args p, hipStream_t s, const char* who) {
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   p.mt = (int)mt;
   fp8_ring_kernel<BM, BN, WM, WN, S, GATED><<<(unsigned)blocks, 64 * WM * WN, 0, s>>>(p);
+  return check_launch(who);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of 16 MI rows x 16 NJ weight rows for products of a few dozen rows: the NW waves of a
+// workgroup split K (blocks w, w + NW, ...), operands go from memory straight to registers, one
+// block ahead, and the waves' sums of the whole tile meet in LDS in wave order.  Bound by what
+// a compute unit takes in, 31 bytes per ns whatever is in flight (two to four blocks ahead or 16
+// waves change nothing): so the smallest tile that still needs no second round of workgroups
+// (M = 64, N = 4096, K = 7168: 18.1 us on 32 x 32 tiles, 24.7 on 32 x 64, 54 on 64 x 64).
+// ---------------------------------------------------------------------------
+template <int MI, int NJ, int NW>
+__global__ __launch_bounds__(64 * NW) void fp8_split_kernel(Fp8Args p) {
+  constexpr int BM = 16 * MI, BN = 16 * NJ, U = 2;
+  static_assert(MI * NJ <= NW && kFp8Block % BN == 0, "one subtile per wave, one scale per tile");
+  __shared__ f32x4 red[NW][MI * NJ][64];
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  RowTile t;
+  int nb;
+  {
+    RowTiles<BM> tiles;
+    const int mt = p.counts ? tiles.load(p.counts, p.offsets, p.E, lane) : p.mt;
+    const int G = mt * p.nnb, per = (G + kXcds - 1) / kXcds;
+    const int i = (int)blockIdx.x / kXcds, v = (int)blockIdx.x % kXcds * per + i;
+    if (i >= per || v >= G) return;  // uniform per block
+    int tile;
+    panel_tile(v, mt, p.nnb, tile, nb);
+    if (p.counts) {
+      t = tiles.at(tile);
+      dbg_segment(t.row0, t.rows, p.M);
+      if (t.rows <= 0) return;
+    } else {
+      t.e = 0;
+      t.row0 = tile * BM;
+      t.rows = min(BM, p.M - t.row0);
+    }
+  }
+  const int K = p.K, kb = (K + kFp8Block - 1) / kFp8Block;
+  const int n0 = nb * BN;
+  const uint8_t* w = slot_base(p.w, p.w_stride, p, t.e) + (size_t)n0 * K;
+  const float* ws = reinterpret_cast<const float*>(slot_base(p.ws, p.ws_stride, p, t.e)) +
+                    n0 / kFp8Block * kb;
+  const uint8_t* a = p.a + (size_t)t.row0 * K;
+  const float* as = p.a_scale + (size_t)t.row0 * kb;
+  // lane group g: codes 16 g.. and 64 + 16 g.. of a block
+  uint32_t wo[NJ], ao[MI], so[MI];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    wo[j] = (uint32_t)min(16 * j + l16, p.N - 1 - n0) * (uint32_t)K + 16u * g;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const uint32_t r = (uint32_t)min(16 * i + l16, t.rows - 1);
+    ao[i] = r * (uint32_t)K + 16u * g;
+    so[i] = r * (uint32_t)kb;
+  }
+  struct Block {
+    i32x4 w[NJ][2], a[MI][2];
+    float sa[MI], sw;
+  };
+  auto load = [&](Block& b, int c) {
+    const int c0 = c * kFp8Block;
+    const uint8_t* wc = w + c0;
+    const uint8_t* ac = a + c0;
+    if (c0 + kFp8Block <= K) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        b.w[j][0] = *reinterpret_cast<const i32x4*>(wc + wo[j]);
+        b.w[j][1] = *reinterpret_cast<const i32x4*>(wc + wo[j] + 64);
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        b.a[i][0] = *reinterpret_cast<const i32x4*>(ac + ao[i]);
+        b.a[i][1] = *reinterpret_cast<const i32x4*>(ac + ao[i] + 64);
+      }
+    } else {
+      const i32x4 zero = {0, 0, 0, 0};
+      const bool ok0 = c0 + 16 * g < K, ok1 = c0 + 64 + 16 * g < K;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        b.w[j][0] = ok0 ? *reinterpret_cast<const i32x4*>(wc + wo[j]) : zero;
+        b.w[j][1] = ok1 ? *reinterpret_cast<const i32x4*>(wc + wo[j] + 64) : zero;
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        b.a[i][0] = ok0 ? *reinterpret_cast<const i32x4*>(ac + ao[i]) : zero;
+        b.a[i][1] = ok1 ? *reinterpret_cast<const i32x4*>(ac + ao[i] + 64) : zero;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) b.sa[i] = as[so[i] + c];
+    b.sw = ws[c];
+  };
+  f32x4 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto join = [](const i32x4 (&v)[2]) {
+    return fp8x32{v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
+  };
+  auto take = [&](const Block& b) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const fp8x32 af = join(b.a[i]);
+      const float s = b.sa[i] * b.sw;
+      f32x4 d[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) d[j] = mfma_e4m3(join(b.w[j]), af, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, d[j][q], acc[i][j][q]);
+    }
+  };
+  Block b[U];
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (wave + u * NW < kb) load(b[u], wave + u * NW);
+  for (int c0 = wave; c0 < kb; c0 += U * NW) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * NW, ahead = c + (U - 1) * NW;
+      if (c >= kb) break;
+      if (ahead < kb) load(b[(u + U - 1) % U], ahead);
+      __builtin_amdgcn_sched_barrier(0);
+      take(b[u]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) red[wave][i * NJ + j][lane] = acc[i][j];
+  __syncthreads();
+  if (wave >= MI * NJ) return;
+  f32x4 v = red[0][wave][lane];
+#pragma unroll
+  for (int x = 1; x < NW; ++x) {
+    const f32x4 o = red[x][wave][lane];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] += o[r];
+  }
+  const int row = 16 * (wave / NJ) + l16, col = n0 + 16 * (wave % NJ) + 4 * g;
+  if (row < t.rows)
+    store4(p.y + (size_t)(t.row0 + row) * p.N + col, v, p.N - col, p.N % 4 == 0);
+}
+
+template <int MI, int NJ, int NW>
+int launch_split(Fp8Args p, hipStream_t s, const char* who) {
+  p.nnb = (p.N + 16 * NJ - 1) / (16 * NJ);
+  const int64_t mt = p.counts ? row_tiles_bound(p.M, p.E, 16 * MI)
+                              : ((int64_t)p.M + 16 * MI - 1) / (16 * MI);
+  const int64_t blocks = (mt * p.nnb + kXcds - 1) / kXcds * kXcds;
+  if (blocks > ((int64_t)1 << 31) - 1)
+    return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+  p.mt = (int)mt;
+  fp8_split_kernel<MI, NJ, NW><<<(unsigned)blocks, 64 * NW, 0, s>>>(p);
   return check_launch(who);
 }
 
@@ -1049,10 +1222,14 @@ int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
 // Which kernel: by what fills the chip and how often weights are read again (times in us, E4M3
 // weights resident in HBM; R = rows per expert, M / E).
 //  * 16-row tiles read an expert's weights once per 16 rows: up to 4 rows per expert on average,
-//    or 32 rows in all (M = 32, N = 4096, K = 7168: 21.3 against 27.2 on 64 x 64 tiles, M = 128:
-//    38.1 against 27.9; FFN of 512 experts of 4096 x 1024: R = 1 1192 against 1189 on 64 x 256
+//    or 32 rows in all (M = 32, N = 4096, K = 7168: 21.3 against 27.2 on 64 x 64 tiles; FFN of 512 experts of 4096 x 1024: R = 1 1192 against 1189 on 64 x 256
 //    tiles, R = 16 1754 against 1324; of 64 experts of 2048 x 1024: R = 8 87 against 92).
 // Products of codes:
+//  * 32 x 16, 32 x 32 or 32 x 64 tiles while at most one of them falls on a compute unit, smallest
+//    first, for more than 16 rows (N = 4096, K = 7168: M = 32 15.1 against 17.8 on 16-row tiles,
+//    M = 64 18.1 and M = 128 24.6 against 27.4 and 27.8 on 64 x 64 tiles; N = 600, K = 4096: M = 64
+//    9.4 against 17.1, M = 384 11.8 against 17.0), but up to 32 rows 16-row tiles if those need
+//    no second round either (M = 32, N = 600, K = 4096: 7.9 against 9.3).
 //  * 64 x 64 tiles while at most two of them fall on a compute unit (N = 4096, K = 7168: M = 512
 //    36 against 47 on 64 x 256 tiles, M = 777 67 against 48).
 //  * 64 x 256 tiles while at most two of them fall on a compute unit (N = 4096, K = 7168: M = 1024
@@ -1077,6 +1254,12 @@ bool few_rows(int64_t M, int64_t E) { return M <= 4 * E || M <= 32; }
 int launch_product(const Fp8Args& p, hipStream_t s, const char* who) {
   const int64_t M = p.M, E = p.E;
   const int64_t rt = row_tiles_bound(M, E, 64);
+  const int64_t rt16 = row_tiles_bound(M, E, 16), rt32 = row_tiles_bound(M, E, 32);
+  if (M > 16 && M > 4 * E && (M > 32 || rt16 * ((p.N + 15) / 16) > kCus)) {
+    if (rt32 * ((p.N + 15) / 16) <= kCus) return launch_split<2, 1, 8>(p, s, who);
+    if (rt32 * ((p.N + 31) / 32) <= kCus) return launch_split<2, 2, 8>(p, s, who);
+    if (rt32 * ((p.N + 63) / 64) <= kCus) return launch_split<2, 4, 8>(p, s, who);
+  }
   if (few_rows(M, E)) return launch_rows16<kSrcCodes, false>(p, s, who);
   if (rt * ((p.N + 63) / 64) <= kTwoPerCu) return launch_ring<64, 64, 2, 2, 4, false>(p, s, who);
   if (rt * ((p.N + 255) / 256) <= kTwoPerCu || M <= 64 * E || p.K <= kFp8Block)

@@ -202,6 +202,37 @@ def test_matmul_grouped(E, counts, N, K, tail):
     p.check()                                   # rows behind the last segment keep the mark
 
 
+@pytest.mark.parametrize("M,N,K", [
+    (33, 200, 2048), (40, 17, 1040), (100, 1, 272), (20, 4096, 144),       # 32 x 16 tiles
+    (64, 4095, 1040), (65, 1301, 2064), (33, 4096, 16),                    # 32 x 32
+    (128, 4096, 272), (250, 1413, 1168), (97, 3333, 2000),                 # 32 x 64
+    (400, 1411, 400), (500, 1302, 144), (330, 2049, 640)])                 # 64 x 64, unaligned rows
+def test_matmul_dozens_of_rows(M, N, K):
+    """Tiles whose waves split K: fewer blocks than waves, a short last block, ragged edges."""
+    flush(f"[matmul] M={M} N={N} K={K}")
+    p = Product(M, N, K, seed=M + N + K).upload()
+    p.call()
+    torch.cuda.synchronize()
+    p.check()
+    ref = p.y.clone()
+    p.y.fill_(MARK)
+    p.call()
+    torch.cuda.synchronize()
+    assert torch.equal(p.y, ref)
+
+
+@pytest.mark.parametrize("E,counts,N,K,tail", [
+    (3, [20, 0, 33], 100, 1168, 2), (2, [0, 100], 1500, 400, 0), (4, [64, 1, 31, 32], 2050, 272, 3),
+    (5, [0, 0, 60, 0, 0], 700, 1040, 7), (3, [900, 300, 101], 2501, 144, 5)])  # the last: 64 x 256
+def test_matmul_dozens_of_rows_grouped(E, counts, N, K, tail):
+    M = sum(counts) + tail
+    flush(f"[matmul] grouped E={E} M={M} N={N} K={K}")
+    p = Product(M, N, K, E, counts, seed=E + N).upload()
+    p.call()
+    torch.cuda.synchronize()
+    p.check()
+
+
 def test_matmul_extreme_scales():
     """Any fp32 scales: zero, subnormal, negative, large; a NaN code or scale reaches its row only."""
     p = Product(70, 160, 384, seed=3)
