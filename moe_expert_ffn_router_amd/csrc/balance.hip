@@ -677,7 +677,7 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, in
     return check_launch(who);
   }
   const unsigned chunks = (unsigned)((T + a.R - 1) / a.R);
-  with_row_shape(E, [&](auto r) {
+  if (chunks) with_row_shape(E, [&](auto r) {
     using Q = decltype(r);
     balance_partial_kernel<4, Q::lpr, Q::vpl, Q::vec, false><<<chunks, 256, 0, s>>>(a);
   });

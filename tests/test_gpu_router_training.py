@@ -130,6 +130,10 @@ def test_against_oracle(T, E, k, seq, masked, renorm):
     Batch(T, E, k, seq, masked, seed=T + E, renorm=renorm).run()
 
 
+def test_no_row_in_many_sequences():
+    Batch(0, 8, 2, [0] * 301).run()
+
+
 def test_every_sequence_masked():
     b = Batch(150, 40, 4, [0, 70, 150], True, seed=1)
     b.mask[:] = 0
