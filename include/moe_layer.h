@@ -290,7 +290,7 @@ int moe_shared_ffn(const moe_experts* W, const uint16_t* x, int32_t T, uint16_t*
  * NaN in a counting row makes probs and loss of its sequence NaN.
  * Sums over tokens are taken in fp32 within a few dozen rows and in double
  * above, in a fixed order.
- * 1 <= E <= 1024, 1 <= k <= min(E, 16), T >= 0, T*k <= 2^28, 1 <= S <= 2^20.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 16), T >= 0, T*k <= 2^27, 1 <= S <= 2^20.
  * ws: device, >= moe_balance_loss_workspace(T, E, S).                       */
 size_t moe_balance_loss_workspace(int32_t T, int32_t E, int32_t S);
 int moe_balance_loss(const float* logits, const int32_t* topk_ids, int32_t T, int32_t E, int32_t k,

@@ -15,6 +15,8 @@
 // adds a sequence's pieces in double in chunk order, a workgroup per sequence and
 // 16 experts, and a third forms the loss.  A batch of one chunk is finished by the
 // first kernel.
+#include <algorithm>
+
 #include "fp8_common.h"
 
 namespace moe {
@@ -378,66 +380,69 @@ __global__ __launch_bounds__(kSlice * kRedLanes) void balance_reduce_kernel(BalA
   __shared__ int sc[NW][kSlice], sn[NW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nsl = (a.E + kSlice - 1) / kSlice;
-  const int s = (int)blockIdx.x / nsl, sl = (int)blockIdx.x - s * nsl;
-  int lo, hi;
-  seq_rows(a.seq, s, a.T, lo, hi);
-  const int c0 = lo / a.R, c1 = hi > lo ? (hi - 1) / a.R + 1 : c0;
-  const int e = sl * kSlice + tid % kSlice, cl = tid / kSlice;
-  double p = 0.0;
-  int c = 0;
-  for (int i = c0 + cl; i < c1; i += kRedLanes * U) {
-    float pv[U];
-    int cv[U];
+  for (int b = (int)blockIdx.x; b < a.S * nsl; b += (int)gridDim.x) {
+    const int s = b / nsl, sl = b - s * nsl;
+    int lo, hi;
+    seq_rows(a.seq, s, a.T, lo, hi);
+    const int c0 = lo / a.R, c1 = hi > lo ? (hi - 1) / a.R + 1 : c0;
+    const int e = sl * kSlice + tid % kSlice, cl = tid / kSlice;
+    double p = 0.0;
+    int c = 0;
+    for (int i = c0 + cl; i < c1; i += kRedLanes * U) {
+      float pv[U];
+      int cv[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool ok = i + u * kRedLanes < c1 && e < a.E;
-      const size_t o = (size_t)(i + u * kRedLanes + s) * a.E + e;
-      pv[u] = ok ? a.part_p[o] : 0.0f;
-      cv[u] = ok ? a.part_c[o] : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      p += (double)pv[u];
-      c += cv[u];
-    }
-  }
-  int n = 0;
-  if (sl == 0)
-    for (int i = c0 + tid; i < c1; i += NT) n += a.part_n[i + s];
-#pragma unroll
-  for (int o = 16; o < 64; o *= 2) {  // the wave's four chunk lanes
-    p += __shfl_xor(p, o, 64);
-    c += __shfl_xor(c, o, 64);
-  }
-#pragma unroll
-  for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o, 64);
-  if (lane < kSlice) {
-    sp[wave][lane] = p;
-    sc[wave][lane] = c;
-  }
-  if (lane == 0) sn[wave] = n;
-  __syncthreads();
-  if (wave == 0) {
-    double dot = 0.0;
-    if (lane < kSlice && e < a.E) {
-#pragma unroll
-      for (int w = 1; w < NW; ++w) {
-        p += sp[w][lane];
-        c += sc[w][lane];
+      for (int u = 0; u < U; ++u) {
+        const bool ok = i + u * kRedLanes < c1 && e < a.E;
+        const size_t o = (size_t)(i + u * kRedLanes + s) * a.E + e;
+        pv[u] = ok ? a.part_p[o] : 0.0f;
+        cv[u] = ok ? a.part_c[o] : 0;
       }
-      a.probs[(size_t)s * a.E + e] = (float)p;
-      a.counts[(size_t)s * a.E + e] = c;
-      dot = p * (double)c;
-    }
-    dot = wave_sum_f64(dot);
-    if (lane == 0) {
-      a.part_d[(size_t)s * nsl + sl] = dot;
-      if (sl == 0) {
 #pragma unroll
-        for (int w = 1; w < NW; ++w) n += sn[w];
-        a.n_tokens[s] = n;
+      for (int u = 0; u < U; ++u) {
+        p += (double)pv[u];
+        c += cv[u];
       }
     }
+    int n = 0;
+    if (sl == 0)
+      for (int i = c0 + tid; i < c1; i += NT) n += a.part_n[i + s];
+#pragma unroll
+    for (int o = 16; o < 64; o *= 2) {  // the wave's four chunk lanes
+      p += __shfl_xor(p, o, 64);
+      c += __shfl_xor(c, o, 64);
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o, 64);
+    if (lane < kSlice) {
+      sp[wave][lane] = p;
+      sc[wave][lane] = c;
+    }
+    if (lane == 0) sn[wave] = n;
+    __syncthreads();
+    if (wave == 0) {
+      double dot = 0.0;
+      if (lane < kSlice && e < a.E) {
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+          p += sp[w][lane];
+          c += sc[w][lane];
+        }
+        a.probs[(size_t)s * a.E + e] = (float)p;
+        a.counts[(size_t)s * a.E + e] = c;
+        dot = p * (double)c;
+      }
+      dot = wave_sum_f64(dot);
+      if (lane == 0) {
+        a.part_d[(size_t)s * nsl + sl] = dot;
+        if (sl == 0) {
+#pragma unroll
+          for (int w = 1; w < NW; ++w) n += sn[w];
+          a.n_tokens[s] = n;
+        }
+      }
+    }
+    __syncthreads();  // sp, sc and sn are reused by the next slice
   }
 }
 
@@ -615,7 +620,7 @@ int check_router_args(const char* who, int T, int E, int k, const int* seq, int 
   if (S < 1 || S > (1 << 20) || (!seq && S != 1))
     return set_error(MOE_ERR_INVALID_ARG, "%s: S=%d sequences (1..2^20; 1 without seq_offsets)",
                      who, S);
-  if ((int64_t)T * k > (1 << 28))
+  if ((int64_t)T * k > (1 << 27))
     return set_error(MOE_ERR_UNSUPPORTED, "%s: T*k too large", who);
   if (!aligned16(seq)) return set_error(MOE_ERR_INVALID_ARG, "%s: seq_offsets misaligned", who);
   return MOE_OK;
@@ -682,7 +687,9 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, in
     balance_partial_kernel<4, Q::lpr, Q::vpl, Q::vec, false><<<chunks, 256, 0, s>>>(a);
   });
   const unsigned slices = (unsigned)((E + kSlice - 1) / kSlice);
-  balance_reduce_kernel<<<(unsigned)S * slices, kSlice * kRedLanes, 0, s>>>(a);
+  // a grid has fewer than 2^32 threads
+  const unsigned blocks = std::min((unsigned)S * slices, 1u << 21);
+  balance_reduce_kernel<<<blocks, kSlice * kRedLanes, 0, s>>>(a);
   balance_loss_kernel<<<((unsigned)S + 3) / 4, 256, 0, s>>>(a);
   return check_launch(who);
 }

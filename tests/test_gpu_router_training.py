@@ -134,6 +134,29 @@ def test_no_row_in_many_sequences():
     Batch(0, 8, 2, [0] * 301).run()
 
 
+def test_a_million_sequences():
+    """2^20 sequences of which three hold rows: more slices of sums than a grid has workgroups."""
+    T, E, k, S = 2000, 64, 4, 1 << 20
+    small = Batch(T, E, k, [0, 700, 701, T], seed=5).upload()
+    small.forward()
+    seq = np.zeros(S + 1, np.int32)
+    at = [3, 400_000, S - 2]                   # the sequences with rows
+    seq[at[0] + 1:], seq[at[1] + 1:], seq[at[2] + 1:] = 700, 701, T
+    big = Batch(T, E, k, list(seq), seed=5).upload()
+    big.forward()
+    big.backward()
+    torch.cuda.synchronize()
+    for name in "ncpl":
+        got = big.o[name]
+        assert torch.equal(got[at], small.o[name])
+        got[at] = 0
+        assert not bool(got.any())
+    small.d["dl"] = big.d["dl"][at].contiguous()
+    small.backward()
+    torch.cuda.synchronize()
+    assert torch.equal(big.o["g"], small.o["g"])
+
+
 def test_every_sequence_masked():
     b = Batch(150, 40, 4, [0, 70, 150], True, seed=1)
     b.mask[:] = 0
