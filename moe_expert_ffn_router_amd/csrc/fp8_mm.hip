@@ -88,6 +88,9 @@ struct Fp8Args {
   int mt, nnb;        // tiles: row tiles (dense) and column blocks
 };
 
+// A grid has fewer than 2^32 threads.
+bool grid_fits(int64_t blocks, int threads) { return blocks < ((int64_t)1 << 32) / threads; }
+
 __device__ __forceinline__ const uint8_t* slot_base(const uint8_t* base, int64_t stride,
                                                     const Fp8Args& p, int e) {
   const int slot = p.slot_of ? dbg_clamp(p.slot_of[e], p.E, kDbgSlot) : e;
@@ -1027,7 +1030,7 @@ int launch_ring(Fp8Args p, hipStream_t s, const char* who) {
   p.nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
   const int64_t mt = p.counts ? row_tiles_bound(p.M, p.E, BM) : ((int64_t)p.M + BM - 1) / BM;
   const int64_t blocks = (mt * p.nnb + kXcds - 1) / kXcds * kXcds;
-  if (blocks > ((int64_t)1 << 31) - 1)
+  if (!grid_fits(blocks, 64 * WM * WN))
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   p.mt = (int)mt;
   fp8_ring_kernel<BM, BN, WM, WN, S, GATED><<<(unsigned)blocks, 64 * WM * WN, 0, s>>>(p);
@@ -1185,7 +1188,7 @@ int launch_split(Fp8Args p, hipStream_t s, const char* who) {
   const int64_t mt = p.counts ? row_tiles_bound(p.M, p.E, 16 * MI)
                               : ((int64_t)p.M + 16 * MI - 1) / (16 * MI);
   const int64_t blocks = (mt * p.nnb + kXcds - 1) / kXcds * kXcds;
-  if (blocks > ((int64_t)1 << 31) - 1)
+  if (!grid_fits(blocks, 64 * NW))
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   p.mt = (int)mt;
   fp8_split_kernel<MI, NJ, NW><<<(unsigned)blocks, 64 * NW, 0, s>>>(p);
@@ -1196,7 +1199,7 @@ template <int SRC, bool GATED, int NSUB, int NW, int SPLIT, int U>
 int launch_rows16_as(Fp8Args p, int64_t tiles, hipStream_t s, const char* who) {
   const int cols = (GATED ? NSUB / 2 : NSUB) * 16 * (SPLIT == 1 ? NW : 1);
   p.nnb = ((GATED ? p.I : p.N) + cols - 1) / cols;
-  if (p.nnb * tiles > ((int64_t)1 << 31) - 1)
+  if (!grid_fits(p.nnb * tiles, 64 * NW))
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   fp8_rows16_kernel<SRC, GATED, NSUB, NW, SPLIT, U>
       <<<(unsigned)(p.nnb * tiles), 64 * NW, 0, s>>>(p);

@@ -269,6 +269,10 @@ def test_expert_ffn_fp8_refusals():
         _refused(m.MOE_ERR_UNSUPPORTED, f, *args(fmt=fmt, stride=1 << 20))
     _refused(m.MOE_ERR_UNSUPPORTED, f, *args(H=200, stride=1 << 20))
     _refused(m.MOE_ERR_UNSUPPORTED, f, *args(T=1 << 27))
+    # rows past 32-bit offsets on 16-row tiles, more of them than a grid can hold
+    _refused(m.MOE_ERR_UNSUPPORTED, f, *args(
+        T=1 << 20, H=4096, I=16384, k=8, nb=1 << 62,
+        stride=synth.record_layout("fp8_b128", 4096, 16384)["stride"]))
     W = m.experts("fp8_b128", 8, 256, 128, P, st)
     need = m.moe_expert_ffn_fp8_workspace(W, 4, 2)
     assert 0 < need <= m.moe_expert_ffn_fp8_workspace(W, 5, 2)
