@@ -492,6 +492,23 @@ def test_expert_ffn_fp8_masked_rows_zero_and_nan():
     assert np.all(np.isfinite(np.delete(y, inv[7], 0)))
 
 
+@pytest.mark.parametrize("T,I", [(3, 128), (20, 128), (2100, 512)])  # 16-row, 64-row, 256-row tiles
+def test_expert_ffn_fp8_nan_weight_code(T, I):
+    """A NaN code among an expert's gate, up or down weights: NaN where its rows meet it, and
+    nowhere else."""
+    for name, n, whole in (("w13", 5 * 256 + 9, True), ("w13", (I + 7) * 256, True),
+                           ("w2", 3 * I + 2, False)):
+        c = Layer(T, 256, I, 4, 2, seed=91)
+        o, _ = synth.record_layout("fp8_b128", 256, I)["sections"][name]
+        c.records[1, o + n] = 0x7f
+        y = c.run()[:T * 2].float().cpu().numpy()
+        ids, _ = OR.route(c.logits_np, 2)
+        _, off, _, _ = OP.permute(ids, 4)
+        bad = np.zeros_like(y, bool)
+        bad[off[1]:off[2], slice(None) if whole else 3] = True
+        assert np.array_equal(np.isnan(y), bad)
+
+
 # ---- every kernel the size rules choose ------------------------------------
 def _check_all_rows(p, sample):
     """Every output against the product in float64 on the device, within a bound that only a
