@@ -8,6 +8,7 @@
 // lane's four results are consecutive output columns of one activation row,
 // whose scale it holds once, and the weight scale is the same for the whole
 // 16-row subtile.
+#include <algorithm>
 #include <type_traits>
 
 #include "fp8_common.h"
@@ -17,11 +18,12 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------------------
-// bf16 rows -> E4M3.  A thread holds 8 consecutive columns, 16 lanes
+// bf16 (x) or fp32 (h) rows -> E4M3.  A thread holds 8 consecutive columns, 16 lanes
 // (one DPP row) a 128-block; short blocks leave lanes without columns.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t* __restrict__ x, int T,
-                                                           int K, uint8_t* __restrict__ codes,
+template <typename SRC>
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(const SRC* __restrict__ x, int T, int K,
+                                                           uint8_t* __restrict__ codes,
                                                            float* __restrict__ scales) {
   const int kb = (K + kFp8Block - 1) / kFp8Block;
   const int64_t n = (int64_t)T * kb * 16;  // 8-column units, rows padded to whole blocks
@@ -32,12 +34,19 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t* __res
     const int col = b * kFp8Block + (int)(u & 15) * 8;
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (col < K) {
-      const uint4 v = *reinterpret_cast<const uint4*>(x + row * K + col);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      if constexpr (sizeof(SRC) == 2) {
+        const uint4 v = *reinterpret_cast<const uint4*>(x + row * K + col);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f[2 * q] = __uint_as_float(w[q] << 16);
-        f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+        for (int q = 0; q < 4; ++q) {
+          f[2 * q] = __uint_as_float(w[q] << 16);
+          f[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+        }
+      } else {
+        const float4* v = reinterpret_cast<const float4*>(x + row * K + col);
+        const float4 lo = v[0], hi = v[1];
+        f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w;
+        f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
       }
     }
     uint32_t am = 0;
@@ -57,7 +66,8 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(const uint16_t* __res
   }
 }
 
-void launch_quantize(const uint16_t* x, int T, int K, uint8_t* codes, float* scales,
+template <typename SRC>
+void launch_quantize(const SRC* x, int T, int K, uint8_t* codes, float* scales,
                      hipStream_t s) {
   const int64_t n = (int64_t)T * ((K + kFp8Block - 1) / kFp8Block) * 16;
   const int64_t blocks = (n + 255) / 256;
@@ -1040,15 +1050,16 @@ int launch_ring(Fp8Args p, hipStream_t s, const char* who) {
 // ---------------------------------------------------------------------------
 // Tiles of 16 MI rows x 16 NJ weight rows for products of a few dozen rows: the NW waves of a
 // workgroup split K (blocks w, w + NW, ...), operands go from memory straight to registers, one
-// block ahead, and the waves' sums of the whole tile meet in LDS in wave order.  Bound by what
+// block ahead, and the waves' sums of the whole tile meet in LDS in wave order.  Gate/up: half of
+// the weight rows are gate rows, half their up rows, on the bf16 MFMA.  Bound by what
 // a compute unit takes in, 31 bytes per ns whatever is in flight (two to four blocks ahead or 16
 // waves change nothing): so the smallest tile that still needs no second round of workgroups
 // (M = 64, N = 4096, K = 7168: 18.1 us on 32 x 32 tiles, 24.7 on 32 x 64, 54 on 64 x 64).
 // ---------------------------------------------------------------------------
-template <int MI, int NJ, int NW>
+template <int MI, int NJ, int NW, bool GATED>
 __global__ __launch_bounds__(64 * NW) void fp8_split_kernel(Fp8Args p) {
-  constexpr int BM = 16 * MI, BN = 16 * NJ, U = 2;
-  static_assert(MI * NJ <= NW && kFp8Block % BN == 0, "one subtile per wave, one scale per tile");
+  constexpr int BM = 16 * MI, OUT = GATED ? NJ / 2 : NJ, COLS = 16 * OUT, U = 2;
+  static_assert(MI * OUT <= NW && kFp8Block % COLS == 0, "one subtile per wave, one scale per tile");
   __shared__ f32x4 red[NW][MI * NJ][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1073,26 +1084,29 @@ __global__ __launch_bounds__(64 * NW) void fp8_split_kernel(Fp8Args p) {
     }
   }
   const int K = p.K, kb = (K + kFp8Block - 1) / kFp8Block;
-  const int n0 = nb * BN;
+  const int n0 = nb * COLS, up = GATED ? p.I : 0;  // up rows lie behind the gate rows
   const uint8_t* w = slot_base(p.w, p.w_stride, p, t.e) + (size_t)n0 * K;
   const float* ws = reinterpret_cast<const float*>(slot_base(p.ws, p.ws_stride, p, t.e)) +
                     n0 / kFp8Block * kb;
-  const uint8_t* a = p.a + (size_t)t.row0 * K;
-  const float* as = p.a_scale + (size_t)t.row0 * kb;
+  const uint8_t* a = GATED ? p.a : p.a + (size_t)t.row0 * K;
+  const float* as = GATED ? p.a_scale : p.a_scale + (size_t)t.row0 * kb;
   // lane group g: codes 16 g.. and 64 + 16 g.. of a block
   uint32_t wo[NJ], ao[MI], so[MI];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    wo[j] = (uint32_t)min(16 * j + l16, p.N - 1 - n0) * (uint32_t)K + 16u * g;
+  for (int j = 0; j < NJ; ++j) {
+    const int row = min(16 * (j % OUT) + l16, p.N - 1 - n0) + (j < OUT ? 0 : up);
+    wo[j] = (uint32_t)row * (uint32_t)K + 16u * g;
+  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const uint32_t r = (uint32_t)min(16 * i + l16, t.rows - 1);
-    ao[i] = r * (uint32_t)K + 16u * g;
-    so[i] = r * (uint32_t)kb;
+    int r = min(16 * i + l16, t.rows - 1);
+    if constexpr (GATED) r = dbg_clamp(p.row_of[t.row0 + r], p.M, kDbgSorted) / p.k;
+    ao[i] = (uint32_t)r * (uint32_t)K + 16u * g;
+    so[i] = (uint32_t)r * (uint32_t)kb;
   }
   struct Block {
     i32x4 w[NJ][2], a[MI][2];
-    float sa[MI], sw;
+    float sa[MI], sw[GATED ? 2 : 1];
   };
   auto load = [&](Block& b, int c) {
     const int c0 = c * kFp8Block;
@@ -1125,7 +1139,8 @@ __global__ __launch_bounds__(64 * NW) void fp8_split_kernel(Fp8Args p) {
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) b.sa[i] = as[so[i] + c];
-    b.sw = ws[c];
+    b.sw[0] = ws[c];
+    if constexpr (GATED) b.sw[1] = ws[up / kFp8Block * kb + c];
   };
   f32x4 acc[MI][NJ];
 #pragma unroll
@@ -1135,18 +1150,31 @@ __global__ __launch_bounds__(64 * NW) void fp8_split_kernel(Fp8Args p) {
   auto join = [](const i32x4 (&v)[2]) {
     return fp8x32{v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
   };
+  using Frag = std::conditional_t<GATED, Decoded, fp8x32>;
+  auto operand = [&](const i32x4 (&v)[2]) -> Frag {
+    if constexpr (GATED) return decode_e4m3(join(v));
+    else return join(v);
+  };
   auto take = [&](const Block& b) {
+    Frag af[MI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const fp8x32 af = join(b.a[i]);
-      const float s = b.sa[i] * b.sw;
-      f32x4 d[NJ];
+    for (int i = 0; i < MI; ++i) af[i] = operand(b.a[i]);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) d[j] = mfma_e4m3(join(b.w[j]), af, f32x4{0.f, 0.f, 0.f, 0.f});
+    for (int j = 0; j < NJ; ++j) {
+      const Frag wf = operand(b.w[j]);
+      f32x4 d[MI];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int i = 0; i < MI; ++i) {
+        d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (GATED) d[i] = mfma_decoded(wf, af[i], d[i]);
+        else d[i] = mfma_e4m3(wf, af[i], d[i]);
+      }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, d[j][q], acc[i][j][q]);
+      for (int i = 0; i < MI; ++i) {
+        const float s = b.sa[i] * b.sw[j / OUT];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(s, d[i][q], acc[i][j][q]);
+      }
     }
   };
   Block b[U];
@@ -1169,29 +1197,41 @@ __global__ __launch_bounds__(64 * NW) void fp8_split_kernel(Fp8Args p) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) red[wave][i * NJ + j][lane] = acc[i][j];
   __syncthreads();
-  if (wave >= MI * NJ) return;
-  f32x4 v = red[0][wave][lane];
+  if (wave >= MI * OUT) return;
+  auto total = [&](int n) {
+    f32x4 v = red[0][n][lane];
 #pragma unroll
-  for (int x = 1; x < NW; ++x) {
-    const f32x4 o = red[x][wave][lane];
+    for (int x = 1; x < NW; ++x) {
+      const f32x4 o = red[x][n][lane];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] += o[r];
-  }
-  const int row = 16 * (wave / NJ) + l16, col = n0 + 16 * (wave % NJ) + 4 * g;
-  if (row < t.rows)
+      for (int r = 0; r < 4; ++r) v[r] += o[r];
+    }
+    return v;
+  };
+  const int i = wave / OUT, j = wave % OUT;
+  const int row = 16 * i + l16, col = n0 + 16 * j + 4 * g;
+  const f32x4 v = total(i * NJ + j);
+  if constexpr (GATED) {
+    const f32x4 u = total(i * NJ + OUT + j);
+    if (row < t.rows)
+      *reinterpret_cast<float4*>(p.h + (size_t)(t.row0 + row) * p.I + col) =
+          float4{swiglu(v[0], u[0]), swiglu(v[1], u[1]), swiglu(v[2], u[2]), swiglu(v[3], u[3])};
+  } else if (row < t.rows) {
     store4(p.y + (size_t)(t.row0 + row) * p.N + col, v, p.N - col, p.N % 4 == 0);
+  }
 }
 
-template <int MI, int NJ, int NW>
+template <int MI, int NJ, int NW, bool GATED>
 int launch_split(Fp8Args p, hipStream_t s, const char* who) {
-  p.nnb = (p.N + 16 * NJ - 1) / (16 * NJ);
+  constexpr int COLS = GATED ? 8 * NJ : 16 * NJ;
+  p.nnb = ((GATED ? p.I : p.N) + COLS - 1) / COLS;
   const int64_t mt = p.counts ? row_tiles_bound(p.M, p.E, 16 * MI)
                               : ((int64_t)p.M + 16 * MI - 1) / (16 * MI);
   const int64_t blocks = (mt * p.nnb + kXcds - 1) / kXcds * kXcds;
   if (!grid_fits(blocks, 64 * NW))
     return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
   p.mt = (int)mt;
-  fp8_split_kernel<MI, NJ, NW><<<(unsigned)blocks, 64 * NW, 0, s>>>(p);
+  fp8_split_kernel<MI, NJ, NW, GATED><<<(unsigned)blocks, 64 * NW, 0, s>>>(p);
   return check_launch(who);
 }
 
@@ -1241,7 +1281,8 @@ int launch_rows16(const Fp8Args& p, hipStream_t s, const char* who) {
 //    R = 96 154 against 117; of 256 experts of 7168 x 2048: R = 64 2359 against 2741, R = 128 3577
 //    against 2723).
 //  * 256 x 256 tiles otherwise (two K blocks at least).
-// Gate/up products, whose 64 x 256 tiles run on the bf16 MFMA (FFN times):
+// Gate/up products, whose tiles of 32 and 64 rows run on the bf16 MFMA (FFN times):
+//  * 32-row tiles where gateup_split_cols says so.
 //  * 64 x 256 tiles while at most one of them falls on a compute unit where the rows spread evenly
 //    over the experts (8 experts of 4096 x 1024: R = 256 86 against 98, R = 400 132 against 101;
 //    32 of 2048 x 768: R = 64 47 against 50, R = 128 77 against 57), or two for up to 32 rows per
@@ -1259,9 +1300,9 @@ int launch_product(const Fp8Args& p, hipStream_t s, const char* who) {
   const int64_t rt = row_tiles_bound(M, E, 64);
   const int64_t rt16 = row_tiles_bound(M, E, 16), rt32 = row_tiles_bound(M, E, 32);
   if (M > 16 && M > 4 * E && (M > 32 || rt16 * ((p.N + 15) / 16) > kCus)) {
-    if (rt32 * ((p.N + 15) / 16) <= kCus) return launch_split<2, 1, 8>(p, s, who);
-    if (rt32 * ((p.N + 31) / 32) <= kCus) return launch_split<2, 2, 8>(p, s, who);
-    if (rt32 * ((p.N + 63) / 64) <= kCus) return launch_split<2, 4, 8>(p, s, who);
+    if (rt32 * ((p.N + 15) / 16) <= kCus) return launch_split<2, 1, 8, false>(p, s, who);
+    if (rt32 * ((p.N + 31) / 32) <= kCus) return launch_split<2, 2, 8, false>(p, s, who);
+    if (rt32 * ((p.N + 63) / 64) <= kCus) return launch_split<2, 4, 8, false>(p, s, who);
   }
   if (few_rows(M, E)) return launch_rows16<kSrcCodes, false>(p, s, who);
   if (rt * ((p.N + 63) / 64) <= kTwoPerCu) return launch_ring<64, 64, 2, 2, 4, false>(p, s, who);
@@ -1279,10 +1320,22 @@ int launch_gateup(const Fp8Args& p, hipStream_t s, const char* who) {
   return launch_tiles<256, 256, 2, 4, true>(p, s, who);
 }
 
-// FFN workspace: h (fp32) on the 16-row path; xq, its scales, hq and its scales on the others.
-// The size covers both.
+// Output columns of the gate/up tiles of 32 rows whose waves split K (h leaves them in fp32 and
+// takes a launch of its own to be quantised): 16 or 32 where at most one tile falls on a
+// compute unit with the rows spread evenly, 0 where they are not taken.  FFN of 8 experts of
+// 4096 x 1024, 16 rows each: 34 us, on 64 x 256 tiles 56; 4 of 2048 x 512, 128 rows each: 25 and 35;
+// up to two tiles per unit: 32 of 1408 x 512, 16 rows each 32.3 against 30.7.  A K of less than one
+// block per wave does not pay for the launch (4 of 256 x 256, 10 rows each: 19 against 17).
+int gateup_split_cols(int64_t A, int64_t E, int64_t H, int64_t I) {
+  const int64_t rt = std::min(A, E) * ((A + 32 * E - 1) / (32 * E));
+  if (H < 8 * kFp8Block) return 0;
+  return rt * (I / 16) <= kCus ? 16 : rt * (I / 32) <= kCus ? 32 : 0;
+}
+
+// FFN workspace: h (fp32) on the 16-row path; xq, its scales, hq and its scales on the others,
+// and h behind them where gate/up tiles do not hold whole scale blocks.  The size covers all.
 struct Fp8FfnWs {
-  size_t h, xq, xs, hq, hs, total;
+  size_t h, xq, xs, hq, hs, h_behind, total;
 };
 Fp8FfnWs fp8_ffn_ws(int64_t T, int64_t k, int64_t H, int64_t I) {
   auto up = [](int64_t v) { return (size_t)((v + 255) / 256 * 256); };
@@ -1293,7 +1346,9 @@ Fp8FfnWs fp8_ffn_ws(int64_t T, int64_t k, int64_t H, int64_t I) {
   w.xs = w.xq + up(T * H);
   w.hq = w.xs + up(T * (H / kFp8Block) * 4);
   w.hs = w.hq + up(A * I);
-  w.total = w.hs + up(A * (I / kFp8Block) * 4);
+  w.h_behind = w.hs + up(A * (I / kFp8Block) * 4);
+  // tiles of 32 x 32 on every compute unit at most; never less for more tokens
+  w.total = w.h_behind + up(std::min(A * I, 32 * 32 * kCus) * 4);
   if (w.total < up(A * I * 4)) w.total = up(A * I * 4);
   return w;
 }
@@ -1433,8 +1488,13 @@ extern "C" int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_e
   p.a_scale = reinterpret_cast<const float*>(wb + B.xs);
   p.hq = wb + B.hq;
   p.hs = reinterpret_cast<float*>(wb + B.hs);
-  const int st = launch_gateup(p, s, who);
+  const int cols = gateup_split_cols(A, W->E, H, I);
+  if (cols) p.h = reinterpret_cast<float*>(wb + B.h_behind);
+  const int st = cols == 16   ? launch_split<2, 2, 8, true>(p, s, who)
+                 : cols == 32 ? launch_split<2, 4, 8, true>(p, s, who)
+                              : launch_gateup(p, s, who);
   if (st) return st;
+  if (cols) launch_quantize(p.h, (int)A, I, p.hq, p.hs, s);
   d.a = p.hq;
   d.a_scale = p.hs;
   return launch_product(d, s, who);

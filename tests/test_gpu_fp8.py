@@ -419,7 +419,10 @@ class Layer:
 @pytest.mark.parametrize("T,H,I,E,k,zipf", [
     (1, 128, 128, 4, 2, None), (8, 256, 128, 16, 4, None), (5, 384, 256, 1, 1, None),
     (40, 512, 384, 8, 2, 1.2), (150, 256, 256, 6, 3, 0.7), (64, 1024, 512, 40, 8, None),
-    (300, 384, 640, 3, 2, None), (16, 2048, 512, 64, 8, None), (600, 256, 256, 4, 2, 1.5)])
+    (300, 384, 640, 3, 2, None), (16, 2048, 512, 64, 8, None), (600, 256, 256, 4, 2, 1.5),
+    # 32-row gate/up tiles: 16 columns (few tiles), 32 columns, one expert's rows over many tiles
+    (40, 1024, 256, 4, 2, 1.5), (90, 1152, 512, 8, 4, None), (64, 1024, 128, 3, 3, None),
+    (33, 2048, 128, 2, 1, None), (100, 1024, 640, 7, 2, 2.5)])
 def test_expert_ffn_fp8(T, H, I, E, k, zipf):
     flush(f"[ffn fp8] T={T} H={H} I={I} E={E} k={k}")
     c = Layer(T, H, I, E, k, seed=T + H + I, zipf=zipf)
@@ -429,7 +432,8 @@ def test_expert_ffn_fp8(T, H, I, E, k, zipf):
 
 @pytest.mark.parametrize("T,H,I,E,k,zipf", [
     (1, 512, 128, 4, 2, None), (8, 2048, 512, 64, 8, None),      # 16-row tiles
-    (40, 512, 384, 8, 2, 1.2), (90, 2048, 256, 6, 4, None)])     # 64 x 256 tiles
+    (40, 512, 384, 8, 2, 1.2), (150, 384, 256, 6, 4, None),      # 64 x 256 tiles
+    (90, 2048, 256, 6, 4, None), (90, 1152, 512, 8, 4, 1.0)])    # 32-row tiles
 def test_expert_ffn_fp8_of_few_rows_keeps_every_product(T, H, I, E, k, zipf):
     """Ordinary values, whose products span more than the E4M3 MFMA keeps: few rows take their
     gate/up products exactly, with the tolerance of fp32 additions."""
@@ -439,8 +443,9 @@ def test_expert_ffn_fp8_of_few_rows_keeps_every_product(T, H, I, E, k, zipf):
     c.check()
 
 
-def test_expert_ffn_fp8_through_a_slot_table_and_larger_buffers():
-    c = Layer(30, 256, 256, 12, 3, seed=77, T_max=50)
+@pytest.mark.parametrize("H", [256, 1024])
+def test_expert_ffn_fp8_through_a_slot_table_and_larger_buffers(H):
+    c = Layer(30, H, 256, 12, 3, seed=77, T_max=50)
     perm = torch.randperm(c.E)
     pool = torch.empty_like(c.records)
     pool[perm.to(DEV)] = c.records              # record e in slot perm[e]
@@ -492,14 +497,15 @@ def test_expert_ffn_fp8_masked_rows_zero_and_nan():
     assert np.all(np.isfinite(np.delete(y, inv[7], 0)))
 
 
-@pytest.mark.parametrize("T,I", [(3, 128), (20, 128), (2100, 512)])  # 16-row, 64-row, 256-row tiles
-def test_expert_ffn_fp8_nan_weight_code(T, I):
+@pytest.mark.parametrize("T,H,I", [(3, 256, 128), (20, 256, 128), (20, 1024, 128),
+                                   (2100, 256, 512)])  # tiles of 16, 64, 32 and 256 rows
+def test_expert_ffn_fp8_nan_weight_code(T, H, I):
     """A NaN code among an expert's gate, up or down weights: NaN where its rows meet it, and
     nowhere else."""
-    for name, n, whole in (("w13", 5 * 256 + 9, True), ("w13", (I + 7) * 256, True),
+    for name, n, whole in (("w13", 5 * H + 9, True), ("w13", (I + 7) * H, True),
                            ("w2", 3 * I + 2, False)):
-        c = Layer(T, 256, I, 4, 2, seed=91)
-        o, _ = synth.record_layout("fp8_b128", 256, I)["sections"][name]
+        c = Layer(T, H, I, 4, 2, seed=91)
+        o, _ = synth.record_layout("fp8_b128", H, I)["sections"][name]
         c.records[1, o + n] = 0x7f
         y = c.run()[:T * 2].float().cpu().numpy()
         ids, _ = OR.route(c.logits_np, 2)

@@ -276,6 +276,9 @@ def test_expert_ffn_fp8_refusals():
     W = m.experts("fp8_b128", 8, 256, 128, P, st)
     need = m.moe_expert_ffn_fp8_workspace(W, 4, 2)
     assert 0 < need <= m.moe_expert_ffn_fp8_workspace(W, 5, 2)
+    W2 = m.experts("fp8_b128", 8, 2048, 512, P, st)     # never less for more tokens
+    sizes = [m.moe_expert_ffn_fp8_workspace(W2, T, 2) for T in range(0, 2000, 7)]
+    assert sizes == sorted(sizes)
     _refused(m.MOE_ERR_WORKSPACE, f, *args(nb=need - 1))
     _refused(m.MOE_OK, f, *args(T=0))
 
