@@ -153,6 +153,9 @@ def _ptr(t) -> int | None:
 # The current stream's handle without building a Stream object (2.9 us a call, measured; this
 # is 0.1 us); torch builds without the function go the long way.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# Likewise the current device, for calls that hold a device tensor already (so that the
+# runtime is initialised).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
@@ -527,8 +530,8 @@ def _arg(t, name: str, dtype, numel: int | None, dev) -> int | None:
         return None
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
     return t.data_ptr()
 
 
@@ -537,21 +540,28 @@ def _opt(t, name: str, dtype, numel: int | None, dev) -> int | None:
 
 
 def _device_of(t, name: str):
-    """The device that a call runs on: its first tensor's, which must be the current one."""
+    """Index of the device that a call runs on: its first tensor's, which must be the current one."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor, got {type(t)}")
     if not t.is_cuda:
         raise ValueError(f"{name}: device tensor expected")
-    if t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != _current_device():
         raise ValueError(f"{name}: on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return t.device
+    return dev
+
+
+def _stream_on(stream, dev) -> int | None:
+    """_stream for a call whose device is known to be the current one."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _matrix(t, name: str) -> tuple[int, int]:
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if len(shape) != 2:
         raise ValueError(f"{name}: expected a matrix")
-    return t.shape[0], t.shape[1]
+    return shape
 
 
 def _seq_count(seq_offsets) -> int:
@@ -574,7 +584,7 @@ def moe_balance_loss(logits, topk_ids, k: int, n_tokens, counts, probs, loss, ws
         _opt(seq_offsets, "seq_offsets", _I32T, None, dev), S,
         _arg(n_tokens, "n_tokens", _I32T, S, dev), _arg(counts, "counts", _I32T, S * E, dev),
         _arg(probs, "probs", _F32, S * E, dev), _arg(loss, "loss", _F32, S, dev),
-        _arg(ws, "ws", _U8, None, dev), ws.numel(), _stream(stream)), "moe_balance_loss")
+        _arg(ws, "ws", _U8, None, dev), ws.numel(), _stream_on(stream, dev)), "moe_balance_loss")
 
 
 def moe_route_backward(logits, k: int, topk_ids, topk_w, d_topk_w, n_tokens, counts, d_loss,
@@ -592,7 +602,7 @@ def moe_route_backward(logits, k: int, topk_ids, topk_w, d_topk_w, n_tokens, cou
         _opt(seq_offsets, "seq_offsets", _I32T, None, dev), S,
         _opt(n_tokens, "n_tokens", _I32T, S, dev), _opt(counts, "counts", _I32T, S * E, dev),
         _opt(d_loss, "d_loss", _F32, S, dev), _arg(d_logits, "d_logits", _F32, T * E, dev),
-        _stream(stream)), "moe_route_backward")
+        _stream_on(stream, dev)), "moe_route_backward")
 
 
 def moe_fp8_quantize(x, codes, scales, stream=None) -> None:
@@ -601,7 +611,7 @@ def moe_fp8_quantize(x, codes, scales, stream=None) -> None:
     dev = _device_of(x, "x")
     _check(_lib.moe_fp8_quantize(
         _arg(x, "x", _BF16, None, dev), T, K, _arg(codes, "codes", _FP8, T * K, dev),
-        _arg(scales, "scales", _F32, T * ((K + 127) // 128), dev), _stream(stream)),
+        _arg(scales, "scales", _F32, T * ((K + 127) // 128), dev), _stream_on(stream, dev)),
         "moe_fp8_quantize")
 
 
@@ -615,16 +625,17 @@ def moe_fp8_matmul(a, a_scale, w, w_scale, y, ws=None, counts=None, offsets=None
     each expert given by counts and offsets."""
     M, K = _matrix(a, "a")
     dev = _device_of(a, "a")
-    if w.dim() not in (2, 3) or w.shape[-1] != K:
-        raise ValueError(f"w: shape {tuple(w.shape)}, expected [N, {K}] or [E, N, {K}]")
-    N, E = w.shape[-2], (w.shape[0] if w.dim() == 3 else 1)
+    shape = w.shape
+    if len(shape) not in (2, 3) or shape[-1] != K:
+        raise ValueError(f"w: shape {tuple(shape)}, expected [N, {K}] or [E, N, {K}]")
+    N, E = shape[-2], (shape[0] if len(shape) == 3 else 1)
     kb, nb = (K + 127) // 128, (N + 127) // 128
     _check(_lib.moe_fp8_matmul(
         _arg(a, "a", _FP8, None, dev), _arg(a_scale, "a_scale", _F32, M * kb, dev), M,
         _arg(w, "w", _FP8, None, dev), _arg(w_scale, "w_scale", _F32, E * nb * kb, dev), N, K,
         _opt(counts, "counts", _I32T, E, dev), _opt(offsets, "offsets", _I32T, E + 1, dev), E,
         _arg(y, "y", _BF16, M * N, dev), _opt(ws, "ws", _U8, None, dev),
-        0 if ws is None else ws.numel(), _stream(stream)), "moe_fp8_matmul")
+        0 if ws is None else ws.numel(), _stream_on(stream, dev)), "moe_fp8_matmul")
 
 
 def moe_expert_ffn_fp8_workspace(W: Experts, T: int, k: int) -> int:
@@ -646,7 +657,7 @@ def moe_expert_ffn_fp8(W: Experts, slot_of_expert, x, T: int, k: int, counts, of
         _arg(x, "x", _BF16, None, dev), T, k, _arg(counts, "counts", _I32T, None, dev),
         _arg(offsets, "offsets", _I32T, None, dev), _arg(sorted_idx, "sorted_idx", _I32T, None, dev),
         _arg(y_perm, "y_perm", _BF16, None, dev), _arg(ws, "ws", _U8, None, dev), ws.numel(),
-        _stream(stream)), "moe_expert_ffn_fp8")
+        _stream_on(stream, dev)), "moe_expert_ffn_fp8")
 
 
 def moe_version() -> int:
