@@ -619,7 +619,13 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(Fp8Args p) {
   issue_b(1, 0, CPB);
   issue_a(1, 0, CPA);
   MOE_DMA_SYNC(CPA + CPB);
-  if (p.row_of && mine > 1) issue_src(1);
+  if (p.row_of && mine > 1) {
+    issue_src(1);
+    // Two blocks of K: the first turn opens tile 1 and reads its rows with no landed() before
+    // that (of three and more, the first turn's covers this copy; of later tiles' copies, the
+    // second turn's of the tile before).
+    if (kb == 2) MOE_DMA_SYNC(0);
+  }
   whole(0, 0);
 
   f32x4 acc[MI][NJ], d[2];  // d: the last two results, not folded in yet
