@@ -11,6 +11,8 @@ library calls.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -25,6 +27,16 @@ from . import (Experts, experts, moe_balance_loss, moe_balance_loss_workspace, m
 
 def _i32(n, dev):
     return torch.empty(max(int(n), 1), dtype=torch.int32, device=dev)
+
+
+def _on(stream):
+    """Context in which torch allocates for work on `stream` (None: the current stream).  Memory
+    allocated outside it could still be in use by work pending on the current stream, which a
+    kernel on `stream` does not wait for."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                             else stream)
 
 
 class MoELayer:
@@ -87,9 +99,10 @@ class MoELayer:
         products in E4M3 (moe_expert_ffn_fp8); the others keep bf16 activations."""
         if variant == "fp8":
             if self.fp8_ws is None:
-                self.fp8_ws = torch.empty(
-                    max(moe_expert_ffn_fp8_workspace(self._probe, self.T_max, self.k), 256),
-                    dtype=torch.uint8, device=self.device)
+                with _on(stream):
+                    self.fp8_ws = torch.empty(
+                        max(moe_expert_ffn_fp8_workspace(self._probe, self.T_max, self.k), 256),
+                        dtype=torch.uint8, device=self.device)
             moe_expert_ffn_fp8(W, slot_of_expert, x, T, self.k, self.counts, self.offsets,
                                self.sorted_idx, self.y_perm, self.fp8_ws, stream)
             return
@@ -113,20 +126,19 @@ class MoELayer:
     def balance_loss(self, logits: torch.Tensor, token_mask=None, seq_offsets=None,
                      stream=None) -> dict:
         """Load-balance loss of the batch last routed (self.ids), per sequence, with the
-        per-expert counts and probability sums (moe_balance_loss)."""
+        per-expert counts and probability sums (moe_balance_loss).  The results belong to
+        `stream`: work on another one waits for it and records its use, as for any tensor of torch."""
         T, E = logits.shape
         S = 1 if seq_offsets is None else seq_offsets.numel() - 1
         i32 = dict(dtype=torch.int32, device=self.device)
         f32 = dict(dtype=torch.float32, device=self.device)
-        r = {"n_tokens": torch.empty(S, **i32), "counts": torch.empty(S, E, **i32),
-             "probs": torch.empty(S, E, **f32), "loss": torch.empty(S, **f32)}
-        ws = torch.empty(max(moe_balance_loss_workspace(T, E, S), 256), dtype=torch.uint8,
-                         device=self.device)
+        with _on(stream):
+            r = {"n_tokens": torch.empty(S, **i32), "counts": torch.empty(S, E, **i32),
+                 "probs": torch.empty(S, E, **f32), "loss": torch.empty(S, **f32)}
+            ws = torch.empty(max(moe_balance_loss_workspace(T, E, S), 256), dtype=torch.uint8,
+                             device=self.device)
         moe_balance_loss(logits, self.ids[:T * self.k], self.k, r["n_tokens"], r["counts"],
                          r["probs"], r["loss"], ws, token_mask, seq_offsets, stream)
-        if stream is not None:          # the scratch is in use there after this call returns
-            ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
-                             else stream)
         return r
 
     def route_backward(self, logits: torch.Tensor, d_logits: torch.Tensor, d_topk_w=None,
@@ -192,9 +204,10 @@ class MoELayer:
         E = self.E
         cs = stream if stream is not None else torch.cuda.current_stream()
         if self.stream_ws is None:
-            self.stream_ws = torch.empty(
-                max(moe_expert_ffn_streamed_workspace(self._probe, self.T_max, self.k), 256),
-                dtype=torch.uint8, device=self.device)
+            with _on(cs):
+                self.stream_ws = torch.empty(
+                    max(moe_expert_ffn_streamed_workspace(self._probe, self.T_max, self.k), 256),
+                    dtype=torch.uint8, device=self.device)
         self.route_permute(logits, cs)
         with torch.cuda.stream(cs):
             self.counts_host.copy_(self.counts[:E], non_blocking=True)
@@ -220,9 +233,10 @@ class MoELayer:
         E = self.E
         cs = stream if stream is not None else torch.cuda.current_stream()
         if self.stream_ws is None:
-            self.stream_ws = torch.empty(
-                max(moe_expert_ffn_streamed_workspace(self._probe, self.T_max, self.k), 256),
-                dtype=torch.uint8, device=self.device)
+            with _on(cs):
+                self.stream_ws = torch.empty(
+                    max(moe_expert_ffn_streamed_workspace(self._probe, self.T_max, self.k), 256),
+                    dtype=torch.uint8, device=self.device)
         if self.host_stage is None:
             self.host_stage = torch.empty(
                 moe_expert_ffn_hybrid_host_bytes(self._probe, self.T_max, self.k),
