@@ -199,7 +199,10 @@ class MoELayer:
         """Slot-table path with the FFN behind the fills (moe_expert_ffn_streamed): waves of
         at most S (or S/2 when the step needs more than S experts), each wave's misses in
         `groups` copy groups on `side`, the FFN over the hits at once and over each group as
-        it lands.  y is bit-identical to forward_cached whenever that one fits."""
+        it lands.  y is bit-identical to forward_cached whenever that one fits.  There is no
+        streamed FFN with E4M3 activations: variant "fp8" is refused."""
+        if variant == "fp8":
+            raise ValueError('forward_streamed: variant "fp8" is not available; use forward_cached')
         T = logits.shape[0]
         E = self.E
         cs = stream if stream is not None else torch.cuda.current_stream()
