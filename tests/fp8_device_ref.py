@@ -48,13 +48,14 @@ def quantize(x: torch.Tensor):
     return round_e4m3(x / s) * s, s
 
 
-def cut(a: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+def cut(a: torch.Tensor, w: torch.Tensor, dtype=torch.float32) -> torch.Tensor:
     """Bound on what the E4M3 MFMA drops: 7 * 2^-13 of the largest product of every 8 consecutive k.
     a, w: magnitudes with their scales, an operand below 2^-6 (a subnormal code) raised to it
-    (raised()), which bounds the product of the operands' binades too."""
-    a, w = a.float(), w.float()
+    (raised()), which bounds the product of the operands' binades too.  dtype: of the products and
+    their sum, double where fp32 would not hold them."""
+    a, w = a.to(dtype), w.to(dtype)
     K = a.shape[1]
-    out = torch.zeros(a.shape[0], w.shape[0], device=a.device)
+    out = torch.zeros(a.shape[0], w.shape[0], dtype=dtype, device=a.device)
     step = max(1, (1 << 26) // (8 * w.shape[0]))
     for r in range(0, a.shape[0], step):
         o = out[r:r + step]
@@ -68,7 +69,7 @@ def raised(mag: torch.Tensor, scale: torch.Tensor) -> torch.Tensor:
     return torch.where(mag > 0, torch.maximum(mag, scale * 2.0 ** -6), mag)
 
 
-def matmul(a, sa, w, sw, with_cut=True):
+def matmul(a, sa, w, sw, with_cut=True, dtype=torch.float32):
     """(y, tol) of moe_fp8_matmul: one rounding to bf16 (2^-8 |y|), fp32 additions (each off by at
     most 2 eps of the magnitudes, 128 a block, its scaling and the blocks' sum), and the cut."""
     N, K = w.shape
@@ -77,7 +78,7 @@ def matmul(a, sa, w, sw, with_cut=True):
     y, mag = A @ W.t(), A.abs() @ W.t().abs()
     err = (2 * BLOCK + -(-K // BLOCK) + 20) * EPS * mag
     if with_cut:
-        err = err + cut(raised(A.abs(), fa.abs()), raised(W.abs(), fw.abs()))
+        err = err + cut(raised(A.abs(), fa.abs()), raised(W.abs(), fw.abs()), dtype)
     return y, 2.0 ** -8 * y.abs() + (1 + 2.0 ** -8) * err
 
 

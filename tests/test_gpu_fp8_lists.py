@@ -58,3 +58,16 @@ def test_ffn_several_tiles_per_unit(T, H, I, E, k, zipf):
     ref = y.clone()
     assert torch.equal(c.run(), ref)
     assert bool((ref != MARK).any(1).all())
+
+
+@pytest.mark.parametrize("T,H,I,E,k,zipf", [
+    (4100, 256, 512, 4, 2, None), (4096, 512, 384, 8, 4, 1.4), (4100, 1024, 1280, 8, 4, 1.0),
+    (2100, 2048, 1408, 6, 4, None)])
+def test_ffn_tiles_on_ordinary_values(T, H, I, E, k, zipf):
+    """Normal x and codes over the range, whose products the E4M3 MFMA cuts: gate and up sums
+    within its bound, every row."""
+    flush(f"[ffn fp8 lists, wide] T={T} H={H} I={I} E={E} k={k}")
+    c = Layer(T, H, I, E, k, seed=T + H + 1, zipf=zipf, wide=True)
+    assert _gateup_tiles(c) > 128
+    c.run()
+    _check_ffn(c, gateup_cut=True)
