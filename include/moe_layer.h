@@ -359,8 +359,12 @@ int moe_fp8_quantize(const uint16_t* x, int32_t T, int32_t K, uint8_t* codes, fl
  *            segment are left as they were.  Both NULL with E = 1: every row.
  *            Segments must lie in [0, M).
  *   y        device bf16 [M][N] (out)
- * Scales may be any fp32 values (not only moe_fp8_quantize's).  N >= 1; K a
- * multiple of 16; N, K <= 65536, N * K < 2^32, 1 <= E <= 1024, M <= 2^27.
+ * Scales need not be moe_fp8_quantize's, and may be negative or 0.  The product
+ * of a row's and a weight block's scale is formed first, in fp32: below 2^-126
+ * it loses bits, and where it overflows, the outputs of its row and columns are
+ * infinite or NaN whatever the block holds; a NaN scale makes them NaN.
+ * N >= 1; K a multiple of 16; N, K <= 65536, N * K < 2^32, 1 <= E <= 1024,
+ * M <= 2^27.
  * ws: device, >= moe_fp8_matmul_workspace(M, N, K, E) bytes; may be NULL where
  * that is 0.                                                                 */
 size_t moe_fp8_matmul_workspace(int32_t M, int32_t N, int32_t K, int32_t E);
@@ -378,8 +382,12 @@ int moe_fp8_matmul(const uint8_t* a, const float* a_scale, int32_t M, const uint
  *          without its cut, which would show there
  *   hq   = moe_fp8_quantize's rule applied to fp32 h = SiLU(g) * u
  *   y_perm = bf16(hq W2^T)
- * Arguments as for moe_expert_ffn (W->fmt must be MOE_W_FP8_B128, others
- * return MOE_ERR_UNSUPPORTED).
+ * (products of two scales as in moe_fp8_matmul).  Arguments as for
+ * moe_expert_ffn (W->fmt must be MOE_W_FP8_B128, others return
+ * MOE_ERR_UNSUPPORTED); T*k <= 2^27.  Batches of T*H >= 2^32 take the 16-row
+ * tiles of small ones, which read an expert's weights once per 16 rows, and
+ * return MOE_ERR_UNSUPPORTED where a grid does not hold them (T*k*I or T*k*H of
+ * about 2^33 and more).
  * ws: device, >= moe_expert_ffn_fp8_workspace(W, T, k).                      */
 size_t moe_expert_ffn_fp8_workspace(const moe_experts* W, int32_t T, int32_t k);
 int moe_expert_ffn_fp8(const moe_experts* W, const int32_t* slot_of_expert, const uint16_t* x,

@@ -38,15 +38,16 @@ def _product(M, N, K, E, counts, narrow):
     return p.upload()
 
 
-def _check_rows(p, narrow):
+def _check_rows(p, narrow, slack=0.0, dtype=torch.float32):
     seen = torch.zeros(p.M, dtype=torch.bool, device=DEV)
     segs = [(0, p.M, 0)] if not p.E else [(int(p.offsets[e]), int(p.offsets[e] + p.counts[e]), e)
                                          for e in range(p.E) if p.counts[e]]
     a, sa, w, sw = p.d
     for lo, hi, e in segs:
-        y, tol = R.matmul(a[lo:hi], sa[lo:hi], w[e] if p.E else w, sw[e] if p.E else sw, not narrow)
+        y, tol = R.matmul(a[lo:hi], sa[lo:hi], w[e] if p.E else w, sw[e] if p.E else sw, not narrow,
+                          dtype)
         err = (p.y[lo:hi].double() - y).abs()
-        bad = torch.nonzero(~(err <= tol))
+        bad = torch.nonzero(~(err <= tol + slack))
         assert not len(bad), (e, bad[:4].tolist(), len(bad))
         seen[lo:hi] = True
     assert bool((p.y[~seen] == MARK).all())
@@ -102,3 +103,27 @@ def test_a_row_is_the_same_in_any_batch(big, small, N, K):
         moe.moe_fp8_matmul(a, sa, *p.d[2:], y)
         torch.cuda.synchronize()
         assert torch.equal(y, p.y[first:first + small])
+
+
+@pytest.mark.parametrize("M", [6, 40, 300, 1100, 8200])
+def test_scale_products_at_the_ends_of_their_range(M):
+    """Products of two scales up to 2^127 and down to 2^-126: a block of zeros under the largest
+    is nothing, the smallest code there is a finite result, and nothing is lost at the small end."""
+    N, K = 2300, 384
+    p = _product(M, N, K, 0, None, False)
+    a, sa, w, sw = p.d
+    sw[:, 1], sw[:, 2] = 2.0 ** 64, 2.0 ** -26
+    sa[:, 1] = 0.0
+    sa[0, 1], a[0, 128:256] = 2.0 ** 63, 0                  # 2^127, zeros
+    sa[1, 1], a[1, 128:256] = 2.0 ** 63, 0
+    a[1, 131] = 0x01                                        # 2^-9: at most 2^127 * 2^-9 * 448
+    sa[2] = 0.0
+    sa[2, 2] = 2.0 ** -100                                  # 2^-126
+    sa[3] = 0.0                                             # zero scales: zeros
+    sa[M - 1, 1] = -2.0 ** -60                              # negative
+    p.call()
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(p.y).all()) and bool((p.y[3] == 0).all())
+    assert float(p.y[1].float().abs().max()) > 2.0 ** 120
+    # fp32 roundings below 2^-126 are at most 2^-150 each, under 2^10 of them
+    _check_rows(p, False, slack=2.0 ** -140, dtype=torch.float64)
