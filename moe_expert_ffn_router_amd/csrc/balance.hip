@@ -13,8 +13,8 @@
 // R / 4 terms), the waves are added in LDS, and the ids are counted with
 // integer LDS atomics (their order does not matter).  A second kernel
 // adds a sequence's pieces in double in chunk order, a workgroup per sequence and
-// 16 experts, and a third forms the loss.  A batch of one chunk is finished by the
-// first kernel.
+// 16 experts, and a third forms the loss.  A batch of one chunk in up to
+// kOneKernelSeqs sequences is finished by the first kernel.
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -184,7 +184,12 @@ __device__ __forceinline__ void row_softmax(float (&x)[VPL]) {
 }
 
 constexpr int kMaxChunk = 128;  // rows of a chunk at most
-constexpr int kOneKernelSeqs = 256;  // sequences that one workgroup writes out by itself
+// Sequences of one chunk that the first kernel finishes by itself, one after another; more leave
+// the sums to the other two.  us a call, one kernel against three, E = 256 (E = 1024): T = 64, 1
+// sequence 7.2 / 13.7, 2 10.6 / 14.6, 4 19.3 / 15.7, 8 36.7 / 23.5, 64 281 / 134; T = 128, 1 9.4 /
+// 19.2 (18.6 / 33.4), 4 19.3 / 21.6 (25.4 / 37.1), 8 36.6 / 24.3 (32.5 / 42.6), 16 71 / 39 (62 / 54),
+// 64 281 / 134 (235 / 181).
+constexpr int kOneKernelSeqs = 4;
 
 // U rows of a group, NG rows apart from row t on: loads in flight together, with the rows'
 // mask bytes beside them (a masked row is read and dropped: waiting for its mask first
