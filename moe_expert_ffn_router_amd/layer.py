@@ -126,8 +126,9 @@ class MoELayer:
     def balance_loss(self, logits: torch.Tensor, token_mask=None, seq_offsets=None,
                      stream=None) -> dict:
         """Load-balance loss of the batch last routed (self.ids), per sequence, with the
-        per-expert counts and probability sums (moe_balance_loss).  The results belong to
-        `stream`: work on another one waits for it and records its use, as for any tensor of torch."""
+        per-expert counts and probability sums (moe_balance_loss).  The results are
+        memory of `stream`, recorded as used on the current stream too, which may read them
+        once it has waited for `stream`."""
         T, E = logits.shape
         S = 1 if seq_offsets is None else seq_offsets.numel() - 1
         i32 = dict(dtype=torch.int32, device=self.device)
@@ -139,6 +140,9 @@ class MoELayer:
                              device=self.device)
         moe_balance_loss(logits, self.ids[:T * self.k], self.k, r["n_tokens"], r["counts"],
                          r["probs"], r["loss"], ws, token_mask, seq_offsets, stream)
+        if stream is not None:
+            for t in r.values():
+                t.record_stream(torch.cuda.current_stream())
         return r
 
     def route_backward(self, logits: torch.Tensor, d_logits: torch.Tensor, d_topk_w=None,

@@ -73,6 +73,72 @@ def test_balance_loss_results_freed_while_their_stream_works(raw):
 
 
 @pytest.mark.parametrize("raw", [False, True])
+def test_balance_loss_results_read_by_the_current_stream(raw):
+    """The current stream waits, reads the results late, and they are dropped before it has: the
+    caller's stream does not write over them meanwhile."""
+    case = Case(WL)
+    layer = _layer(case)
+    ref = layer.balance_loss(case.logits)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = layer.balance_loss(case.logits, None, None, _handle(s, raw))
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(20_000_000)
+    read = {name: t.clone() for name, t in got.items()}
+    del got
+    with torch.cuda.stream(s):
+        for n in (4, 4 * WL.E, max(moe.moe_balance_loss_workspace(WL.T, WL.E, 1), 256)):
+            for _ in range(4):
+                torch.full((n,), 0x5a, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for name in ref:
+        assert torch.equal(read[name], ref[name]), name
+
+
+def test_handle_of_the_default_stream():
+    """The current stream's raw handle (0) is the current stream."""
+    case = Case(WL)
+    layer = _layer(case)
+    W = layer.weights(case.records)
+    ref = layer.balance_loss(case.logits)
+    layer.expert_ffn(W, case.x, WL.T, None, "fp8")
+    torch.cuda.synchronize()
+    y = layer.y_perm.clone()
+    layer.fp8_ws = None
+    raw = torch.cuda.current_stream().cuda_stream
+    got = layer.balance_loss(case.logits, stream=raw)
+    layer.expert_ffn(W, case.x, WL.T, None, "fp8", raw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[name], ref[name]) for name in ref) and torch.equal(layer.y_perm, y)
+
+
+def test_balance_loss_captured_on_its_stream():
+    """Allocations and records inside a capture; two graphs, replayed with eager work between."""
+    case = Case(WL)
+    layer = _layer(case)
+    ref = layer.balance_loss(case.logits)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.wait_stream(torch.cuda.current_stream())
+            r = layer.balance_loss(case.logits, stream=s)
+            torch.cuda.current_stream().wait_stream(s)
+        runs.append((g, r))
+    for _ in range(3):
+        for g, r in runs:
+            for t in r.values():
+                t.zero_()
+            g.replay()
+            eager = layer.balance_loss(case.logits)
+            torch.cuda.synchronize()
+            for name in ref:
+                assert torch.equal(r[name], ref[name]) and torch.equal(eager[name], ref[name]), name
+
+
+@pytest.mark.parametrize("raw", [False, True])
 def test_fp8_workspace_allocates_on_its_stream(raw):
     case = Case(WL)
     layer = _layer(case)
