@@ -326,6 +326,133 @@ int moe_route_backward(const float* logits, int32_t T, int32_t E, int32_t k, int
                        float* d_logits, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Training the experts.  The pages describe serving and give no training
+ * formula; these are the derivatives of moe_combine and of moe_expert_ffn over
+ * BF16 records, with the steps that stand between them.  A step of the layer:
+ * moe_route, moe_permute, moe_expert_ffn_train, moe_combine; then
+ * moe_combine_backward, moe_expert_ffn_backward, moe_dispatch_backward (the
+ * layer's input) and moe_route_backward (its logits), and moe_clip_grad_norm
+ * over all gradients.  A = T*k assignments a = t*k + j; w[a] = topk_w[t][j].
+ *
+ * moe_dispatch — token rows into expert order, weighted on the way if wanted:
+ *   x_perm[inv_idx[a]] = bf16(w[a] x[t])        (topk_w NULL: a copy of x[t])
+ * An inv_idx outside [0, R) is a dropped assignment here and in the two calls
+ * below: nothing is read or written for it, and its d_topk_w is 0.  Rows of
+ * x_perm that no assignment names are left as they were.  The calls gather
+ * tokens for experts that live elsewhere or outside this library;
+ * moe_expert_ffn and moe_expert_ffn_train gather them by themselves.
+ *   x  device bf16 [T][H];  inv_idx  device int32 [T*k], as from moe_permute
+ *   (no two alike among those in range);  topk_w  device fp32 [T][k] or NULL;
+ *   x_perm  device bf16 [R][H] (out)
+ * H a multiple of 8, 1 <= k <= 16, T*k and R at most 2^27.                   */
+int moe_dispatch(const uint16_t* x, const int32_t* inv_idx, const float* topk_w, int32_t T,
+                 int32_t k, int32_t H, int32_t R, uint16_t* x_perm, moe_stream_t stream);
+
+/* moe_dispatch_backward — its gradient:
+ *   d_x[t]      = bf16( sum_j w[a] d_x_perm[inv_idx[a]] (+ d_add[t]) )
+ *   d_topk_w[a] = <d_x_perm[inv_idx[a]], x[t]>
+ * summed in fp32 in j order, d_add last.  (With topk_w it is also the combine
+ * of rows some of which were dropped.)
+ *   d_x_perm  device bf16 [R][H];  topk_w  as in moe_dispatch, or NULL (1)
+ *   d_add     device bf16 [T][H] or NULL: a gradient of x from elsewhere (the
+ *             shared expert, the residual); d_x may be d_add
+ *   d_topk_w  device fp32 [T][k] (out) or NULL;  x  device bf16 [T][H], read
+ *             for d_topk_w only (else may be NULL)
+ *   d_x       device bf16 [T][H] (out)                                        */
+int moe_dispatch_backward(const uint16_t* d_x_perm, const int32_t* inv_idx, const float* topk_w,
+                          const uint16_t* x, int32_t T, int32_t k, int32_t H, int32_t R,
+                          const uint16_t* d_add, uint16_t* d_x, float* d_topk_w,
+                          moe_stream_t stream);
+
+/* moe_combine_backward — the gradient of moe_combine:
+ *   d_y_perm[inv_idx[a]] = bf16(w[a] d_y[t])
+ *   d_topk_w[a]          = <y_perm[inv_idx[a]], d_y[t]>     (fp32)
+ * (y_shared's gradient is d_y itself.)
+ *   d_y       device bf16 [T][H];  topk_w  device fp32 [T][k]
+ *   y_perm    device bf16 [R][H], read for d_topk_w only (else may be NULL)
+ *   d_y_perm  device bf16 [R][H] (out); may be y_perm itself
+ *   d_topk_w  device fp32 [T][k] (out) or NULL: moe_route_backward's input    */
+int moe_combine_backward(const uint16_t* d_y, const uint16_t* y_perm, const int32_t* inv_idx,
+                         const float* topk_w, int32_t T, int32_t k, int32_t H, int32_t R,
+                         uint16_t* d_y_perm, float* d_topk_w, moe_stream_t stream);
+
+/* moe_expert_ffn_train — moe_expert_ffn over BF16 records, keeping what its
+ * gradient needs:
+ *   g, u      = x_p W_gate[e]^T, x_p W_up[e]^T   (fp32 sums)
+ *   gate_up_p = bf16(g), bf16(u) side by side
+ *   y_perm_p  = bf16( bf16(SiLU(g) u) W_down[e]^T )
+ * Rows in no expert's segment are left as they were, in gate_up and y_perm.
+ *   x           device bf16 [T][H]; row p is x[sorted_idx[p] / k]
+ *   sorted_idx  device int32 [T*k], or NULL: x is device bf16 [T*k][H], its
+ *               rows in expert order already (as moe_dispatch leaves them)
+ *   counts, offsets  device int32 [E], [E+1]; segments within [0, T*k)
+ *   gate_up     device bf16 [T*k][2I] (out);  y_perm  device bf16 [T*k][H] (out)
+ * Other formats return MOE_ERR_UNSUPPORTED, as does T*H >= 2^31 with
+ * sorted_idx; T*k <= 2^27.
+ * ws: device, >= moe_expert_ffn_train_workspace(W, T, k).                    */
+size_t moe_expert_ffn_train_workspace(const moe_experts* W, int32_t T, int32_t k);
+int moe_expert_ffn_train(const moe_experts* W, const uint16_t* x, int32_t T, int32_t k,
+                         const int32_t* counts, const int32_t* offsets, const int32_t* sorted_idx,
+                         uint16_t* gate_up, uint16_t* y_perm, void* ws, size_t ws_bytes,
+                         moe_stream_t stream);
+
+/* Element types of gradients. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 } moe_type;
+
+/* moe_expert_ffn_backward — its gradient, from the kept gate_up = (g, u):
+ *   dh = d_y_p W_down[e],   s = 1 / (1 + e^-g),   h = g s u
+ *   du = dh g s,            dg = dh u s (1 + g (1 - s))
+ *   d_x_perm_p = bf16( dg W_gate[e] + du W_up[e] )
+ *   d_w13[e]   = sum over the rows of e of (dg, du)^T x_p      [2I][H]
+ *   d_w2[e]    = sum over the rows of e of d_y_p^T h           [H][I]
+ * with fp32 sums; h, dg and du are rounded to bf16 as operands.  Each output
+ * may be NULL (not wanted).  An expert without rows gets gradients of 0.
+ *   x, sorted_idx, counts, offsets   as in moe_expert_ffn_train
+ *   gate_up   device bf16 [T*k][2I], as written there
+ *   d_y_perm  device bf16 [T*k][H]
+ *   d_x_perm  device bf16 [T*k][H] (out); rows in no segment are left alone
+ *   d_w13, d_w2  device, of type d_w_type (moe_type) [E][2I][H], [E][H][I] (out)
+ *   accumulate   1: d_w13 and d_w2, which must be fp32, are added to (a sum of
+ *                several batches' gradients in bf16 would round each of them);
+ *                experts without rows are not touched
+ * T = 0 writes zeros to d_w13 and d_w2 (counts are not read).  For a dense
+ * expert (the shared one): E = 1, k = 1, sorted_idx NULL, counts {T},
+ * offsets {0, T}.  Limits as for moe_expert_ffn_train.
+ * ws: device, >= moe_expert_ffn_backward_workspace(W, T, k).                 */
+size_t moe_expert_ffn_backward_workspace(const moe_experts* W, int32_t T, int32_t k);
+int moe_expert_ffn_backward(const moe_experts* W, const uint16_t* x, int32_t T, int32_t k,
+                            const int32_t* counts, const int32_t* offsets,
+                            const int32_t* sorted_idx, const uint16_t* gate_up,
+                            const uint16_t* d_y_perm, uint16_t* d_x_perm, void* d_w13, void* d_w2,
+                            int32_t d_w_type, int32_t accumulate, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/* moe_clip_grad_norm — the norm over all elements of n gradients, and the
+ * gradients clipped by it:
+ *   norm  = sqrt( sum of the squares of all elements )     (64-bit sums)
+ *   scale = min(1, max_norm / (norm + 1e-6))
+ *   clipped_i = scale * grad_i, rounded to grad_i's type
+ * Not finite: an infinite element makes norm inf and scale 0 (finite elements
+ * become 0, infinite ones NaN), a NaN makes both NaN; a caller that skips such
+ * steps looks at norm.
+ *   grads    host array of n device pointers, aligned to their element only;
+ *            numel  host int64 [n] (0 allowed);  types  host int32 [n], moe_type
+ *   max_norm >= 0 (infinity: no clipping)
+ *   clipped  host array of n device pointers, of the gradients' types, or NULL
+ *            (only the norm is wanted); clipped[i] may be grads[i] (in place;
+ *            with scale 1 it is not touched).  Outputs must not overlap each
+ *            other or any other gradient.
+ *   norm_scale  device fp32 [2] (out): norm, scale
+ * The arrays are read before the call returns; the pointers travel as kernel
+ * arguments (nothing is copied to the device, so a captured graph replays the
+ * same tensors).  n <= 65536.
+ * ws: device, >= moe_clip_grad_norm_workspace(n).                            */
+size_t moe_clip_grad_norm_workspace(int32_t n);
+int moe_clip_grad_norm(int32_t n, const void* const* grads, const int64_t* numel,
+                       const int32_t* types, float max_norm, void* const* clipped,
+                       float* norm_scale, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * FP8 products with a scale for each block of 128 (guide, "CPU layer split"
  * lists fp8 experts; the weight layout is MOE_W_FP8_B128's, the activations
  * are E4M3 here instead of bf16).

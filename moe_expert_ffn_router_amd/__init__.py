@@ -109,6 +109,17 @@ _SIGS = {
                                         _sz, _p]),
     "moe_route_backward": (ctypes.c_int, [_p, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _i32, _p,
                                           _p, _p, _p, _p]),
+    "moe_dispatch": (ctypes.c_int, [_p, _p, _p, _i32, _i32, _i32, _i32, _p, _p]),
+    "moe_dispatch_backward": (ctypes.c_int, [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _p, _p, _p, _p]),
+    "moe_combine_backward": (ctypes.c_int, [_p, _p, _p, _p, _i32, _i32, _i32, _i32, _p, _p, _p]),
+    "moe_expert_ffn_train_workspace": (_sz, [ctypes.POINTER(Experts), _i32, _i32]),
+    "moe_expert_ffn_train": (ctypes.c_int, [ctypes.POINTER(Experts), _p, _i32, _i32, _p, _p, _p, _p,
+                                            _p, _p, _sz, _p]),
+    "moe_expert_ffn_backward_workspace": (_sz, [ctypes.POINTER(Experts), _i32, _i32]),
+    "moe_expert_ffn_backward": (ctypes.c_int, [ctypes.POINTER(Experts), _p, _i32, _i32, _p, _p, _p,
+                                               _p, _p, _p, _p, _p, _i32, _i32, _p, _sz, _p]),
+    "moe_clip_grad_norm_workspace": (_sz, [_i32]),
+    "moe_clip_grad_norm": (ctypes.c_int, [_i32, _p, _p, _p, ctypes.c_float, _p, _p, _p, _sz, _p]),
     "moe_fp8_quantize": (ctypes.c_int, [_p, _i32, _i32, _p, _p, _p]),
     "moe_fp8_matmul_workspace": (_sz, [_i32, _i32, _i32, _i32]),
     "moe_fp8_matmul": (ctypes.c_int, [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _i32, _p, _p, _sz,
@@ -603,6 +614,152 @@ def moe_route_backward(logits, k: int, topk_ids, topk_w, d_topk_w, n_tokens, cou
         _opt(n_tokens, "n_tokens", _I32T, S, dev), _opt(counts, "counts", _I32T, S * E, dev),
         _opt(d_loss, "d_loss", _F32, S, dev), _arg(d_logits, "d_logits", _F32, T * E, dev),
         _stream_on(stream, dev)), "moe_route_backward")
+
+
+# ---------------------------------------------------------------------------
+# Training the experts.
+# ---------------------------------------------------------------------------
+_GRAD_TYPE = {torch.bfloat16: 0, torch.float32: 1}   # moe_type
+
+
+def _row_shapes(rows, rows_name: str, perm, perm_name: str) -> tuple[int, int, int]:
+    """(T, H, R) of token rows [T][H] and of rows in expert order [R][H]."""
+    T, H = _matrix(rows, rows_name)
+    R, H2 = _matrix(perm, perm_name)
+    if H2 != H:
+        raise ValueError(f"{perm_name}: rows of {H2}, expected {H}")
+    return T, H, R
+
+
+def moe_dispatch(x, inv_idx, k: int, x_perm, topk_w=None, stream=None) -> None:
+    """Token rows into expert order, weighted if topk_w is given (see the header)."""
+    T, H, R = _row_shapes(x, "x", x_perm, "x_perm")
+    dev = _device_of(x, "x")
+    _check(_lib.moe_dispatch(
+        _arg(x, "x", _BF16, None, dev), _arg(inv_idx, "inv_idx", _I32T, T * k, dev),
+        _opt(topk_w, "topk_w", _F32, T * k, dev), T, k, H, R,
+        _arg(x_perm, "x_perm", _BF16, None, dev), _stream_on(stream, dev)), "moe_dispatch")
+
+
+def moe_dispatch_backward(d_x_perm, inv_idx, k: int, d_x, topk_w=None, d_add=None, x=None,
+                          d_topk_w=None, stream=None) -> None:
+    """Gradient of moe_dispatch: d_x, and d_topk_w where it is given (with x; see the header)."""
+    T, H, R = _row_shapes(d_x, "d_x", d_x_perm, "d_x_perm")
+    dev = _device_of(d_x, "d_x")
+    _check(_lib.moe_dispatch_backward(
+        _arg(d_x_perm, "d_x_perm", _BF16, None, dev), _arg(inv_idx, "inv_idx", _I32T, T * k, dev),
+        _opt(topk_w, "topk_w", _F32, T * k, dev), _opt(x, "x", _BF16, T * H, dev), T, k, H, R,
+        _opt(d_add, "d_add", _BF16, T * H, dev), _arg(d_x, "d_x", _BF16, None, dev),
+        _opt(d_topk_w, "d_topk_w", _F32, T * k, dev), _stream_on(stream, dev)),
+        "moe_dispatch_backward")
+
+
+def moe_combine_backward(d_y, inv_idx, topk_w, k: int, d_y_perm, y_perm=None, d_topk_w=None,
+                         stream=None) -> None:
+    """Gradient of moe_combine: d_y_perm (may be y_perm), and d_topk_w where it is given (with
+    y_perm; see the header)."""
+    T, H, R = _row_shapes(d_y, "d_y", d_y_perm, "d_y_perm")
+    dev = _device_of(d_y, "d_y")
+    _check(_lib.moe_combine_backward(
+        _arg(d_y, "d_y", _BF16, None, dev), _opt(y_perm, "y_perm", _BF16, R * H, dev),
+        _arg(inv_idx, "inv_idx", _I32T, T * k, dev), _arg(topk_w, "topk_w", _F32, T * k, dev), T, k, H,
+        R, _arg(d_y_perm, "d_y_perm", _BF16, None, dev), _opt(d_topk_w, "d_topk_w", _F32, T * k, dev),
+        _stream_on(stream, dev)), "moe_combine_backward")
+
+
+def _at_least(t, name: str, dtype, need: int, dev) -> int | None:
+    """_arg for a buffer that may be longer than the call needs."""
+    p = _arg(t, name, dtype, None, dev)
+    if t.numel() < need:
+        raise ValueError(f"{name}: {t.numel()} elements, expected at least {need}")
+    return p
+
+
+def _ffn_args(W: Experts, x, T: int, k: int, counts, offsets, sorted_idx, dev):
+    A = T * k
+    return (_at_least(x, "x", _BF16, (T if sorted_idx is not None else A) * W.H, dev), T, k,
+            _at_least(counts, "counts", _I32T, W.E, dev),
+            _at_least(offsets, "offsets", _I32T, W.E + 1, dev),
+            None if sorted_idx is None else _at_least(sorted_idx, "sorted_idx", _I32T, A, dev))
+
+
+def moe_expert_ffn_train_workspace(W: Experts, T: int, k: int) -> int:
+    return int(_lib.moe_expert_ffn_train_workspace(ctypes.byref(W), T, k))
+
+
+def moe_expert_ffn_train(W: Experts, x, T: int, k: int, counts, offsets, sorted_idx, gate_up, y_perm,
+                         ws, stream=None) -> None:
+    """moe_expert_ffn over BF16 records that keeps gate_up [T*k][2I] for the gradient;
+    sorted_idx None: x holds the rows in expert order.  The buffers may be longer than T rows
+    need (as MoELayer's are)."""
+    dev = _device_of(x, "x")
+    A = T * k
+    _check(_lib.moe_expert_ffn_train(
+        ctypes.byref(W), *_ffn_args(W, x, T, k, counts, offsets, sorted_idx, dev),
+        _at_least(gate_up, "gate_up", _BF16, A * 2 * W.I, dev),
+        _at_least(y_perm, "y_perm", _BF16, A * W.H, dev), _arg(ws, "ws", _U8, None, dev), ws.numel(),
+        _stream_on(stream, dev)), "moe_expert_ffn_train")
+
+
+def moe_expert_ffn_backward_workspace(W: Experts, T: int, k: int) -> int:
+    return int(_lib.moe_expert_ffn_backward_workspace(ctypes.byref(W), T, k))
+
+
+def moe_expert_ffn_backward(W: Experts, x, T: int, k: int, counts, offsets, sorted_idx, gate_up,
+                            d_y_perm, ws, d_x_perm=None, d_w13=None, d_w2=None,
+                            accumulate: bool = False, stream=None) -> None:
+    """Gradient of moe_expert_ffn_train: of its rows (d_x_perm) and of the weights (d_w13
+    [E][2I][H] and d_w2 [E][H][I], both bf16 or both fp32; accumulate adds to fp32 ones).  Any
+    of the three may be None (see the header)."""
+    dev = _device_of(x, "x")
+    A = T * k
+    types = {t.dtype for t in (d_w13, d_w2) if t is not None}
+    if len(types) > 1 or not types <= set(_GRAD_TYPE):
+        raise ValueError("d_w13, d_w2: both bfloat16 or both float32 expected")
+    wt = types.pop() if types else _BF16
+    _check(_lib.moe_expert_ffn_backward(
+        ctypes.byref(W), *_ffn_args(W, x, T, k, counts, offsets, sorted_idx, dev),
+        _at_least(gate_up, "gate_up", _BF16, A * 2 * W.I, dev),
+        _at_least(d_y_perm, "d_y_perm", _BF16, A * W.H, dev),
+        None if d_x_perm is None else _at_least(d_x_perm, "d_x_perm", _BF16, A * W.H, dev),
+        _opt(d_w13, "d_w13", wt, W.E * 2 * W.I * W.H, dev), _opt(d_w2, "d_w2", wt, W.E * W.H * W.I, dev),
+        _GRAD_TYPE[wt], int(accumulate), _arg(ws, "ws", _U8, None, dev), ws.numel(),
+        _stream_on(stream, dev)), "moe_expert_ffn_backward")
+
+
+def moe_clip_grad_norm_workspace(n: int) -> int:
+    return int(_lib.moe_clip_grad_norm_workspace(n))
+
+
+def _pointers(ts, like, name: str, dev):
+    """ctypes array of the tensors' addresses; each checked against its counterpart in `like`."""
+    for i, (t, o) in enumerate(zip(ts, like)):
+        if t.dtype is not o.dtype or t.numel() != o.numel() or not t.is_contiguous() \
+                or t.get_device() != dev:
+            raise ValueError(f"{name}[{i}]: a contiguous {o.dtype} tensor of {o.numel()} elements on "
+                             f"cuda:{dev} expected")
+    return (_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def moe_clip_grad_norm(grads, max_norm: float, norm_scale, ws, clipped=None, stream=None) -> None:
+    """Norm over all gradients (a list of bf16 and fp32 tensors) and the scale that clips it to
+    max_norm, into norm_scale [2]; with `clipped` (tensors like the gradients, or the
+    gradients themselves) also the clipped gradients (see the header)."""
+    dev = _device_of(norm_scale, "norm_scale")
+    n = len(grads)
+    try:
+        types = (_i32 * n)(*[_GRAD_TYPE[t.dtype] for t in grads])
+    except KeyError as e:
+        raise ValueError(f"grads: dtype {e.args[0]}, expected bfloat16 or float32") from None
+    if clipped is not None and len(clipped) != n:
+        raise ValueError(f"clipped: {len(clipped)} tensors, expected {n}")
+    src = _pointers(grads, grads, "grads", dev)
+    dst = src if clipped is grads else None if clipped is None else _pointers(clipped, grads, "clipped",
+                                                                             dev)
+    _check(_lib.moe_clip_grad_norm(
+        n, src, (_i64 * n)(*[t.numel() for t in grads]), types, max_norm, dst,
+        _arg(norm_scale, "norm_scale", _F32, 2, dev), _arg(ws, "ws", _U8, None, dev), ws.numel(),
+        _stream_on(stream, dev)), "moe_clip_grad_norm")
 
 
 def moe_fp8_quantize(x, codes, scales, stream=None) -> None:

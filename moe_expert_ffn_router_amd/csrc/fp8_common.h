@@ -154,6 +154,7 @@ inline int64_t row_tiles_bound(int64_t A, int64_t E, int64_t BM) {
 #ifdef MOE_DEBUG
 uint32_t dbg_take_balance();
 uint32_t dbg_take_fp8();
+uint32_t dbg_take_train();
 #endif
 
 }  // namespace moe

@@ -79,7 +79,7 @@ int moe_debug_take(uint32_t* flags) {
   if (!flags) return moe::set_error(MOE_ERR_INVALID_ARG, "moe_debug_take: flags is NULL");
 #ifdef MOE_DEBUG
   *flags = moe::dbg_take_ffn() | moe::dbg_take_decode() | moe::dbg_take_combine() |
-           moe::dbg_take_balance() | moe::dbg_take_fp8();
+           moe::dbg_take_balance() | moe::dbg_take_fp8() | moe::dbg_take_train();
   return MOE_OK;
 #else
   *flags = 0;

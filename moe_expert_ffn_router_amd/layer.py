@@ -17,7 +17,9 @@ import numpy as np
 import torch
 
 from . import (Experts, experts, moe_balance_loss, moe_balance_loss_workspace, moe_combine,
-               moe_expert_ffn, moe_expert_ffn_fp8, moe_expert_ffn_fp8_workspace,
+               moe_combine_backward, moe_dispatch_backward, moe_expert_ffn, moe_expert_ffn_backward,
+               moe_expert_ffn_backward_workspace, moe_expert_ffn_fp8, moe_expert_ffn_fp8_workspace,
+               moe_expert_ffn_train, moe_expert_ffn_train_workspace,
                moe_expert_ffn_workspace, moe_expert_ffn_hybrid_host_bytes,
                moe_expert_ffn_streamed_workspace, moe_route_backward,
                moe_forward_decode, moe_forward_decode_supported, moe_forward_decode_workspace,
@@ -64,6 +66,7 @@ class MoELayer:
         self._probe = probe
         self.stream_ws = None                 # streamed cache path: made on first use
         self.fp8_ws = None                    # variant "fp8": made on first use
+        self.train = None                     # training buffers: made on first use
         self.counts_host = torch.zeros(E, dtype=torch.int32).pin_memory()
         self.plan_out = tuple(torch.zeros(E, dtype=torch.int32) for _ in range(3))
         self.hybrid_out = tuple(torch.zeros(E, dtype=torch.int32) for _ in range(4))
@@ -156,6 +159,87 @@ class MoELayer:
                            b.get("n_tokens"), b.get("counts"), d_loss, d_logits, self.renorm,
                            token_mask, seq_offsets, stream)
         return d_logits
+
+    # -- training the experts -------------------------------------------------
+    def _train_buffers(self, stream) -> dict:
+        """What a training step keeps: the gate and up products, the gradients of the rows in
+        expert order, and the workspace of both directions."""
+        if self.train is None:
+            A, H, I, dev = max(self.T_max * self.k, 1), self.H, self.I, self.device
+            bf = dict(dtype=torch.bfloat16, device=dev)
+            with _on(stream):
+                b = {"gate_up": torch.empty((A, 2 * I), **bf), "d_y_perm": torch.empty((A, H), **bf),
+                     "d_x_perm": torch.empty((A, H), **bf)}
+                size = max(moe_expert_ffn_train_workspace(self._probe, self.T_max, self.k),
+                           moe_expert_ffn_backward_workspace(self._probe, self.T_max, self.k), 256)
+                if self.shared_I:
+                    sp = Experts(0, 1, H, self.shared_I, None, self.shared_stride)
+                    b["shared_gate_up"] = torch.empty((max(self.T_max, 1), 2 * self.shared_I), **bf)
+                    b["shared_counts"], b["shared_offsets"] = _i32(1, dev), _i32(2, dev)
+                    size = max(size, moe_expert_ffn_train_workspace(sp, self.T_max, 1),
+                               moe_expert_ffn_backward_workspace(sp, self.T_max, 1))
+                b["ws"] = torch.empty(size, dtype=torch.uint8, device=dev)
+            self.train = b
+        return self.train
+
+    def forward_train(self, logits: torch.Tensor, x: torch.Tensor, W: Experts,
+                      Ws: Experts | None = None, stream=None) -> torch.Tensor:
+        """The layer's forward over BF16 records, keeping what `backward` needs until the next
+        call on this layer (the routing, the gate and up products, the experts' outputs).  Ws: the
+        shared expert's record."""
+        T = logits.shape[0]
+        assert T <= self.T_max and x.shape == (T, self.H)
+        b = self._train_buffers(stream)
+        self.route_permute(logits, stream)
+        if T == 0:
+            return self.y[:0]
+        moe_expert_ffn_train(W, x, T, self.k, self.counts, self.offsets, self.sorted_idx, b["gate_up"],
+                             self.y_perm, b["ws"], stream)
+        if Ws is not None:
+            with _on(stream):
+                b["shared_counts"].fill_(T)
+                b["shared_offsets"].copy_(torch.arange(2, dtype=torch.int32, device=self.device) * T)
+            moe_expert_ffn_train(Ws, x, T, 1, b["shared_counts"], b["shared_offsets"], None,
+                                 b["shared_gate_up"], self.y_shared, b["ws"], stream)
+        self.combine(T, Ws is not None, stream)
+        return self.y[:T]
+
+    def backward(self, logits: torch.Tensor, x: torch.Tensor, W: Experts, d_y: torch.Tensor,
+                 d_w13=None, d_w2=None, Ws: Experts | None = None, d_s13=None, d_s2=None,
+                 accumulate: bool = False, balance: dict | None = None, d_loss=None, token_mask=None,
+                 seq_offsets=None, stream=None) -> dict:
+        """Gradient of the last forward_train with the same logits, x, W and Ws: writes (or adds to)
+        the weights' gradients that are given, d_s13 and d_s2 being the shared expert's, and
+        returns {"d_x", "d_logits", "d_topk_w"}.  balance, d_loss, token_mask and seq_offsets as
+        for route_backward.  The results are memory of `stream`, as balance_loss's are."""
+        T, E = logits.shape
+        b = self._train_buffers(stream)
+        with _on(stream):
+            r = {"d_x": torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device),
+                 "d_logits": torch.zeros((T, E), dtype=torch.float32, device=self.device),
+                 "d_topk_w": torch.empty((T, self.k), dtype=torch.float32, device=self.device)}
+        A = T * self.k
+        w, inv = self.w[:A], self.inv_idx[:A]
+        d_y_perm, d_x_perm = b["d_y_perm"][:A], b["d_x_perm"][:A]
+        if T:
+            moe_combine_backward(d_y, inv, w, self.k, d_y_perm, self.y_perm[:A], r["d_topk_w"], stream)
+        moe_expert_ffn_backward(W, x, T, self.k, self.counts, self.offsets, self.sorted_idx,
+                                b["gate_up"], d_y_perm, b["ws"], d_x_perm, d_w13, d_w2, accumulate,
+                                stream)
+        d_add = None
+        if Ws is not None:
+            moe_expert_ffn_backward(Ws, x, T, 1, b["shared_counts"], b["shared_offsets"], None,
+                                    b["shared_gate_up"], d_y, b["ws"], r["d_x"], d_s13, d_s2,
+                                    accumulate, stream)
+            d_add = r["d_x"]
+        if T:
+            moe_dispatch_backward(d_x_perm, inv, self.k, r["d_x"], d_add=d_add, stream=stream)
+            self.route_backward(logits, r["d_logits"], r["d_topk_w"], balance, d_loss, token_mask,
+                                seq_offsets, stream)
+        if stream is not None:
+            for t in r.values():
+                t.record_stream(torch.cuda.current_stream())
+        return r
 
     # -- whole layer ----------------------------------------------------------
     def weights(self, base) -> Experts:
