@@ -10,10 +10,18 @@
 // Roundings: h and (dg; du) go to bf16 once, as the operands of the next product; the forward's
 // h comes from the fp32 gate and up sums, the gradient's from the kept bf16 ones.
 //
-// Tiles of BM x 256 outputs on 8 waves, 2 along the rows x 4 along the columns, K in blocks of
-// 64, both operands copied from memory straight into LDS, two stages.  An operand with K
-// contiguous lies as rows of 128 bytes, one with K strided as 64 rows of its tile's columns, read
-// back through the transposing LDS loads.
+// Tiles of 256 x 256 outputs on 4 waves, one per SIMD, 128 x 128 outputs each (all of a wave's
+// 256 accumulation registers): a K step of 16 then reads 8 KB of operands per wave from LDS for 16
+// MFMAs.  The LDS delivers about 117 bytes a clock (measured; 97 through its transposing loads)
+// and takes the copies besides, so 8 waves of 128 x 64 would need it for longer than the MFMAs.
+// K goes in blocks of 64, both operands copied from memory straight into LDS, two stages.  An
+// operand with K contiguous lies as rows of 128 bytes, one with K strided as 64 rows of the tile's
+// columns, read back through the transposing loads.
+//   One barrier per block, in its last K step, by when every wave has read the stage to its end
+// and the next block has landed: the stage is then refilled with the block after the next, whose
+// copies are issued between the MFMAs of that step and the next block's first.
+//   A workgroup owns its compute unit and works through a list of tiles as one sequence of blocks:
+// the next tile's first blocks are copied under the current one's last and its epilogue.
 #include "fp8_common.h"
 #include "lds_copy.h"
 #include "moe_internal.h"
@@ -23,114 +31,63 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short i16x4;
+typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8;
 
-constexpr int kBK = 64;   // K of a block
-constexpr int kBN = 256;  // output columns of a tile
-constexpr int kWM = 2, kWN = 4, kNW = kWM * kWN;
-constexpr int kXcds = 8;
-constexpr int kPanel = 4;  // row tiles that share weights in an XCD's L2
+constexpr int kBK = 64;            // K of a block
+constexpr int kTile = 256;         // rows and columns of a tile
+constexpr int kNW = 4;             // waves: 2 along the rows x 2 along the columns
+constexpr int kXcds = 8, kXcdCus = 32;
+constexpr int kPanel = 4;          // row tiles that share weights in an XCD's L2
+constexpr int kListTiles = 64;     // tiles of one workgroup at most
+constexpr int kOperandB = kTile * kBK * 2;          // bytes of an operand's block
+constexpr int kCopies = kOperandB / 1024 / kNW;     // 1 KB copies of it per wave
+constexpr int kEpiB = 4096;        // per wave: 32 rows of 128 bytes on their way out
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// One operand of a tile in LDS: ROWS x 64 values.  STRIDED: [k][ROWS], 64-byte pieces of a row
-// swizzled by k so that the transposing loads of 4 (k) x 32 values meet distinct banks;
-// else [row][64], 16-byte units swizzled by row.
-template <int ROWS, bool STRIDED>
+// One operand's block in LDS.  STRIDED: [k][256], the 64-byte pieces of a row XORed with k % 4 so
+// that a transposing load's 4 k x 32 values meet distinct banks; else [row][64], 16-byte units
+// XORed by row.
+template <bool STRIDED>
 struct Operand {
-  static constexpr int kBytes = ROWS * kBK * 2;
-  static constexpr int kCopies = kBytes / 1024 / kNW;  // 1 KB copies per wave
-  static constexpr int kRowB = STRIDED ? ROWS * 2 : kBK * 2;
-  static constexpr int kLanes = kRowB / 16;            // lanes (16-byte units) of a row
-  static constexpr int kChunks = kRowB / 64;
-  static_assert(kBytes % (1024 * kNW) == 0, "copies");
+  static constexpr int kRowB = STRIDED ? kTile * 2 : kBK * 2;
+  static constexpr int kLanes = kRowB / 16;  // lanes (16-byte units) of a row
 
-  // row of the stage that this lane's part of copy q fills
+  // row of the block that this lane's part of copy q fills, and which unit of the source's row
   static __device__ __forceinline__ int row_of(int wave, int q, int lane) {
     return (wave * kCopies + q) * (64 / kLanes) + lane / kLanes;
   }
-  // which 16-byte unit of that row's source goes there
   static __device__ __forceinline__ int unit_of(int row, int lane) {
     const int u = lane % kLanes;
-    if constexpr (STRIDED) return (((u >> 2) ^ swz(row)) << 2) | (u & 3);
-    return u ^ a_swz(row);
+    return STRIDED ? (((u >> 2) ^ (row & 3)) << 2) | (u & 3) : u ^ a_swz(row);
   }
-  static __device__ __forceinline__ int swz(int k) {
-    return ((k & 3) ^ (((k >> 3) & 1) << 2)) & (kChunks - 1);
-  }
-  // the 8 values at K = 16 s + 8 (lane / 32) of row (column) block*32 + lane % 32
-  static __device__ __forceinline__ bf16x8 frag(const uint8_t* st, int block, int s, int lane) {
+  // This lane's address of subtile i (32 rows, of 4 from `first`) at K step 0; the step's own part
+  // is applied by frag.
+  static __device__ __forceinline__ int addr(int first, int i, int lane) {
     if constexpr (STRIDED) {
-      const int i = lane & 15, hh = lane >> 5;
-      const int k = 16 * s + 8 * hh + (i >> 2);
-      const uint8_t* p = st + k * kRowB + ((block ^ swz(k)) << 6) + ((lane >> 4) & 1) * 32 + (i & 3) * 8;
+      const int l = lane & 15, k = 8 * (lane >> 5) + (l >> 2);
+      return k * kRowB + (((first + i) ^ (k & 3)) << 6) + ((lane >> 4) & 1) * 32 + (l & 3) * 8;
+    } else {
+      const int r = (first + i) * 32 + (lane & 31);
+      return r * kRowB + (((lane >> 5) ^ a_swz(r)) << 4);
+    }
+  }
+  // The 8 values at K = 16 s + 8 (lane / 32) of the subtile's row (column) lane % 32.
+  static __device__ __forceinline__ bf16x8 frag(const uint8_t* block, int addr, int s) {
+    if constexpr (STRIDED) {
       using lds_t = __attribute__((address_space(3))) i16x4;
+      const uint8_t* p = block + addr + s * 16 * kRowB;
       const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)p);
       const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(p + 4 * kRowB));
-      typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8;
       const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       return __builtin_bit_cast(bf16x8, v);
     } else {
-      const int r = block * 32 + (lane & 31);
-      return *reinterpret_cast<const bf16x8*>(st + r * kRowB + (((2 * s + (lane >> 5)) ^ a_swz(r)) << 4));
+      return *reinterpret_cast<const bf16x8*>(block + (addr ^ (s * 32)));
     }
   }
 };
-
-template <int BM, bool AT, bool BT>
-struct Stage {
-  uint8_t a[Operand<BM, AT>::kBytes];
-  uint8_t b[Operand<kBN, BT>::kBytes];
-};
-
-// acc += the products of one block
-template <int BM, bool AT, bool BT>
-__device__ __forceinline__ void multiply(const Stage<BM, AT, BT>& st, int mh, int nh, int lane,
-                                         f32x16 (&acc)[BM / 64][2]) {
-  constexpr int MI = BM / 64;
-  bf16x8 af[2][MI], bf[2][2];
-  auto load = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i) af[s & 1][i] = Operand<BM, AT>::frag(st.a, mh * MI + i, s, lane);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) bf[s & 1][j] = Operand<kBN, BT>::frag(st.b, nh * 2 + j, s, lane);
-  };
-  load(0);
-#pragma unroll
-  for (int s = 0; s < kBK / 16; ++s) {
-    if (s + 1 < kBK / 16) load(s + 1);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(bf[s & 1][j], af[s & 1][i], acc[i][j]);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-}
-
-// Value 4q + r of acc[i][j] is output row 32 (mh MI + i) + lane % 32, column
-// 32 (2 nh + j) + 8q + 4 (lane / 32) + r of the tile.
-__device__ __forceinline__ void put4(uint16_t* p, const float* v) {
-  *reinterpret_cast<uint2*>(p) = uint2{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3])};
-}
-
-struct TrainArgs {
-  int E, H, I, k, A;
-  const int* counts;
-  const int* offsets;
-  const int* sorted_idx;  // rows of the gathered operand, NULL: in expert order
-  const uint8_t* w;       // weights of expert 0
-  int64_t stride;         // bytes between experts
-  const uint8_t* a;       // bf16 [rows][K]
-  int K, N;               // reduction length, output columns
-  int nnb;                // column blocks
-  uint16_t* out;          // rows: [A][N]; gated: h
-  uint16_t* out2;         // gated: gate_up; dswiglu: (dg; du)
-  const uint16_t* gu;     // dswiglu: gate_up
-};
-
-enum { kPlain, kGated, kDswiglu };
 
 // v-th tile of mt row tiles x nnb column blocks: panels of kPanel row tiles, column by column
 __device__ __forceinline__ void panel_tile(int v, int mt, int nnb, int& tile, int& nb) {
@@ -140,256 +97,567 @@ __device__ __forceinline__ void panel_tile(int v, int mt, int nnb, int& tile, in
   tile = panel * kPanel + r - nb * rows;
 }
 
-template <int BM, int MODE, bool BT>
-__global__ __launch_bounds__(64 * kNW) void train_rows_kernel(TrainArgs p) {
-  constexpr int MI = BM / 64;
-  constexpr int COLS = MODE == kGated ? kBN / 2 : kBN;
-  using OA = Operand<BM, false>;
-  using OB = Operand<kBN, BT>;
-  __shared__ Stage<BM, false, BT> st[2];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int mh = wave / kWN, nh = wave % kWN;
-  RowTiles<BM> rt;
-  const int mt = rt.load(p.counts, p.offsets, p.E, lane);
-  const int G = mt * p.nnb, per = (G + kXcds - 1) / kXcds;
-  const int x = (int)blockIdx.x % kXcds, i0 = (int)blockIdx.x / kXcds;
-  const int v = x * per + i0;
-  if (i0 >= per || v >= G) return;
-  int tile, nb;
-  panel_tile(v, mt, p.nnb, tile, nb);
-  RowTile t = rt.at(tile);
-  dbg_segment(t.row0, t.rows, p.A);
-  if (t.rows <= 0) return;  // only where the debug check took the tile's rows away
-  const int K = p.K, nblk = K / kBK;
+enum Kind { kDown, kGateUp, kDh, kDx, kWeights };
 
-  const uint8_t* ab = p.sorted_idx ? p.a : p.a + (size_t)t.row0 * K * 2;
-  const uint8_t* wb = p.w + (size_t)t.e * p.stride;
-  uint32_t ao[OA::kCopies], bo[OB::kCopies];
-#pragma unroll
-  for (int q = 0; q < OA::kCopies; ++q) {
-    const int lr = OA::row_of(wave, q, lane), r = min(lr, t.rows - 1);
-    const uint32_t src = p.sorted_idx
-        ? (uint32_t)(dbg_clamp(p.sorted_idx[t.row0 + r], p.A, kDbgSorted) / p.k) : (uint32_t)r;
-    ao[q] = src * (uint32_t)(K * 2) + (uint32_t)OA::unit_of(lr, lane) * 16;
-  }
-#pragma unroll
-  for (int q = 0; q < OB::kCopies; ++q) {
-    const int lr = OB::row_of(wave, q, lane), u = OB::unit_of(lr, lane);
-    if constexpr (BT) {  // [K][N]: lr is k, the unit 8 columns
-      bo[q] = (uint32_t)lr * (uint32_t)(p.N * 2) + (uint32_t)min(nb * kBN + u * 8, p.N - 8) * 2;
-    } else if constexpr (MODE == kGated) {  // a wave's 64 weight rows: 32 gate rows, then their up rows
-      const int col = min(nb * COLS + (lr >> 6) * 32 + (lr & 31), p.N - 1);
-      bo[q] = (uint32_t)((lr & 32) ? p.I + col : col) * (uint32_t)(K * 2) + (uint32_t)u * 16;
-    } else {
-      bo[q] = (uint32_t)min(nb * kBN + lr, p.N - 1) * (uint32_t)(K * 2) + (uint32_t)u * 16;
-    }
-  }
-  const size_t bstep = BT ? (size_t)kBK * p.N * 2 : (size_t)kBK * 2;
-  auto issue = [&](int c) {
-    Stage<BM, false, BT>& S = st[c & 1];
-#pragma unroll
-    for (int q = 0; q < OA::kCopies; ++q)
-      dma16(ab + (size_t)c * kBK * 2, ao[q], S.a + (wave * OA::kCopies + q) * 1024);
-#pragma unroll
-    for (int q = 0; q < OB::kCopies; ++q)
-      dma16(wb + c * bstep, bo[q], S.b + (wave * OB::kCopies + q) * 1024);
-  };
-  f32x16 acc[MI][2];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  issue(0);
-  for (int c = 0; c < nblk; ++c) {
-    MOE_DMA_SYNC(0);
-    if (c + 1 < nblk) issue(c + 1);
-    multiply<BM, false, BT>(st[c & 1], mh, nh, lane, acc);
-  }
-
-  const int l32 = lane & 31, hh = lane >> 5;
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int lr = (mh * MI + i) * 32 + l32;
-    if (lr >= t.rows) continue;
-    const size_t row = (size_t)(t.row0 + lr);
-    if constexpr (MODE == kGated) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = nb * COLS + nh * 32 + 8 * q + 4 * hh;
-        if (col >= p.N) continue;
-        float g[4], u[4], h[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          g[r] = acc[i][0][4 * q + r];
-          u[r] = acc[i][1][4 * q + r];
-          h[r] = swiglu(g[r], u[r]);
-        }
-        put4(p.out + row * p.I + col, h);
-        put4(p.out2 + row * 2 * p.I + col, g);
-        put4(p.out2 + row * 2 * p.I + p.I + col, u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = nb * kBN + (nh * 2 + j) * 32 + 8 * q + 4 * hh;
-          if (col >= p.N) continue;
-          if constexpr (MODE == kPlain) {
-            float o[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = acc[i][j][4 * q + r];
-            put4(p.out + row * p.N + col, o);
-          } else {
-            const uint2 gb = *reinterpret_cast<const uint2*>(p.gu + row * 2 * p.I + col);
-            const uint2 ub = *reinterpret_cast<const uint2*>(p.gu + row * 2 * p.I + p.I + col);
-            const uint32_t gw[2] = {gb.x, gb.y}, uw[2] = {ub.x, ub.y};
-            float h[4], dg[4], du[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float g = __uint_as_float(r & 1 ? gw[r / 2] & 0xffff0000u : gw[r / 2] << 16);
-              const float u = __uint_as_float(r & 1 ? uw[r / 2] & 0xffff0000u : uw[r / 2] << 16);
-              const float dh = acc[i][j][4 * q + r];
-              const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f));
-              h[r] = g * s * u;
-              du[r] = dh * (g * s);
-              dg[r] = dh * u * (s * fmaf(g, 1.f - s, 1.f));
-            }
-            put4(p.out + row * p.I + col, h);
-            put4(p.out2 + row * 2 * p.I + col, dg);
-            put4(p.out2 + row * 2 * p.I + p.I + col, du);
-          }
-        }
-    }
-  }
-}
-
-struct WgradArgs {
-  int E, k, A;
-  const int* counts;      // NULL: no expert has rows
+struct TrainArgs {
+  int E, I, k, A;
+  const int* counts;
   const int* offsets;
-  const int* sorted_idx;  // rows of b, NULL: in expert order
-  const uint8_t* a;       // bf16 [A][M]
-  const uint8_t* b;       // bf16 [A][N], or gathered
-  int M, N, mt, nt;
-  void* out;              // [E][M][N]
+  const int* sorted_idx;   // rows of the gathered operand (a; weights: b), NULL: in expert order
+  const uint8_t* a;        // bf16 [rows][K]; weights: [rows][M]
+  const uint8_t* b;        // weights of expert 0; kWeights: bf16 [rows][N]
+  int64_t stride;          // bytes between experts
+  int M, N, K;             // M: kWeights' output rows; N: output columns (kGateUp: I); K: summed over
+  int mt, nnb;             // kWeights: row tiles of an expert; column blocks
+  void* out;               // [A][N]; kGateUp, kDh: h [A][I]; kWeights: [E][M][N]
+  uint16_t* out2;          // kGateUp: gate_up; kDh: (dg; du)
+  const uint16_t* gu;      // kDh: gate_up
+  uint32_t k_magic;        // floor(2^32 / k) + 1: a / k for k > 1 and a < 2^27 as a 64-bit product's high word
 };
 
-// accumulate: out += (fp32 only)
-template <bool F32>
-__global__ __launch_bounds__(64 * kNW) void train_weights_kernel(WgradArgs p, int accumulate) {
-  constexpr int BM = 256, MI = BM / 64;
-  using OA = Operand<BM, true>;
-  using OB = Operand<kBN, true>;
-  __shared__ Stage<BM, true, true> st[2];
+__device__ __forceinline__ uint32_t token_of(uint32_t a, const TrainArgs& p) {
+  return p.k == 1 ? a : __umulhi(a, p.k_magic);
+}
+
+struct TrainLds {
+  uint8_t a[2][kOperandB];
+  uint8_t b[2][kOperandB];
+  uint8_t epi[kNW][kEpiB];
+  __attribute__((aligned(16))) int list[kListTiles][4];
+  int src[4][kTile];  // gathered rows: of a tile ([tile % 2]); kWeights: of a block ([block % 4][64])
+};
+static_assert(sizeof(TrainLds) <= 160 * 1024, "LDS");
+
+// 32 x 32 fp32 or 32 x 64 bf16 values from the MFMA's layout to rows: 8 lanes per row, 16 bytes
+// each, rows lane / 8 + 8 r.  A wave's own 4 KB of LDS, whose accesses stay in order.
+__device__ __forceinline__ int epi_at(int row, int unit) {
+  return row * 128 + ((unit ^ ((row >> 1) & 7)) << 4);
+}
+__device__ __forceinline__ void epi_put16(uint8_t* e, int lane, int unit, uint4 v) {
+  *reinterpret_cast<uint4*>(e + epi_at(lane & 31, unit)) = v;
+}
+__device__ __forceinline__ void epi_put8(uint8_t* e, int lane, int unit, uint2 v) {
+  *reinterpret_cast<uint2*>(e + epi_at(lane & 31, unit) + (lane >> 5) * 8) = v;
+}
+__device__ __forceinline__ uint4 epi_get(const uint8_t* e, int lane, int r) {
+  return *reinterpret_cast<const uint4*>(e + epi_at((lane >> 3) + 8 * r, lane & 7));
+}
+
+// Keeps accumulators in their registers up to here: without it the compiler moves all 256 to
+// others as the loop ends, and spills.
+__device__ __forceinline__ void keep(f32x16& v) { asm volatile("" : "+a"(v)); }
+
+// Value 4q + r of acc[i][j] is output row 32 i + lane % 32, column 32 j + 8q + 4 (lane / 32) + r of
+// the wave's 128 x 128.
+__device__ __forceinline__ uint2 pack4(const f32x16& v, int q) {
+  return uint2{bf16_pack2(v[4 * q], v[4 * q + 1]), bf16_pack2(v[4 * q + 2], v[4 * q + 3])};
+}
+
+template <Kind KIND, bool F32>
+__global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, int accumulate) {
+  constexpr bool W = KIND == kWeights;
+  constexpr bool AT = W, BT = W || KIND == kDh || KIND == kDx;
+  constexpr int COLS = KIND == kGateUp ? kTile / 2 : kTile;
+  using OA = Operand<AT>;
+  using OB = Operand<BT>;
+  __shared__ TrainLds lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int mh = wave / kWN, nh = wave % kWN;
-  const int per_e = p.mt * p.nt;
-  const int e = (int)(blockIdx.x / (unsigned)per_e), v = (int)(blockIdx.x % (unsigned)per_e);
-  const int mb = v / p.nt, nb = v % p.nt;
-  int n = p.counts ? p.counts[e] : 0, row0 = p.counts ? p.offsets[e] : 0;
-  dbg_segment(row0, n, p.A);
-  n = __builtin_amdgcn_readfirstlane(n);
-  row0 = __builtin_amdgcn_readfirstlane(row0);
-  if (n <= 0 && accumulate) return;
-  const int nblk = n > 0 ? (n + kBK - 1) / kBK : 0;
+  const int mh = wave >> 1, nh = wave & 1;
 
-  int cola[OA::kCopies], colb[OB::kCopies];
+  // -- this workgroup's tiles: (expert, first row, rows, column block | row block << 16) -----------
+  int mine;
+  {
+    const int x = (int)blockIdx.x % kXcds, i0 = (int)blockIdx.x / kXcds;
+    const int NWG = (int)gridDim.x / kXcds;
+    int* before = reinterpret_cast<int*>(lds.a);  // [E + 1]: row tiles before each expert
+    int mt = 0;
+    if constexpr (!W) {
+      if (wave == 0) {
+        RowTiles<kTile> t;
+        const int total = t.load(p.counts, p.offsets, p.E, lane);
+        int run = t.upto - t.mine;
 #pragma unroll
-  for (int q = 0; q < OA::kCopies; ++q)
-    cola[q] = min(mb * BM + OA::unit_of(OA::row_of(wave, q, lane), lane) * 8, p.M - 8) * 2;
-#pragma unroll
-  for (int q = 0; q < OB::kCopies; ++q)
-    colb[q] = min(nb * kBN + OB::unit_of(OB::row_of(wave, q, lane), lane) * 8, p.N - 8) * 2;
-  auto issue = [&](int c) {
-    Stage<BM, true, true>& S = st[c & 1];
-    const int last = min(kBK, n - c * kBK) - 1;  // rows past the segment read its last one
-    const uint8_t* ab = p.a + (size_t)(row0 + c * kBK) * p.M * 2;
-    const uint8_t* bb = p.sorted_idx ? p.b : p.b + (size_t)(row0 + c * kBK) * p.N * 2;
-#pragma unroll
-    for (int q = 0; q < OA::kCopies; ++q)
-      dma16(ab, (uint32_t)min(OA::row_of(wave, q, lane), last) * (uint32_t)(p.M * 2) + cola[q],
-            S.a + (wave * OA::kCopies + q) * 1024);
-#pragma unroll
-    for (int q = 0; q < OB::kCopies; ++q) {
-      const int r = min(OB::row_of(wave, q, lane), last);
-      const uint32_t src = p.sorted_idx
-          ? (uint32_t)(dbg_clamp(p.sorted_idx[row0 + c * kBK + r], p.A, kDbgSorted) / p.k) : (uint32_t)r;
-      dma16(bb, src * (uint32_t)(p.N * 2) + colb[q], S.b + (wave * OB::kCopies + q) * 1024);
-    }
-  };
-  f32x16 acc[MI][2];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  if (nblk) issue(0);
-  for (int c = 0; c < nblk; ++c) {
-    MOE_DMA_SYNC(0);
-    const int left = n - c * kBK;
-    if (left < kBK) {  // zeros past the segment's end (uniform; the last block)
-      uint4* za = reinterpret_cast<uint4*>(st[c & 1].a + left * OA::kRowB);
-      uint4* zb = reinterpret_cast<uint4*>(st[c & 1].b + left * OB::kRowB);
-      for (int i = tid; i < (kBK - left) * OA::kRowB / 16; i += 64 * kNW) za[i] = uint4{0, 0, 0, 0};
-      for (int i = tid; i < (kBK - left) * OB::kRowB / 16; i += 64 * kNW) zb[i] = uint4{0, 0, 0, 0};
+        for (int i = 0; i < kMaxE / 64; ++i)
+          if (i < t.per && t.first + i < p.E) {
+            before[t.first + i] = run;
+            run += (t.n[i] + kTile - 1) / kTile;
+          }
+        if (lane == 0) before[p.E] = total;
+      }
       __syncthreads();
+      mt = before[p.E];
     }
-    if (c + 1 < nblk) issue(c + 1);
-    multiply<BM, true, true>(st[c & 1], mh, nh, lane, acc);
+    // rows: an XCD takes a contiguous range; weights: groups of 32 tiles in turn
+    const int per_e = p.mt * p.nnb;
+    const int G = W ? p.E * per_e : mt * p.nnb;
+    const int per = (G + kXcds - 1) / kXcds;
+    mine = 0;
+    if constexpr (W) {
+      const int groups = (G + kXcdCus - 1) / kXcdCus;
+      const int mine_g = (groups - x + kXcds - 1) / kXcds;  // this XCD's groups
+      const int n = mine_g * kXcdCus;
+      mine = i0 < n ? (n - i0 + NWG - 1) / NWG : 0;
+      // the last group may be short: its tiles past G are dropped
+      while (mine > 0) {
+        const int i = i0 + (mine - 1) * NWG;
+        if (((i / kXcdCus) * kXcds + x) * kXcdCus + i % kXcdCus < G) break;
+        --mine;
+      }
+    } else {
+      const int n = min(per, G - x * per);
+      mine = i0 < n ? (n - i0 + NWG - 1) / NWG : 0;
+    }
+    mine = __builtin_amdgcn_readfirstlane(min(mine, kListTiles));
+    if (mine == 0) return;  // uniform
+    if (tid < mine) {
+      const int i = i0 + tid * NWG;
+      int e, row0, rows, place;
+      if constexpr (W) {
+        const int v = ((i / kXcdCus) * kXcds + x) * kXcdCus + i % kXcdCus;
+        e = v / per_e;
+        int mb, nb;
+        panel_tile(v - e * per_e, p.mt, p.nnb, mb, nb);
+        place = nb | mb << 16;
+        rows = max(p.counts[e], 0);
+        row0 = p.offsets[e];
+        dbg_segment(row0, rows, p.A);
+      } else {
+        int tile, nb;
+        panel_tile(x * per + i, mt, p.nnb, tile, nb);
+        int lo = 0, hi = p.E - 1;  // the last expert with before[e] <= tile
+        while (lo < hi) {
+          const int m = (lo + hi + 1) >> 1;
+          if (before[m] <= tile) lo = m;
+          else hi = m - 1;
+        }
+        e = lo;
+        const int sub = tile - before[e];
+        rows = min(kTile, p.counts[e] - sub * kTile);
+        row0 = p.offsets[e] + sub * kTile;
+        dbg_segment(row0, rows, p.A);
+        place = nb;
+      }
+      *reinterpret_cast<i32x4*>(lds.list[tid]) = i32x4{e, row0, rows, place};
+    }
+    __syncthreads();
   }
-  const int l32 = lane & 31, hh = lane >> 5;
+  auto entry = [&](int r, int f) { return __builtin_amdgcn_readfirstlane(lds.list[r][f]); };
+  // blocks of a tile (weights: at least one, of zeros where the expert has no rows)
+  auto blocks_of = [&](int r) { return W ? max((entry(r, 2) + kBK - 1) / kBK, 1) : p.K / kBK; };
+
+  // -- copies -------------------------------------------------------------------------------------
+  // Cursor of the copies: tile cr, block cc of cn.
+  int cr = 0, cc = 0, cn = blocks_of(0), seq = 0;  // seq: blocks copied so far
+  const uint8_t *ab, *bb;
+  uint32_t ao[kCopies], bo[kCopies];
+  auto point_at = [&](int r) {
+    const int e = entry(r, 0), row0 = entry(r, 1), rows = entry(r, 2), place = entry(r, 3);
+    const int nb = place & 0xffff;
+    if constexpr (W) {
+      const int mb = place >> 16;
+      const int first = min(max(row0, 0), p.A - 1);  // an expert without rows may start at A
+      ab = p.a + (size_t)first * p.M * 2;
+      bb = p.sorted_idx ? p.b : p.b + (size_t)first * p.N * 2;
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = mb * BM + (mh * MI + i) * 32 + l32;
-    if (m >= p.M) continue;
+      for (int q = 0; q < kCopies; ++q) {
+        const int lr = OA::row_of(wave, q, lane), u = OA::unit_of(lr, lane) * 8;
+        ao[q] = (uint32_t)min(mb * kTile + u, p.M - 8) * 2;
+        bo[q] = (uint32_t)min(nb * kTile + u, p.N - 8) * 2;
+      }
+    } else {
+      ab = p.sorted_idx ? p.a : p.a + (size_t)row0 * p.K * 2;
+      bb = p.b + (size_t)e * p.stride;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int q = 0; q < kCopies; ++q) {
+        const int lr = OA::row_of(wave, q, lane);
+        const uint32_t row = p.sorted_idx
+            ? token_of((uint32_t)dbg_clamp(lds.src[r & 1][lr], p.A, kDbgSorted), p)
+            : (uint32_t)max(min(lr, rows - 1), 0);
+        ao[q] = row * (uint32_t)(p.K * 2) + (uint32_t)OA::unit_of(lr, lane) * 16;
+      }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = nb * kBN + (nh * 2 + j) * 32 + 8 * q + 4 * hh;
-        if (col >= p.N) continue;
-        const size_t at = ((size_t)e * p.M + m) * p.N + col;
-        float o[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = acc[i][j][4 * q + r];
-        if constexpr (F32) {
-          f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at);
-          f32x4 w = {o[0], o[1], o[2], o[3]};
-          if (accumulate) w += *dst;
-          *dst = w;
+      for (int q = 0; q < kCopies; ++q) {
+        const int lr = OB::row_of(wave, q, lane), u = OB::unit_of(lr, lane);
+        if constexpr (BT) {  // [K][N]: lr is k, the unit 8 columns
+          bo[q] = (uint32_t)lr * (uint32_t)(p.N * 2) + (uint32_t)min(nb * kTile + u * 8, p.N - 8) * 2;
+        } else if constexpr (KIND == kGateUp) {  // a wave's 128 weight rows: 64 gate rows, their up rows
+          const int col = min(nb * COLS + (lr >> 7) * 64 + (lr & 63), p.N - 1);
+          bo[q] = (uint32_t)((lr & 64) ? p.I + col : col) * (uint32_t)(p.K * 2) + (uint32_t)u * 16;
         } else {
-          put4(static_cast<uint16_t*>(p.out) + at, o);
+          bo[q] = (uint32_t)min(nb * kTile + lr, p.N - 1) * (uint32_t)(p.K * 2) + (uint32_t)u * 16;
         }
       }
+    }
+  };
+  // Gathered rows on their way into LDS: of tile r, or (weights) of block c of tile r, the q-th copied.
+  auto issue_src = [&](int r, int c, int q) {
+    if constexpr (W) {
+      if (wave == 0) {
+        const int row0 = min(max(entry(r, 1), 0), p.A - 1), n = max(entry(r, 2), 1);
+        const int i = min(lane, n - 1 - c * kBK);
+        dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + row0 + c * kBK), (uint32_t)i * 4u,
+             lds.src[q & 3]);
+      }
+    } else {
+      const int i = min(wave * 64 + lane, max(entry(r, 2), 1) - 1);
+      dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + entry(r, 1)), (uint32_t)i * 4u,
+           lds.src[r & 1] + wave * 64);
+    }
+  };
+  const size_t bstep = BT ? (size_t)kBK * p.N * 2 : (size_t)kBK * 2;
+  const uint8_t *asrc, *bsrc;  // of the block being copied
+  int clast = 0;               // weights: its last row
+  uint8_t *adst, *bdst;
+  auto open_block = [&](int s) {
+    adst = lds.a[s] + wave * kCopies * 1024;
+    bdst = lds.b[s] + wave * kCopies * 1024;
+    if constexpr (W) {
+      clast = min(kBK, max(entry(cr, 2), 1) - cc * kBK) - 1;  // rows past the segment read its last one
+      asrc = ab + (size_t)cc * kBK * p.M * 2;
+      bsrc = p.sorted_idx ? bb : bb + (size_t)cc * kBK * p.N * 2;
+    } else {
+      asrc = ab + (size_t)cc * kBK * 2;
+      bsrc = bb + cc * bstep;
+    }
+  };
+  auto copy_a = [&](int q) {
+    uint32_t o = ao[q];
+    if constexpr (W) o += (uint32_t)min(OA::row_of(wave, q, lane), clast) * (uint32_t)(p.M * 2);
+    dma16(asrc, o, adst + q * 1024);
+  };
+  auto copy_b = [&](int q) {
+    uint32_t o = bo[q];
+    if constexpr (W) {
+      const int r = OB::row_of(wave, q, lane);
+      const uint32_t row = p.sorted_idx
+          ? token_of((uint32_t)dbg_clamp(lds.src[seq & 3][r], p.A, kDbgSorted), p)
+          : (uint32_t)min(r, clast);
+      o += row * (uint32_t)(p.N * 2);
+    }
+    dma16(bsrc, o, bdst + q * 1024);
+  };
+  // Moves the cursor on; false behind the last block.  (Weights: the block behind the cursor's is
+  // where the next gathered rows come from.)
+  auto advance = [&]() {
+    if (cc + 1 < cn) {
+      ++cc;
+    } else {
+      if (cr + 1 == mine) return false;
+      ++cr;
+      cc = 0;
+      cn = blocks_of(cr);
+      point_at(cr);
+      if (!W && p.sorted_idx && cr + 1 < mine) issue_src(cr + 1, 0, 0);
+    }
+    ++seq;
+    return true;
+  };
+  auto src_ahead = [&]() {  // weights: the rows of the block behind the cursor's
+    if constexpr (W) {
+      if (!p.sorted_idx) return;
+      if (cc + 1 < cn) issue_src(cr, cc + 1, seq + 1);
+      else if (cr + 1 < mine) issue_src(cr + 1, 0, seq + 1);
+    }
+  };
+
+  // -- the first two blocks -----------------------------------------------------------------------
+  if (p.sorted_idx) {
+    issue_src(0, 0, 0);
+    if constexpr (W) src_ahead();
+    else if (mine > 1) issue_src(1, 0, 0);
+    MOE_DMA_SYNC(0);
   }
+  point_at(0);
+  open_block(0);
+#pragma unroll
+  for (int q = 0; q < kCopies; ++q) {
+    copy_a(q);
+    copy_b(q);
+  }
+  bool more = advance();  // whether there are blocks left to copy
+  if (more) {
+    src_ahead();
+    open_block(1);
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      copy_a(q);
+      copy_b(q);
+    }
+  }
+  MOE_DMA_SYNC(0);
+
+  // -- compute ------------------------------------------------------------------------------------
+  int aa[AT ? 4 : 1], ba[BT ? 4 : 1];
+#pragma unroll
+  for (int i = 0; i < (AT ? 4 : 1); ++i) aa[i] = OA::addr(mh * 4, i, lane);
+#pragma unroll
+  for (int j = 0; j < (BT ? 4 : 1); ++j) ba[j] = OB::addr(nh * 4, j, lane);
+  f32x16 acc[4][4];
+  bf16x8 af[2][4], bf[2][4];
+  auto get_a = [&](int s, int step, int i) {
+    return AT ? OA::frag(lds.a[s], aa[AT ? i : 0], step)
+              : OA::frag(lds.a[s] + i * 32 * OA::kRowB, aa[0], step);
+  };
+  auto get_b = [&](int s, int step, int j) {
+    return BT ? OB::frag(lds.b[s], ba[BT ? j : 0], step)
+              : OB::frag(lds.b[s] + j * 32 * OB::kRowB, ba[0], step);
+  };
+  // the n-th of a step's 8 fragments, in the order that its MFMAs need them
+  auto get = [&](int s, int step, int n) {
+    if (n == 0) af[step & 1][0] = get_a(s, step, 0);
+    else if (n < 5) bf[step & 1][n - 1] = get_b(s, step, n - 1);
+    else af[step & 1][n - 4] = get_a(s, step, n - 4);
+  };
+  // zeros past the end of an expert's rows in a block that has landed (before it is read)
+  auto trim = [&](int s, int left) {
+    if constexpr (W) {
+      if (left >= kBK) return;
+      left = max(left, 0);
+      uint4* za = reinterpret_cast<uint4*>(lds.a[s] + left * OA::kRowB);
+      uint4* zb = reinterpret_cast<uint4*>(lds.b[s] + left * OB::kRowB);
+      for (int i = tid; i < (kBK - left) * OA::kRowB / 16; i += 64 * kNW) za[i] = zb[i] = uint4{0, 0, 0, 0};
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
+      asm volatile("s_barrier" ::: "memory");
+    }
+  };
+  if constexpr (W) trim(0, entry(0, 2));
+  int s = 0;  // stage of the block being multiplied
+#pragma unroll
+  for (int n = 0; n < 8; ++n) get(s, 0, n);
+  int pending = 0;  // copies of the open block left for the next block's first step
+  for (int r = 0; r < mine; ++r) {
+    const int rows = entry(r, 2), row0 = entry(r, 1), place = entry(r, 3), nb = place & 0xffff;
+    const int nblk = blocks_of(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    for (int c = 0; c < nblk; ++c) {
+      // rows of the next block that count (weights)
+      const int next_left = !W ? kBK : c + 1 < nblk ? rows - (c + 1) * kBK
+                                     : r + 1 < mine ? entry(r + 1, 2) : kBK;
+#pragma unroll
+      for (int step = 0; step < 4; ++step) {
+#pragma unroll
+        for (int m = 0; m < 16; ++m) {
+          const int i = m >> 2, j = m & 3;
+          acc[i][j] = mfma32(bf[step & 1][j], af[step & 1][i], acc[i][j]);
+          if (step < 3) {
+            if (m < 8) get(s, step + 1, m);
+            if (step == 0 && m >= 8 && m < 12 && pending) copy_b(m - 4);
+          } else {
+            if (m == 1) {
+              MOE_DMA_SYNC(0);
+              trim(s ^ 1, next_left);
+              more = more && advance();
+              pending = more;
+              if (more) {
+                src_ahead();
+                open_block(s);
+              }
+            }
+            if (m >= 2 && m < 10) get(s ^ 1, 0, m - 2);
+            if (more && m >= 4) {
+              if (m < 12) copy_a(m - 4);
+              else copy_b(m - 12);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      s ^= 1;
+    }
+
+    // -- epilogue -----------------------------------------------------------------------------------
+    uint8_t* ep = lds.epi[wave];
+    const int er = lane >> 3, eu = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int lr = mh * 128 + i * 32;  // first of these 32 rows in the tile
+      if constexpr (W) {
+        const int m0 = (place >> 16) * kTile + lr;
+        if (m0 >= p.M) continue;  // M is a multiple of 32: all rows or none
+        const size_t out0 = (size_t)entry(r, 0) * p.M * p.N;
+        if constexpr (F32) {
+          if (accumulate && rows <= 0) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            keep(acc[i][j]);
+            const int col = nb * kTile + nh * 128 + j * 32 + eu * 4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              epi_put16(ep, lane, 2 * q + (lane >> 5),
+                        __builtin_bit_cast(uint4, f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                        acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]}));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint4 v = epi_get(ep, lane, t);
+              if (col >= p.N) continue;
+              f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + out0 +
+                                                    (size_t)(m0 + er + 8 * t) * p.N + col);
+              f32x4 w = __builtin_bit_cast(f32x4, v);
+              if (accumulate) w += *dst;
+              *dst = w;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            keep(acc[i][j]);
+            keep(acc[i][j + 1]);
+            const int col = nb * kTile + nh * 128 + j * 32 + eu * 8;
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) epi_put8(ep, lane, jj * 4 + q, pack4(acc[i][j + jj], q));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint4 v = epi_get(ep, lane, t);
+              if (col < p.N)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out0 +
+                                          (size_t)(m0 + er + 8 * t) * p.N + col) = v;
+            }
+          }
+        }
+      } else if constexpr (KIND == kDown || KIND == kDx) {
+        if (lr >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          keep(acc[i][j]);
+          keep(acc[i][j + 1]);
+          const int col = nb * kTile + nh * 128 + j * 32 + eu * 8;
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) epi_put8(ep, lane, jj * 4 + q, pack4(acc[i][j + jj], q));
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint4 v = epi_get(ep, lane, t);
+            if (col < p.N && lr + er + 8 * t < rows)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                        (size_t)(row0 + lr + er + 8 * t) * p.N + col) = v;
+          }
+        }
+      } else if constexpr (KIND == kGateUp) {
+        if (lr >= rows) continue;
+        const int col = nb * COLS + nh * 64 + eu * 8;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {  // gate, up, h
+#pragma unroll
+          for (int j = 0; j < 4; ++j) keep(acc[i][j]);
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint2 v;
+              if (part < 2) {
+                v = pack4(acc[i][2 * part + jj], q);
+              } else {
+                float h[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) h[t] = swiglu(acc[i][jj][4 * q + t], acc[i][2 + jj][4 * q + t]);
+                v = uint2{bf16_pack2(h[0], h[1]), bf16_pack2(h[2], h[3])};
+              }
+              epi_put8(ep, lane, jj * 4 + q, v);
+            }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint4 v = epi_get(ep, lane, t);
+            if (col >= p.N || lr + er + 8 * t >= rows) continue;
+            const size_t row = (size_t)(row0 + lr + er + 8 * t);
+            uint16_t* dst = part == 2 ? static_cast<uint16_t*>(p.out) + row * p.I + col
+                                      : p.out2 + row * 2 * p.I + part * p.I + col;
+            *reinterpret_cast<uint4*>(dst) = v;
+          }
+        }
+      } else {
+        if (lr >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          keep(acc[i][j]);
+          const int col = nb * kTile + nh * 128 + j * 32 + eu * 4;
+          uint2 gw[4], uw[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const size_t row = (size_t)(row0 + min(lr + er + 8 * t, rows - 1));
+            const uint16_t* src = p.gu + row * 2 * p.I + min(col, p.I - 4);
+            gw[t] = *reinterpret_cast<const uint2*>(src);
+            uw[t] = *reinterpret_cast<const uint2*>(src + p.I);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            epi_put16(ep, lane, 2 * q + (lane >> 5),
+                      __builtin_bit_cast(uint4, f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                      acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]}));
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const f32x4 dh = __builtin_bit_cast(f32x4, epi_get(ep, lane, t));
+            if (col >= p.N || lr + er + 8 * t >= rows) continue;
+            const uint32_t g2[2] = {gw[t].x, gw[t].y}, u2[2] = {uw[t].x, uw[t].y};
+            float h[4], dg[4], du[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float g = __uint_as_float(v & 1 ? g2[v / 2] & 0xffff0000u : g2[v / 2] << 16);
+              const float u = __uint_as_float(v & 1 ? u2[v / 2] & 0xffff0000u : u2[v / 2] << 16);
+              const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+              h[v] = g * sg * u;
+              du[v] = dh[v] * (g * sg);
+              dg[v] = dh[v] * u * (sg * fmaf(g, 1.f - sg, 1.f));
+            }
+            const size_t row = (size_t)(row0 + lr + er + 8 * t);
+            auto put = [](uint16_t* d, const float* f) {
+              *reinterpret_cast<uint2*>(d) = uint2{bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3])};
+            };
+            put(static_cast<uint16_t*>(p.out) + row * p.I + col, h);
+            put(p.out2 + row * 2 * p.I + col, dg);
+            put(p.out2 + row * 2 * p.I + p.I + col, du);
+          }
+        }
+      }
+    }
+  }
+  MOE_DMA_SYNC(0);  // nothing on its way into this workgroup's LDS any more
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(uint4* out, size_t n) {
+  for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n; i += gridDim.x * (size_t)256)
+    out[i] = uint4{0, 0, 0, 0};
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-template <int MODE, bool BT>
+// Workgroups for `tiles` tiles: one per compute unit, more where a list would overflow.
+unsigned grid_of(int64_t tiles) {
+  const int64_t per = (tiles + kXcds - 1) / kXcds;
+  int64_t n = per < kXcdCus ? per : kXcdCus;
+  if (n * kListTiles < per) n = (per + kListTiles - 1) / kListTiles;
+  return (unsigned)(n * kXcds);
+}
+
+template <Kind KIND>
 int launch_rows(TrainArgs p, hipStream_t s, const char* who) {
-  constexpr int BM = 256, COLS = MODE == kGated ? kBN / 2 : kBN;
+  constexpr int COLS = KIND == kGateUp ? kTile / 2 : kTile;
   p.nnb = (p.N + COLS - 1) / COLS;
-  const int64_t tiles = row_tiles_bound(p.A, p.E, BM) * p.nnb;
-  const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-  if (grid * 64 * kNW >= (int64_t)1 << 32) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-  train_rows_kernel<BM, MODE, BT><<<(unsigned)grid, 64 * kNW, 0, s>>>(p);
+  const int64_t tiles = row_tiles_bound(p.A, p.E, kTile) * p.nnb;
+  if (tiles >= (int64_t)1 << 31) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+  train_gemm_kernel<KIND, false><<<grid_of(tiles), 64 * kNW, 0, s>>>(p, 0);
   return check_launch(who);
 }
 
-int launch_weights(WgradArgs p, bool f32, int accumulate, hipStream_t s, const char* who) {
-  p.mt = (p.M + 255) / 256;
-  p.nt = (p.N + kBN - 1) / kBN;
-  const int64_t grid = (int64_t)p.E * p.mt * p.nt;
-  if (grid * 64 * kNW >= (int64_t)1 << 32) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-  if (f32) train_weights_kernel<true><<<(unsigned)grid, 64 * kNW, 0, s>>>(p, accumulate);
-  else train_weights_kernel<false><<<(unsigned)grid, 64 * kNW, 0, s>>>(p, 0);
+int launch_weights(TrainArgs p, bool f32, int accumulate, hipStream_t s, const char* who) {
+  p.mt = (p.M + kTile - 1) / kTile;
+  p.nnb = (p.N + kTile - 1) / kTile;
+  // whole groups for every XCD
+  const int64_t groups = ((int64_t)p.E * p.mt * p.nnb + kXcdCus - 1) / kXcdCus;
+  const int64_t per = (groups + kXcds - 1) / kXcds * kXcdCus;
+  int64_t n = kXcdCus;
+  if (n * kListTiles < per) n = (per + kListTiles - 1) / kListTiles;
+  const unsigned grid = (unsigned)(n * kXcds);
+  if (f32) train_gemm_kernel<kWeights, true><<<grid, 64 * kNW, 0, s>>>(p, accumulate);
+  else train_gemm_kernel<kWeights, false><<<grid, 64 * kNW, 0, s>>>(p, 0);
   return check_launch(who);
 }
 
@@ -413,6 +681,15 @@ int check_train(const char* who, const moe_experts* W, int32_t T, int32_t k, boo
 }
 
 bool bad(const void* p) { return !p || !aligned16(p); }
+
+TrainArgs args_of(const moe_experts* W, int32_t T, int32_t k, const int32_t* counts,
+                  const int32_t* offsets) {
+  TrainArgs p{};
+  p.E = W->E; p.I = W->I; p.k = k; p.A = T * k;
+  p.counts = counts; p.offsets = offsets; p.stride = W->stride;
+  p.k_magic = k > 1 ? (uint32_t)((1ull << 32) / k + 1) : 0;
+  return p;
+}
 
 }  // namespace
 
@@ -444,20 +721,19 @@ extern "C" int moe_expert_ffn_train(const moe_experts* W, const uint16_t* x, int
   if (ws_bytes < moe_expert_ffn_train_workspace(W, T, k))
     return set_error(MOE_ERR_WORKSPACE, "%s: workspace %zu too small", who, ws_bytes);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  TrainArgs p{};
-  p.E = W->E; p.H = W->H; p.I = W->I; p.k = k; p.A = T * k;
-  p.counts = counts; p.offsets = offsets; p.sorted_idx = sorted_idx;
-  p.w = static_cast<const uint8_t*>(W->base) + Lo.w13; p.stride = W->stride;
+  TrainArgs p = args_of(W, T, k, counts, offsets);
+  p.sorted_idx = sorted_idx;
+  p.b = static_cast<const uint8_t*>(W->base) + Lo.w13;
   p.a = reinterpret_cast<const uint8_t*>(x);
   p.K = W->H; p.N = W->I;
-  p.out = static_cast<uint16_t*>(ws); p.out2 = gate_up;
-  if (int st = launch_rows<kGated, false>(p, s, who)) return st;
+  p.out = ws; p.out2 = gate_up;
+  if (int st = launch_rows<kGateUp>(p, s, who)) return st;
   p.sorted_idx = nullptr;
-  p.w = static_cast<const uint8_t*>(W->base) + Lo.w2;
+  p.b = static_cast<const uint8_t*>(W->base) + Lo.w2;
   p.a = static_cast<const uint8_t*>(ws);
   p.K = W->I; p.N = W->H;
   p.out = y_perm; p.out2 = nullptr;
-  return launch_rows<kPlain, false>(p, s, who);
+  return launch_rows<kDown>(p, s, who);
 }
 
 // Workspace: h bf16 [T*k][I], (dg; du) bf16 [T*k][2I].
@@ -490,43 +766,46 @@ extern "C" int moe_expert_ffn_backward(const moe_experts* W, const uint16_t* x, 
   }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const int A = T * k, H = W->H, I = W->I;
+  const size_t esize = d_w_type == MOE_T_F32 ? 4 : 2;
+  if (T == 0) {
+    auto zero = [&](void* out) {
+      const size_t n = (size_t)W->E * (out == d_w13 ? 2 : 1) * I * H * esize / 16;
+      zero_kernel<<<(unsigned)(n / 256 < 8192 ? n / 256 : 8192), 256, 0, s>>>(static_cast<uint4*>(out), n);
+      return check_launch(who);
+    };
+    if (!accumulate && d_w13)
+      if (int st = zero(d_w13)) return st;
+    return !accumulate && d_w2 ? zero(d_w2) : MOE_OK;
+  }
+  if (!d_x_perm && !d_w13 && !d_w2) return MOE_OK;
   uint16_t* h = static_cast<uint16_t*>(ws);
   uint16_t* dgu = h + align256((size_t)A * I * 2) / 2;
-  if (T > 0 && (d_x_perm || d_w13 || d_w2)) {
-    TrainArgs p{};
-    p.E = W->E; p.H = H; p.I = I; p.k = k; p.A = A;
-    p.counts = counts; p.offsets = offsets;
-    p.stride = W->stride;
-    p.w = static_cast<const uint8_t*>(W->base) + Lo.w2;
+  TrainArgs p = args_of(W, T, k, counts, offsets);
+  p.b = static_cast<const uint8_t*>(W->base) + Lo.w2;
+  p.a = reinterpret_cast<const uint8_t*>(d_y_perm);
+  p.K = H; p.N = I;
+  p.out = h; p.out2 = dgu; p.gu = gate_up;
+  if (int st = launch_rows<kDh>(p, s, who)) return st;
+  if (d_x_perm) {
+    p.b = static_cast<const uint8_t*>(W->base) + Lo.w13;
+    p.a = reinterpret_cast<const uint8_t*>(dgu);
+    p.K = 2 * I; p.N = H;
+    p.out = d_x_perm;
+    if (int st = launch_rows<kDx>(p, s, who)) return st;
+  }
+  if (d_w13) {
+    p.sorted_idx = sorted_idx;
+    p.a = reinterpret_cast<const uint8_t*>(dgu);
+    p.b = reinterpret_cast<const uint8_t*>(x);
+    p.M = 2 * I; p.N = H; p.out = d_w13;
+    if (int st = launch_weights(p, d_w_type == MOE_T_F32, accumulate, s, who)) return st;
+  }
+  if (d_w2) {
+    p.sorted_idx = nullptr;
     p.a = reinterpret_cast<const uint8_t*>(d_y_perm);
-    p.K = H; p.N = I;
-    p.out = h; p.out2 = dgu; p.gu = gate_up;
-    if (int st = launch_rows<kDswiglu, true>(p, s, who)) return st;
-    if (d_x_perm) {
-      p.w = static_cast<const uint8_t*>(W->base) + Lo.w13;
-      p.a = reinterpret_cast<const uint8_t*>(dgu);
-      p.K = 2 * I; p.N = H;
-      p.out = d_x_perm; p.out2 = nullptr; p.gu = nullptr;
-      if (int st = launch_rows<kPlain, true>(p, s, who)) return st;
-    }
-  }
-  WgradArgs g{};
-  g.E = W->E; g.k = k; g.A = A;
-  g.counts = T > 0 ? counts : nullptr;
-  g.offsets = offsets;
-  if (d_w13 && !(T == 0 && accumulate)) {
-    g.sorted_idx = sorted_idx;
-    g.a = reinterpret_cast<const uint8_t*>(dgu);
-    g.b = reinterpret_cast<const uint8_t*>(x);
-    g.M = 2 * I; g.N = H; g.out = d_w13;
-    if (int st = launch_weights(g, d_w_type == MOE_T_F32, accumulate, s, who)) return st;
-  }
-  if (d_w2 && !(T == 0 && accumulate)) {
-    g.sorted_idx = nullptr;
-    g.a = reinterpret_cast<const uint8_t*>(d_y_perm);
-    g.b = reinterpret_cast<const uint8_t*>(h);
-    g.M = H; g.N = I; g.out = d_w2;
-    if (int st = launch_weights(g, d_w_type == MOE_T_F32, accumulate, s, who)) return st;
+    p.b = reinterpret_cast<const uint8_t*>(h);
+    p.M = H; p.N = I; p.out = d_w2;
+    if (int st = launch_weights(p, d_w_type == MOE_T_F32, accumulate, s, who)) return st;
   }
   return MOE_OK;
 }
