@@ -124,7 +124,7 @@ struct TrainLds {
   uint8_t b[2][kOperandB];
   uint8_t epi[kNW][kEpiB];
   __attribute__((aligned(16))) int list[kListTiles][4];
-  int src[4][kTile];  // gathered rows: of a tile ([tile % 2]); kWeights: of a block ([block % 4][64])
+  int src[4][kTile];  // gathered rows: of a tile ([tile % 2]); weights: of a block ([block % 4][64])
 };
 static_assert(sizeof(TrainLds) <= 160 * 1024, "LDS");
 
@@ -153,7 +153,8 @@ __device__ __forceinline__ uint2 pack4(const f32x16& v, int q) {
   return uint2{bf16_pack2(v[4 * q], v[4 * q + 1]), bf16_pack2(v[4 * q + 2], v[4 * q + 3])};
 }
 
-template <Kind KIND, bool F32>
+// GATHER: the rows of a (weights: of b) are tokens', through sorted_idx.
+template <Kind KIND, bool F32, bool GATHER>
 __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, int accumulate) {
   constexpr bool W = KIND == kWeights;
   constexpr bool AT = W, BT = W || KIND == kDh || KIND == kDx;
@@ -247,38 +248,92 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
   auto blocks_of = [&](int r) { return W ? max((entry(r, 2) + kBK - 1) / kBK, 1) : p.K / kBK; };
 
   // -- copies -------------------------------------------------------------------------------------
-  // Cursor of the copies: tile cr, block cc of cn.
-  int cr = 0, cc = 0, cn = blocks_of(0), seq = 0;  // seq: blocks copied so far
-  const uint8_t *ab, *bb;
+  // The block being copied: tile cr, cleft blocks left of it (this one included), from asrc and
+  // bsrc at the lane's offsets.  Behind the last block the copies repeat it, into a stage that
+  // nobody reads: no branches around them.
+  int cr = 0, cleft = blocks_of(0);
+  const uint8_t *asrc, *bsrc;
   uint32_t ao[kCopies], bo[kCopies];
+  uint32_t bcol[2];  // weights, gathered: the lane's column in even and odd copies
+  const size_t astep = W ? (size_t)kBK * p.M * 2 : (size_t)kBK * 2;
+  const size_t bstep = GATHER && W ? 0 : BT ? (size_t)kBK * p.N * 2 : (size_t)kBK * 2;
+  // Gathered rows of a block of weights come by the ring lds.src, two blocks ahead of the copies:
+  // cursor of the block whose rows are next, tile sr, first of its rows sp of sn.
+  int sr = 0, sp = 0, sn = 0, srow = 0, sq = 0;
+  auto issue_ring = [&]() {
+    if (wave == 0) {
+      if (sp == 0) {
+        srow = min(max(entry(sr, 1), 0), p.A - 1);
+        sn = max(entry(sr, 2), 1);
+      }
+      // rows past the segment: its last one
+      dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + srow + sp), (uint32_t)min(lane, sn - 1 - sp) * 4u,
+           lds.src[sq & 3]);
+      ++sq;
+      if (sp + kBK < sn) {
+        sp += kBK;
+      } else if (sr + 1 < mine) {
+        ++sr;
+        sp = 0;
+      }
+    }
+  };
+  int rq = 0;             // blocks whose rows have been read from the ring
+  uint32_t rows_next[GATHER && W ? kCopies : 1];
+  auto read_ring = [&](int q) {
+    rows_next[q] = token_of((uint32_t)dbg_clamp(lds.src[rq & 3][OB::row_of(wave, q, lane)], p.A, kDbgSorted), p) *
+                   (uint32_t)(p.N * 2);
+  };
+  // Gathered rows of tile r on their way into LDS.
+  auto issue_src = [&](int r) {
+    const int i = min(wave * 64 + lane, max(entry(r, 2), 1) - 1);
+    dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + entry(r, 1)), (uint32_t)i * 4u,
+         lds.src[r & 1] + wave * 64);
+  };
+  // A tile's last block of weights may be short: rows past the segment read its last one.
+  auto shorten = [&](int left) {
+    if (left >= kBK) return;
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int over = max(OA::row_of(wave, q, lane) - max(left - 1, 0), 0);
+      ao[q] -= (uint32_t)over * (uint32_t)(p.M * 2);
+      if (!GATHER) bo[q] -= (uint32_t)over * (uint32_t)(p.N * 2);
+    }
+  };
   auto point_at = [&](int r) {
     const int e = entry(r, 0), row0 = entry(r, 1), rows = entry(r, 2), place = entry(r, 3);
     const int nb = place & 0xffff;
+    cleft = blocks_of(r);
+    // the lane's part is recomputed per tile: hoisted out of the loop it would cost registers
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
     if constexpr (W) {
       const int mb = place >> 16;
       const int first = min(max(row0, 0), p.A - 1);  // an expert without rows may start at A
-      ab = p.a + (size_t)first * p.M * 2;
-      bb = p.sorted_idx ? p.b : p.b + (size_t)first * p.N * 2;
+      asrc = p.a + (size_t)first * p.M * 2;
+      bsrc = GATHER ? p.b : p.b + (size_t)first * p.N * 2;
 #pragma unroll
       for (int q = 0; q < kCopies; ++q) {
-        const int lr = OA::row_of(wave, q, lane), u = OA::unit_of(lr, lane) * 8;
-        ao[q] = (uint32_t)min(mb * kTile + u, p.M - 8) * 2;
-        bo[q] = (uint32_t)min(nb * kTile + u, p.N - 8) * 2;
+        const int lr = OA::row_of(wave, q, ln), u = OA::unit_of(lr, ln) * 8;
+        ao[q] = (uint32_t)lr * (uint32_t)(p.M * 2) + (uint32_t)min(mb * kTile + u, p.M - 8) * 2;
+        const uint32_t c = (uint32_t)min(nb * kTile + u, p.N - 8) * 2;
+        if (GATHER) bcol[q & 1] = c;
+        else bo[q] = (uint32_t)lr * (uint32_t)(p.N * 2) + c;
       }
+      if (cleft == 1) shorten(rows);
     } else {
-      ab = p.sorted_idx ? p.a : p.a + (size_t)row0 * p.K * 2;
-      bb = p.b + (size_t)e * p.stride;
+      asrc = GATHER ? p.a : p.a + (size_t)row0 * p.K * 2;
+      bsrc = p.b + (size_t)e * p.stride;
 #pragma unroll
       for (int q = 0; q < kCopies; ++q) {
-        const int lr = OA::row_of(wave, q, lane);
-        const uint32_t row = p.sorted_idx
-            ? token_of((uint32_t)dbg_clamp(lds.src[r & 1][lr], p.A, kDbgSorted), p)
-            : (uint32_t)max(min(lr, rows - 1), 0);
-        ao[q] = row * (uint32_t)(p.K * 2) + (uint32_t)OA::unit_of(lr, lane) * 16;
+        const int lr = OA::row_of(wave, q, ln);
+        const uint32_t row = GATHER ? token_of((uint32_t)dbg_clamp(lds.src[r & 1][lr], p.A, kDbgSorted), p)
+                                    : (uint32_t)max(min(lr, rows - 1), 0);
+        ao[q] = row * (uint32_t)(p.K * 2) + (uint32_t)OA::unit_of(lr, ln) * 16;
       }
 #pragma unroll
       for (int q = 0; q < kCopies; ++q) {
-        const int lr = OB::row_of(wave, q, lane), u = OB::unit_of(lr, lane);
+        const int lr = OB::row_of(wave, q, ln), u = OB::unit_of(lr, ln);
         if constexpr (BT) {  // [K][N]: lr is k, the unit 8 columns
           bo[q] = (uint32_t)lr * (uint32_t)(p.N * 2) + (uint32_t)min(nb * kTile + u * 8, p.N - 8) * 2;
         } else if constexpr (KIND == kGateUp) {  // a wave's 128 weight rows: 64 gate rows, their up rows
@@ -290,100 +345,59 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
       }
     }
   };
-  // Gathered rows on their way into LDS: of tile r, or (weights) of block c of tile r, the q-th copied.
-  auto issue_src = [&](int r, int c, int q) {
-    if constexpr (W) {
-      if (wave == 0) {
-        const int row0 = min(max(entry(r, 1), 0), p.A - 1), n = max(entry(r, 2), 1);
-        const int i = min(lane, n - 1 - c * kBK);
-        dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + row0 + c * kBK), (uint32_t)i * 4u,
-             lds.src[q & 3]);
-      }
-    } else {
-      const int i = min(wave * 64 + lane, max(entry(r, 2), 1) - 1);
-      dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + entry(r, 1)), (uint32_t)i * 4u,
-           lds.src[r & 1] + wave * 64);
-    }
-  };
-  const size_t bstep = BT ? (size_t)kBK * p.N * 2 : (size_t)kBK * 2;
-  const uint8_t *asrc, *bsrc;  // of the block being copied
-  int clast = 0;               // weights: its last row
-  uint8_t *adst, *bdst;
-  auto open_block = [&](int s) {
-    adst = lds.a[s] + wave * kCopies * 1024;
-    bdst = lds.b[s] + wave * kCopies * 1024;
-    if constexpr (W) {
-      clast = min(kBK, max(entry(cr, 2), 1) - cc * kBK) - 1;  // rows past the segment read its last one
-      asrc = ab + (size_t)cc * kBK * p.M * 2;
-      bsrc = p.sorted_idx ? bb : bb + (size_t)cc * kBK * p.N * 2;
-    } else {
-      asrc = ab + (size_t)cc * kBK * 2;
-      bsrc = bb + cc * bstep;
-    }
-  };
-  auto copy_a = [&](int q) {
-    uint32_t o = ao[q];
-    if constexpr (W) o += (uint32_t)min(OA::row_of(wave, q, lane), clast) * (uint32_t)(p.M * 2);
-    dma16(asrc, o, adst + q * 1024);
-  };
-  auto copy_b = [&](int q) {
-    uint32_t o = bo[q];
-    if constexpr (W) {
-      const int r = OB::row_of(wave, q, lane);
-      const uint32_t row = p.sorted_idx
-          ? token_of((uint32_t)dbg_clamp(lds.src[seq & 3][r], p.A, kDbgSorted), p)
-          : (uint32_t)min(r, clast);
-      o += row * (uint32_t)(p.N * 2);
-    }
-    dma16(bsrc, o, bdst + q * 1024);
-  };
-  // Moves the cursor on; false behind the last block.  (Weights: the block behind the cursor's is
-  // where the next gathered rows come from.)
+  // On to the next block.
   auto advance = [&]() {
-    if (cc + 1 < cn) {
-      ++cc;
-    } else {
-      if (cr + 1 == mine) return false;
+    if (cleft > 1) {
+      --cleft;
+      asrc += astep;
+      bsrc += bstep;
+      if (W && cleft == 1) shorten(entry(cr, 2) - (blocks_of(cr) - 1) * kBK);
+    } else if (cr + 1 < mine) {
       ++cr;
-      cc = 0;
-      cn = blocks_of(cr);
       point_at(cr);
-      if (!W && p.sorted_idx && cr + 1 < mine) issue_src(cr + 1, 0, 0);
+      if (!W && GATHER && cr + 1 < mine) issue_src(cr + 1);
     }
-    ++seq;
-    return true;
-  };
-  auto src_ahead = [&]() {  // weights: the rows of the block behind the cursor's
-    if constexpr (W) {
-      if (!p.sorted_idx) return;
-      if (cc + 1 < cn) issue_src(cr, cc + 1, seq + 1);
-      else if (cr + 1 < mine) issue_src(cr + 1, 0, seq + 1);
+    if constexpr (W && GATHER) {
+#pragma unroll
+      for (int q = 0; q < kCopies; ++q) bo[q] = rows_next[q] + bcol[q & 1];
+      ++rq;
+      issue_ring();
     }
   };
+  auto copy_a = [&](int s, int q) { dma16(asrc, ao[q], lds.a[s] + (wave * kCopies + q) * 1024); };
+  auto copy_b = [&](int s, int q) { dma16(bsrc, bo[q], lds.b[s] + (wave * kCopies + q) * 1024); };
 
   // -- the first two blocks -----------------------------------------------------------------------
-  if (p.sorted_idx) {
-    issue_src(0, 0, 0);
-    if constexpr (W) src_ahead();
-    else if (mine > 1) issue_src(1, 0, 0);
+  if constexpr (GATHER) {
+    if constexpr (W) {
+      for (int i = 0; i < 3; ++i) issue_ring();
+    } else {
+      issue_src(0);
+      if (mine > 1) issue_src(1);
+    }
     MOE_DMA_SYNC(0);
   }
   point_at(0);
-  open_block(0);
-#pragma unroll
-  for (int q = 0; q < kCopies; ++q) {
-    copy_a(q);
-    copy_b(q);
-  }
-  bool more = advance();  // whether there are blocks left to copy
-  if (more) {
-    src_ahead();
-    open_block(1);
+  if constexpr (W && GATHER) {
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) {
-      copy_a(q);
-      copy_b(q);
+      read_ring(q);
+      bo[q] = rows_next[q] + bcol[q & 1];
     }
+    ++rq;
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) read_ring(q);
+  }
+#pragma unroll
+  for (int q = 0; q < kCopies; ++q) {
+    copy_a(0, q);
+    copy_b(0, q);
+  }
+  advance();
+#pragma unroll
+  for (int q = 0; q < kCopies; ++q) {
+    copy_a(1, q);
+    copy_b(1, q);
   }
   MOE_DMA_SYNC(0);
 
@@ -425,10 +439,10 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
   int s = 0;  // stage of the block being multiplied
 #pragma unroll
   for (int n = 0; n < 8; ++n) get(s, 0, n);
-  int pending = 0;  // copies of the open block left for the next block's first step
   for (int r = 0; r < mine; ++r) {
     const int rows = entry(r, 2), row0 = entry(r, 1), place = entry(r, 3), nb = place & 0xffff;
     const int nblk = blocks_of(r);
+    const int rows_after = W && r + 1 < mine ? entry(r + 1, 2) : kBK;  // weights: the next tile's
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -436,9 +450,6 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
     for (int c = 0; c < nblk; ++c) {
-      // rows of the next block that count (weights)
-      const int next_left = !W ? kBK : c + 1 < nblk ? rows - (c + 1) * kBK
-                                     : r + 1 < mine ? entry(r + 1, 2) : kBK;
 #pragma unroll
       for (int step = 0; step < 4; ++step) {
 #pragma unroll
@@ -447,23 +458,19 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
           acc[i][j] = mfma32(bf[step & 1][j], af[step & 1][i], acc[i][j]);
           if (step < 3) {
             if (m < 8) get(s, step + 1, m);
-            if (step == 0 && m >= 8 && m < 12 && pending) copy_b(m - 4);
+            // the rest of the copies of the block opened last (the first time: once more)
+            if (step == 0 && m >= 8 && m < 12) copy_b(s ^ 1, m - 4);
+            if constexpr (W && GATHER)
+              if (step == 2 && m >= 8) read_ring(m - 8);
           } else {
             if (m == 1) {
               MOE_DMA_SYNC(0);
-              trim(s ^ 1, next_left);
-              more = more && advance();
-              pending = more;
-              if (more) {
-                src_ahead();
-                open_block(s);
-              }
+              if constexpr (W) trim(s ^ 1, c + 1 < nblk ? rows - (c + 1) * kBK : rows_after);
+              advance();
             }
             if (m >= 2 && m < 10) get(s ^ 1, 0, m - 2);
-            if (more && m >= 4) {
-              if (m < 12) copy_a(m - 4);
-              else copy_b(m - 12);
-            }
+            if (m >= 4 && m < 12) copy_a(s, m - 4);
+            if (m >= 12) copy_b(s, m - 12);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -643,7 +650,13 @@ int launch_rows(TrainArgs p, hipStream_t s, const char* who) {
   p.nnb = (p.N + COLS - 1) / COLS;
   const int64_t tiles = row_tiles_bound(p.A, p.E, kTile) * p.nnb;
   if (tiles >= (int64_t)1 << 31) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-  train_gemm_kernel<KIND, false><<<grid_of(tiles), 64 * kNW, 0, s>>>(p, 0);
+  if constexpr (KIND == kGateUp) {
+    if (p.sorted_idx) {
+      train_gemm_kernel<KIND, false, true><<<grid_of(tiles), 64 * kNW, 0, s>>>(p, 0);
+      return check_launch(who);
+    }
+  }
+  train_gemm_kernel<KIND, false, false><<<grid_of(tiles), 64 * kNW, 0, s>>>(p, 0);
   return check_launch(who);
 }
 
@@ -656,8 +669,10 @@ int launch_weights(TrainArgs p, bool f32, int accumulate, hipStream_t s, const c
   int64_t n = kXcdCus;
   if (n * kListTiles < per) n = (per + kListTiles - 1) / kListTiles;
   const unsigned grid = (unsigned)(n * kXcds);
-  if (f32) train_gemm_kernel<kWeights, true><<<grid, 64 * kNW, 0, s>>>(p, accumulate);
-  else train_gemm_kernel<kWeights, false><<<grid, 64 * kNW, 0, s>>>(p, 0);
+  if (f32 && p.sorted_idx) train_gemm_kernel<kWeights, true, true><<<grid, 64 * kNW, 0, s>>>(p, accumulate);
+  else if (f32) train_gemm_kernel<kWeights, true, false><<<grid, 64 * kNW, 0, s>>>(p, accumulate);
+  else if (p.sorted_idx) train_gemm_kernel<kWeights, false, true><<<grid, 64 * kNW, 0, s>>>(p, 0);
+  else train_gemm_kernel<kWeights, false, false><<<grid, 64 * kNW, 0, s>>>(p, 0);
   return check_launch(who);
 }
 
