@@ -17,9 +17,11 @@
 // K goes in blocks of 64, both operands copied from memory straight into LDS, two stages.  An
 // operand with K contiguous lies as rows of 128 bytes, one with K strided as 64 rows of the tile's
 // columns, read back through the transposing loads.
-//   One barrier per block, in its last K step, by when every wave has read the stage to its end
-// and the next block has landed: the stage is then refilled with the block after the next, whose
-// copies are issued between the MFMAs of that step and the next block's first.
+//   Two barriers per block.  At the first, late in its third K step, every wave has read the stage
+// to its end: it is refilled with the block after the next, a copy between two MFMAs, to spread
+// them.  At the second, early in the last step, the next block has landed and its first
+// fragments are read.  A copy so has nine tenths of a block's time to arrive (with one barrier for
+// both purposes six tenths).
 //   A workgroup owns its compute unit and works through a list of tiles as one sequence of blocks:
 // the next tile's first blocks are copied under the current one's last and its epilogue.
 #include "fp8_common.h"
@@ -38,9 +40,12 @@ constexpr int kTile = 256;         // rows and columns of a tile
 constexpr int kNW = 4;             // waves: 2 along the rows x 2 along the columns
 constexpr int kXcds = 8, kXcdCus = 32;
 constexpr int kPanel = 4;          // row tiles that share weights in an XCD's L2
+constexpr int kSortE = 64 * kNW;   // experts that a workgroup sorts by rows (one per thread); with more, their
+                                   // rows average out and the sort would cost more than a tile
 constexpr int kListTiles = 64;     // tiles of one workgroup at most
 constexpr int kOperandB = kTile * kBK * 2;          // bytes of an operand's block
 constexpr int kCopies = kOperandB / 1024 / kNW;     // 1 KB copies of it per wave
+constexpr int kNextAt = 9;         // copies of a block issued before the one ahead of it has to be there
 constexpr int kEpiB = 4096;        // per wave: 32 rows of 128 bytes on their way out
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
@@ -153,6 +158,13 @@ __device__ __forceinline__ uint2 pack4(const f32x16& v, int q) {
   return uint2{bf16_pack2(v[4 * q], v[4 * q + 1]), bf16_pack2(v[4 * q + 2], v[4 * q + 3])};
 }
 
+// Waits for this wave's LDS accesses, then a barrier that no memory access moves across.
+#define MOE_LDS_SYNC()                                                   \
+  do {                                                                   \
+    __builtin_amdgcn_s_waitcnt(::moe::waitcnt_vm_lgkm0(63));             \
+    asm volatile("s_barrier" ::: "memory");                              \
+  } while (0)
+
 // GATHER: the rows of a (weights: of b) are tokens', through sorted_idx.
 template <Kind KIND, bool F32, bool GATHER>
 __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, int accumulate) {
@@ -189,22 +201,35 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
       __syncthreads();
       mt = before[p.E];
     }
-    // rows: an XCD takes a contiguous range; weights: groups of 32 tiles in turn
+    // rows: an XCD takes a contiguous range.  weights: groups of 32 tiles, one for each of an XCD's
+    // compute units, dealt to the XCDs back and forth from the expert with most rows to the one
+    // with fewest.
     const int per_e = p.mt * p.nnb;
     const int G = W ? p.E * per_e : mt * p.nnb;
     const int per = (G + kXcds - 1) / kXcds;
+    auto tile_of = [&](int i) {
+      const int round = i / kXcdCus;
+      return (round * kXcds + (round & 1 ? kXcds - 1 - x : x)) * kXcdCus + i % kXcdCus;
+    };
+    int* by_rows = before + kMaxE;  // [E]: experts, most rows first
     mine = 0;
     if constexpr (W) {
-      const int groups = (G + kXcdCus - 1) / kXcdCus;
-      const int mine_g = (groups - x + kXcds - 1) / kXcds;  // this XCD's groups
-      const int n = mine_g * kXcdCus;
+      const int rounds = (G + kXcdCus * kXcds - 1) / (kXcdCus * kXcds);
+      const int n = rounds * kXcdCus;
       mine = i0 < n ? (n - i0 + NWG - 1) / NWG : 0;
-      // the last group may be short: its tiles past G are dropped
-      while (mine > 0) {
-        const int i = i0 + (mine - 1) * NWG;
-        if (((i / kXcdCus) * kXcds + x) * kXcdCus + i % kXcdCus < G) break;
-        --mine;
+      while (mine > 0 && tile_of(i0 + (mine - 1) * NWG) >= G) --mine;  // the last round may be short
+      for (int e = tid; e < p.E; e += 64 * kNW) {
+        before[e] = p.counts[e];
+        by_rows[e] = e;
       }
+      __syncthreads();
+      if (p.E <= kSortE && tid < p.E) {
+        const int n_e = before[tid];
+        int rank = 0;
+        for (int f = 0; f < p.E; ++f) rank += before[f] > n_e || (before[f] == n_e && f < tid);
+        by_rows[rank] = tid;
+      }
+      __syncthreads();
     } else {
       const int n = min(per, G - x * per);
       mine = i0 < n ? (n - i0 + NWG - 1) / NWG : 0;
@@ -215,10 +240,11 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
       const int i = i0 + tid * NWG;
       int e, row0, rows, place;
       if constexpr (W) {
-        const int v = ((i / kXcdCus) * kXcds + x) * kXcdCus + i % kXcdCus;
-        e = v / per_e;
+        const int v = tile_of(i);
+        const int at = v / per_e;
+        e = by_rows[at];
         int mb, nb;
-        panel_tile(v - e * per_e, p.mt, p.nnb, mb, nb);
+        panel_tile(v - at * per_e, p.mt, p.nnb, mb, nb);
         place = nb | mb << 16;
         rows = max(p.counts[e], 0);
         row0 = p.offsets[e];
@@ -431,8 +457,7 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
       uint4* za = reinterpret_cast<uint4*>(lds.a[s] + left * OA::kRowB);
       uint4* zb = reinterpret_cast<uint4*>(lds.b[s] + left * OB::kRowB);
       for (int i = tid; i < (kBK - left) * OA::kRowB / 16; i += 64 * kNW) za[i] = zb[i] = uint4{0, 0, 0, 0};
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
-      asm volatile("s_barrier" ::: "memory");
+      MOE_LDS_SYNC();
     }
   };
   if constexpr (W) trim(0, entry(0, 2));
@@ -456,22 +481,22 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
         for (int m = 0; m < 16; ++m) {
           const int i = m >> 2, j = m & 3;
           acc[i][j] = mfma32(bf[step & 1][j], af[step & 1][i], acc[i][j]);
-          if (step < 3) {
-            if (m < 8) get(s, step + 1, m);
-            // the rest of the copies of the block opened last (the first time: once more)
-            if (step == 0 && m >= 8 && m < 12) copy_b(s ^ 1, m - 4);
-            if constexpr (W && GATHER)
-              if (step == 2 && m >= 8) read_ring(m - 8);
-          } else {
-            if (m == 1) {
-              MOE_DMA_SYNC(0);
-              if constexpr (W) trim(s ^ 1, c + 1 < nblk ? rows - (c + 1) * kBK : rows_after);
-              advance();
-            }
-            if (m >= 2 && m < 10) get(s ^ 1, 0, m - 2);
-            if (m >= 4 && m < 12) copy_a(s, m - 4);
-            if (m >= 12) copy_b(s, m - 12);
+          if (step < 3 && m < 8) get(s, step + 1, m);
+          if constexpr (W && GATHER)
+            if (step == 1 && m >= 8) read_ring(m - 8);
+          // the stage is read to its end: the block after the next goes there
+          const int n = (step - 2) * 16 + m - 12;  // copies issued of it
+          if (n == 0) {
+            MOE_LDS_SYNC();
+            advance();
           }
+          if (n == kNextAt) {
+            MOE_DMA_SYNC(kNextAt);  // the next block has landed; those copies may be on their way
+            if constexpr (W) trim(s ^ 1, c + 1 < nblk ? rows - (c + 1) * kBK : rows_after);
+          }
+          if (n >= kNextAt && n < kNextAt + 8) get(s ^ 1, 0, n - kNextAt);
+          if (n >= 0 && n < kCopies) copy_a(s, n);
+          if (n >= kCopies && n < 2 * kCopies) copy_b(s, n - kCopies);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -481,6 +506,23 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
     // -- epilogue -----------------------------------------------------------------------------------
     uint8_t* ep = lds.epi[wave];
     const int er = lane >> 3, eu = lane & 7;
+    // kDh: gate_up of the next pieces (32 x 32) is loaded that many of them ahead
+    constexpr int kGuAhead = 3;
+    uint2 gbuf[KIND == kDh ? kGuAhead + 1 : 1][4], ubuf[KIND == kDh ? kGuAhead + 1 : 1][4];
+    auto load_gu = [&](int piece) {
+      const int col = min(nb * kTile + nh * 128 + (piece & 3) * 32 + eu * 4, p.I - 4);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = row0 + max(min(mh * 128 + (piece >> 2) * 32 + er + 8 * t, rows - 1), 0);
+        const uint16_t* src = p.gu + (size_t)row * 2 * p.I + col;
+        gbuf[piece % (kGuAhead + 1)][t] = *reinterpret_cast<const uint2*>(src);
+        ubuf[piece % (kGuAhead + 1)][t] = *reinterpret_cast<const uint2*>(src + p.I);
+      }
+    };
+    if constexpr (KIND == kDh) {
+#pragma unroll
+      for (int i = 0; i < kGuAhead; ++i) load_gu(i);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int lr = mh * 128 + i * 32;  // first of these 32 rows in the tile
@@ -581,19 +623,14 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
           }
         }
       } else {
-        if (lr >= rows) continue;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          if (i * 4 + j + kGuAhead < 16) load_gu(i * 4 + j + kGuAhead);
+          if (lr >= rows) continue;
           keep(acc[i][j]);
           const int col = nb * kTile + nh * 128 + j * 32 + eu * 4;
-          uint2 gw[4], uw[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const size_t row = (size_t)(row0 + min(lr + er + 8 * t, rows - 1));
-            const uint16_t* src = p.gu + row * 2 * p.I + min(col, p.I - 4);
-            gw[t] = *reinterpret_cast<const uint2*>(src);
-            uw[t] = *reinterpret_cast<const uint2*>(src + p.I);
-          }
+          const uint2(&gw)[4] = gbuf[(i * 4 + j) % (kGuAhead + 1)];
+          const uint2(&uw)[4] = ubuf[(i * 4 + j) % (kGuAhead + 1)];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             epi_put16(ep, lane, 2 * q + (lane >> 5),
