@@ -15,15 +15,18 @@
 // MFMAs.  The LDS delivers about 117 bytes a clock (measured; 97 through its transposing loads)
 // and takes the copies besides, so 8 waves of 128 x 64 would need it for longer than the MFMAs.
 // K goes in blocks of 64, both operands copied from memory straight into LDS, two stages.  An
-// operand with K contiguous lies as rows of 128 bytes, one with K strided as 64 rows of the tile's
-// columns, read back through the transposing loads.
-//   Two barriers per block.  At the first, late in its third K step, every wave has read the stage
-// to its end: it is refilled with the block after the next, a copy between two MFMAs, to spread
-// them.  At the second, early in the last step, the next block has landed and its first
-// fragments are read.  A copy so has nine tenths of a block's time to arrive (with one barrier for
-// both purposes six tenths).
+// operand whose K is strided is read back through the transposing loads.
+//   A wave keeps a block's fragments of the columns' operand (16 of 4 registers) and passes its
+// four row subtiles over them, 16 MFMAs each.  So a block's columns are in registers when its
+// first subtile ends, and its rows are read subtile by subtile: their places are refilled with the
+// block after the next at two barriers per block, long before the stage is done, and a copy has
+// 1.2 blocks' time to arrive.  They are spread over the MFMAs: the compute unit takes 64 bytes a
+// clock, and a wave that issues them faster stands still (one per MFMA: 500 of 2050 clocks lost
+// per block).
 //   A workgroup owns its compute unit and works through a list of tiles as one sequence of blocks:
 // the next tile's first blocks are copied under the current one's last and its epilogue.
+#include <type_traits>
+
 #include "fp8_common.h"
 #include "lds_copy.h"
 #include "moe_internal.h"
@@ -45,51 +48,60 @@ constexpr int kSortE = 64 * kNW;   // experts that a workgroup sorts by rows (on
 constexpr int kListTiles = 64;     // tiles of one workgroup at most
 constexpr int kOperandB = kTile * kBK * 2;          // bytes of an operand's block
 constexpr int kCopies = kOperandB / 1024 / kNW;     // 1 KB copies of it per wave
-constexpr int kNextAt = 9;         // copies of a block issued before the one ahead of it has to be there
 constexpr int kEpiB = 4096;        // per wave: 32 rows of 128 bytes on their way out
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// One operand's block in LDS.  STRIDED: [k][256], the 64-byte pieces of a row XORed with k % 4 so
-// that a transposing load's 4 k x 32 values meet distinct banks; else [row][64], 16-byte units
-// XORed by row.
-template <bool STRIDED>
+// One operand's block in LDS, 256 rows (or columns) x 64 K, copied in 32 pieces of 1 KB.
+//   kRows: K contiguous, [256 rows][64 K], 16-byte units XORed by row; piece n: rows 8 n to 8 n + 7.
+//   kByCols: K strided, [4 x 64 columns][64 K][64 columns], the 64-byte halves of a line exchanged
+//     where K & 2; piece n: K 8 (n % 8) to + 7 of columns 64 (n / 8).
+//   kByK: K strided, [64 K][256 columns], the 64-byte quarters of each 256 bytes XORed with K % 4;
+//     piece n: K 2 n and 2 n + 1.  Whole rows of memory, but no part is done before the whole.
+// The exchanges let a transposing load's 4 K x 32 columns meet distinct banks.
+enum Staging { kRows, kByCols, kByK };
+template <Staging L>
 struct Operand {
-  static constexpr int kRowB = STRIDED ? kTile * 2 : kBK * 2;
-  static constexpr int kLanes = kRowB / 16;  // lanes (16-byte units) of a row
-
-  // row of the block that this lane's part of copy q fills, and which unit of the source's row
-  static __device__ __forceinline__ int row_of(int wave, int q, int lane) {
-    return (wave * kCopies + q) * (64 / kLanes) + lane / kLanes;
+  static constexpr int kAddrs = L == kRows ? 1 : L == kByCols ? 2 : 4;  // subtiles with addresses of their own
+  // Of the lane's 16 bytes of piece n: the operand's row (column of a strided one) and K.
+  static __device__ __forceinline__ int row_of(int n, int lane) {
+    const int line = n * 8 + (lane >> 3);
+    if constexpr (L == kRows) return line;
+    else if constexpr (L == kByCols) return (n >> 3) * 64 + ((lane & 7) ^ ((line & 2) << 1)) * 8;
+    else return ((lane & 31) ^ ((k_of(n, lane) & 3) << 2)) * 8;
   }
-  static __device__ __forceinline__ int unit_of(int row, int lane) {
-    const int u = lane % kLanes;
-    return STRIDED ? (((u >> 2) ^ (row & 3)) << 2) | (u & 3) : u ^ a_swz(row);
+  static __device__ __forceinline__ int k_of(int n, int lane) {
+    if constexpr (L == kRows) return ((lane & 7) ^ a_swz(n * 8 + (lane >> 3))) * 8;
+    else if constexpr (L == kByCols) return (n * 8 + (lane >> 3)) & 63;
+    else return n * 2 + (lane >> 5);
   }
-  // This lane's address of subtile i (32 rows, of 4 from `first`) at K step 0; the step's own part
-  // is applied by frag.
-  static __device__ __forceinline__ int addr(int first, int i, int lane) {
-    if constexpr (STRIDED) {
-      const int l = lane & 15, k = 8 * (lane >> 5) + (l >> 2);
-      return k * kRowB + (((first + i) ^ (k & 3)) << 6) + ((lane >> 4) & 1) * 32 + (l & 3) * 8;
+  // This lane's address of subtile i (of 4, 32 rows each) of half `half` at K step 0, up to what
+  // frag adds.
+  static __device__ __forceinline__ int addr(int half, int i, int lane) {
+    const int l = lane & 15, k = 8 * (lane >> 5) + (l >> 2), in = ((lane >> 4) & 1) * 32 + (l & 3) * 8;
+    if constexpr (L == kRows) {
+      const int r = half * 128 + (lane & 31);
+      return r * 128 + (((lane >> 5) ^ a_swz(r)) << 4);
+    } else if constexpr (L == kByCols) {
+      return (half * 2 * 64 + k) * 128 + (((i & 1) ^ ((k >> 1) & 1)) << 6) + in;
     } else {
-      const int r = (first + i) * 32 + (lane & 31);
-      return r * kRowB + (((lane >> 5) ^ a_swz(r)) << 4);
+      return k * 512 + half * 256 + ((i ^ (k & 3)) << 6) + in;
     }
   }
-  // The 8 values at K = 16 s + 8 (lane / 32) of the subtile's row (column) lane % 32.
-  static __device__ __forceinline__ bf16x8 frag(const uint8_t* block, int addr, int s) {
-    if constexpr (STRIDED) {
+  // The 8 values at K = 16 s + 8 (lane / 32) of subtile i's row (column) lane % 32.
+  static __device__ __forceinline__ bf16x8 frag(const uint8_t* block, int addr, int i, int s) {
+    if constexpr (L == kRows) {
+      return *reinterpret_cast<const bf16x8*>(block + (addr ^ (s * 32)) + i * 32 * 128);
+    } else {
+      constexpr int kLine = L == kByCols ? 128 : 512;
       using lds_t = __attribute__((address_space(3))) i16x4;
-      const uint8_t* p = block + addr + s * 16 * kRowB;
+      const uint8_t* p = block + addr + s * 16 * kLine + (L == kByCols ? (i >> 1) * 64 * 128 : 0);
       const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)p);
-      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(p + 4 * kRowB));
+      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(p + 4 * kLine));
       const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       return __builtin_bit_cast(bf16x8, v);
-    } else {
-      return *reinterpret_cast<const bf16x8*>(block + (addr ^ (s * 32)));
     }
   }
 };
@@ -158,21 +170,14 @@ __device__ __forceinline__ uint2 pack4(const f32x16& v, int q) {
   return uint2{bf16_pack2(v[4 * q], v[4 * q + 1]), bf16_pack2(v[4 * q + 2], v[4 * q + 3])};
 }
 
-// Waits for this wave's LDS accesses, then a barrier that no memory access moves across.
-#define MOE_LDS_SYNC()                                                   \
-  do {                                                                   \
-    __builtin_amdgcn_s_waitcnt(::moe::waitcnt_vm_lgkm0(63));             \
-    asm volatile("s_barrier" ::: "memory");                              \
-  } while (0)
-
 // GATHER: the rows of a (weights: of b) are tokens', through sorted_idx.
 template <Kind KIND, bool F32, bool GATHER>
 __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, int accumulate) {
   constexpr bool W = KIND == kWeights;
-  constexpr bool AT = W, BT = W || KIND == kDh || KIND == kDx;
+  constexpr bool BT = W || KIND == kDh || KIND == kDx;
   constexpr int COLS = KIND == kGateUp ? kTile / 2 : kTile;
-  using OA = Operand<AT>;
-  using OB = Operand<BT>;
+  using OA = Operand<W ? kByCols : kRows>;
+  using OB = Operand<BT ? kByK : kRows>;
   __shared__ TrainLds lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -275,12 +280,16 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
 
   // -- copies -------------------------------------------------------------------------------------
   // The block being copied: tile cr, cleft blocks left of it (this one included), from asrc and
-  // bsrc at the lane's offsets.  Behind the last block the copies repeat it, into a stage that
+  // bsrc at the lane's offsets.  Behind the last block the copies repeat it, into places that
   // nobody reads: no branches around them.
+  //   A wave's pieces: of a, 4 of the waves' first two row subtiles (q < 4) and 4 of the others; of
+  // b, 8 in a row.
+  auto a_piece = [&](int q) { return (wave >> 1) * 16 + (q >> 2) * 8 + (wave & 1) * 4 + (q & 3); };
+  auto b_piece = [&](int q) { return wave * kCopies + q; };
   int cr = 0, cleft = blocks_of(0);
   const uint8_t *asrc, *bsrc;
   uint32_t ao[kCopies], bo[kCopies];
-  uint32_t bcol[2];  // weights, gathered: the lane's column in even and odd copies
+  uint32_t bcol[2];  // weights, gathered: the lane's columns in even and odd pieces
   const size_t astep = W ? (size_t)kBK * p.M * 2 : (size_t)kBK * 2;
   const size_t bstep = GATHER && W ? 0 : BT ? (size_t)kBK * p.N * 2 : (size_t)kBK * 2;
   // Gathered rows of a block of weights come by the ring lds.src, two blocks ahead of the copies:
@@ -289,7 +298,7 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
   auto issue_ring = [&]() {
     if (wave == 0) {
       if (sp == 0) {
-        srow = min(max(entry(sr, 1), 0), p.A - 1);
+        srow = min(max(entry(sr, 1), 0), p.A - 1);  // an expert without rows may start at A
         sn = max(entry(sr, 2), 1);
       }
       // rows past the segment: its last one
@@ -307,7 +316,7 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
   int rq = 0;             // blocks whose rows have been read from the ring
   uint32_t rows_next[GATHER && W ? kCopies : 1];
   auto read_ring = [&](int q) {
-    rows_next[q] = token_of((uint32_t)dbg_clamp(lds.src[rq & 3][OB::row_of(wave, q, lane)], p.A, kDbgSorted), p) *
+    rows_next[q] = token_of((uint32_t)dbg_clamp(lds.src[rq & 3][OB::k_of(b_piece(q), lane)], p.A, kDbgSorted), p) *
                    (uint32_t)(p.N * 2);
   };
   // Gathered rows of tile r on their way into LDS.
@@ -316,14 +325,35 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
     dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + entry(r, 1)), (uint32_t)i * 4u,
          lds.src[r & 1] + wave * 64);
   };
-  // A tile's last block of weights may be short: rows past the segment read its last one.
+  // The last block of an expert's rows may be short (weights): rows past the end read its last one,
+  // and trim puts zeros in their place.
   auto shorten = [&](int left) {
     if (left >= kBK) return;
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) {
-      const int over = max(OA::row_of(wave, q, lane) - max(left - 1, 0), 0);
-      ao[q] -= (uint32_t)over * (uint32_t)(p.M * 2);
-      if (!GATHER) bo[q] -= (uint32_t)over * (uint32_t)(p.N * 2);
+      auto over = [&](int k) { return (uint32_t)max(k - max(left - 1, 0), 0); };
+      ao[q] -= over(OA::k_of(a_piece(q), lane)) * (uint32_t)(p.M * 2);
+      if (!GATHER) bo[q] -= over(OB::k_of(b_piece(q), lane)) * (uint32_t)(p.N * 2);
+    }
+  };
+  // Zeros past the end in what has landed and is about to be read: the columns and the first rows
+  // (all of them: also the second), or the second rows.
+  enum { kFirst = 1, kSecond = 2 };
+  auto trim = [&](int s, int left, int parts) {
+    if constexpr (W) {
+      if (left >= kBK) return;
+      left = max(left, 0);
+      const int n = (kBK - left) * 8;  // 16-byte units of a column piece
+      for (int i = tid; i < 2 * n; i += 64 * kNW) {
+        uint8_t* line = lds.a[s] + (i >= n ? 2 : 0) * 64 * 128 + left * 128 + (i >= n ? i - n : i) * 16;
+        if (parts & kFirst) *reinterpret_cast<uint4*>(line) = uint4{0, 0, 0, 0};
+        if (parts & kSecond) *reinterpret_cast<uint4*>(line + 64 * 128) = uint4{0, 0, 0, 0};
+      }
+      if (parts & kFirst)
+        for (int i = tid; i < 4 * n; i += 64 * kNW)
+          *reinterpret_cast<uint4*>(lds.b[s] + left * 512 + i * 16) = uint4{0, 0, 0, 0};
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
+      asm volatile("s_barrier" ::: "memory");
     }
   };
   auto point_at = [&](int r) {
@@ -340,11 +370,12 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
       bsrc = GATHER ? p.b : p.b + (size_t)first * p.N * 2;
 #pragma unroll
       for (int q = 0; q < kCopies; ++q) {
-        const int lr = OA::row_of(wave, q, ln), u = OA::unit_of(lr, ln) * 8;
-        ao[q] = (uint32_t)lr * (uint32_t)(p.M * 2) + (uint32_t)min(mb * kTile + u, p.M - 8) * 2;
-        const uint32_t c = (uint32_t)min(nb * kTile + u, p.N - 8) * 2;
+        const int na = a_piece(q), nb_ = b_piece(q);
+        ao[q] = (uint32_t)OA::k_of(na, ln) * (uint32_t)(p.M * 2) +
+                (uint32_t)min(mb * kTile + OA::row_of(na, ln), p.M - 8) * 2;
+        const uint32_t c = (uint32_t)min(nb * kTile + OB::row_of(nb_, ln), p.N - 8) * 2;
         if (GATHER) bcol[q & 1] = c;
-        else bo[q] = (uint32_t)lr * (uint32_t)(p.N * 2) + c;
+        else bo[q] = (uint32_t)OB::k_of(nb_, ln) * (uint32_t)(p.N * 2) + c;
       }
       if (cleft == 1) shorten(rows);
     } else {
@@ -352,21 +383,21 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
       bsrc = p.b + (size_t)e * p.stride;
 #pragma unroll
       for (int q = 0; q < kCopies; ++q) {
-        const int lr = OA::row_of(wave, q, ln);
+        const int lr = OA::row_of(a_piece(q), ln);
         const uint32_t row = GATHER ? token_of((uint32_t)dbg_clamp(lds.src[r & 1][lr], p.A, kDbgSorted), p)
                                     : (uint32_t)max(min(lr, rows - 1), 0);
-        ao[q] = row * (uint32_t)(p.K * 2) + (uint32_t)OA::unit_of(lr, ln) * 16;
+        ao[q] = row * (uint32_t)(p.K * 2) + (uint32_t)OA::k_of(a_piece(q), ln) * 2;
       }
 #pragma unroll
       for (int q = 0; q < kCopies; ++q) {
-        const int lr = OB::row_of(wave, q, ln), u = OB::unit_of(lr, ln);
-        if constexpr (BT) {  // [K][N]: lr is k, the unit 8 columns
-          bo[q] = (uint32_t)lr * (uint32_t)(p.N * 2) + (uint32_t)min(nb * kTile + u * 8, p.N - 8) * 2;
+        const int lr = OB::row_of(b_piece(q), ln), k = OB::k_of(b_piece(q), ln);
+        if constexpr (BT) {  // [K][N]
+          bo[q] = (uint32_t)k * (uint32_t)(p.N * 2) + (uint32_t)min(nb * kTile + lr, p.N - 8) * 2;
         } else if constexpr (KIND == kGateUp) {  // a wave's 128 weight rows: 64 gate rows, their up rows
           const int col = min(nb * COLS + (lr >> 7) * 64 + (lr & 63), p.N - 1);
-          bo[q] = (uint32_t)((lr & 64) ? p.I + col : col) * (uint32_t)(p.K * 2) + (uint32_t)u * 16;
+          bo[q] = (uint32_t)((lr & 64) ? p.I + col : col) * (uint32_t)(p.K * 2) + (uint32_t)k * 2;
         } else {
-          bo[q] = (uint32_t)min(nb * kTile + lr, p.N - 1) * (uint32_t)(p.K * 2) + (uint32_t)u * 16;
+          bo[q] = (uint32_t)min(nb * kTile + lr, p.N - 1) * (uint32_t)(p.K * 2) + (uint32_t)k * 2;
         }
       }
     }
@@ -390,8 +421,8 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
       issue_ring();
     }
   };
-  auto copy_a = [&](int s, int q) { dma16(asrc, ao[q], lds.a[s] + (wave * kCopies + q) * 1024); };
-  auto copy_b = [&](int s, int q) { dma16(bsrc, bo[q], lds.b[s] + (wave * kCopies + q) * 1024); };
+  auto copy_a = [&](int s, int q) { dma16(asrc, ao[q], lds.a[s] + a_piece(q) * 1024); };
+  auto copy_b = [&](int s, int q) { dma16(bsrc, bo[q], lds.b[s] + b_piece(q) * 1024); };
 
   // -- the first two blocks -----------------------------------------------------------------------
   if constexpr (GATHER) {
@@ -428,42 +459,25 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
   MOE_DMA_SYNC(0);
 
   // -- compute ------------------------------------------------------------------------------------
-  int aa[AT ? 4 : 1], ba[BT ? 4 : 1];
+  int aa[OA::kAddrs], ba[OB::kAddrs];
 #pragma unroll
-  for (int i = 0; i < (AT ? 4 : 1); ++i) aa[i] = OA::addr(mh * 4, i, lane);
+  for (int i = 0; i < OA::kAddrs; ++i) aa[i] = OA::addr(mh, i, lane);
 #pragma unroll
-  for (int j = 0; j < (BT ? 4 : 1); ++j) ba[j] = OB::addr(nh * 4, j, lane);
+  for (int j = 0; j < OB::kAddrs; ++j) ba[j] = OB::addr(nh, j, lane);
   f32x16 acc[4][4];
-  bf16x8 af[2][4], bf[2][4];
-  auto get_a = [&](int s, int step, int i) {
-    return AT ? OA::frag(lds.a[s], aa[AT ? i : 0], step)
-              : OA::frag(lds.a[s] + i * 32 * OA::kRowB, aa[0], step);
+  bf16x8 af[2][4], bf[4][4];  // of a: two subtiles' four K steps; of b: [K step][subtile]
+  auto get_a = [&](int s, int i, int step) {
+    af[i & 1][step] = OA::frag(lds.a[s], aa[i % OA::kAddrs], i, step);
   };
-  auto get_b = [&](int s, int step, int j) {
-    return BT ? OB::frag(lds.b[s], ba[BT ? j : 0], step)
-              : OB::frag(lds.b[s] + j * 32 * OB::kRowB, ba[0], step);
+  auto get_b = [&](int s, int n) {  // in the order of their use
+    bf[n >> 2][n & 3] = OB::frag(lds.b[s], ba[(n & 3) % OB::kAddrs], n & 3, n >> 2);
   };
-  // the n-th of a step's 8 fragments, in the order that its MFMAs need them
-  auto get = [&](int s, int step, int n) {
-    if (n == 0) af[step & 1][0] = get_a(s, step, 0);
-    else if (n < 5) bf[step & 1][n - 1] = get_b(s, step, n - 1);
-    else af[step & 1][n - 4] = get_a(s, step, n - 4);
-  };
-  // zeros past the end of an expert's rows in a block that has landed (before it is read)
-  auto trim = [&](int s, int left) {
-    if constexpr (W) {
-      if (left >= kBK) return;
-      left = max(left, 0);
-      uint4* za = reinterpret_cast<uint4*>(lds.a[s] + left * OA::kRowB);
-      uint4* zb = reinterpret_cast<uint4*>(lds.b[s] + left * OB::kRowB);
-      for (int i = tid; i < (kBK - left) * OA::kRowB / 16; i += 64 * kNW) za[i] = zb[i] = uint4{0, 0, 0, 0};
-      MOE_LDS_SYNC();
-    }
-  };
-  if constexpr (W) trim(0, entry(0, 2));
   int s = 0;  // stage of the block being multiplied
+  trim(0, entry(0, 2), kFirst | kSecond);
 #pragma unroll
-  for (int n = 0; n < 8; ++n) get(s, 0, n);
+  for (int n = 0; n < 4; ++n) get_a(s, 0, n);
+#pragma unroll
+  for (int n = 0; n < 16; ++n) get_b(s, n);
   for (int r = 0; r < mine; ++r) {
     const int rows = entry(r, 2), row0 = entry(r, 1), place = entry(r, 3), nb = place & 0xffff;
     const int nblk = blocks_of(r);
@@ -475,31 +489,44 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
     for (int c = 0; c < nblk; ++c) {
+      // 64 MFMAs: subtile i = n / 16, K step (n / 4) % 4, column subtile n % 4
+      auto mfmas = [&](auto first, auto last) {
 #pragma unroll
-      for (int step = 0; step < 4; ++step) {
-#pragma unroll
-        for (int m = 0; m < 16; ++m) {
-          const int i = m >> 2, j = m & 3;
-          acc[i][j] = mfma32(bf[step & 1][j], af[step & 1][i], acc[i][j]);
-          if (step < 3 && m < 8) get(s, step + 1, m);
+        for (int n = first; n < last; ++n) {
+          const int i = n >> 4, step = (n >> 2) & 3, j = n & 3;
+          acc[i][j] = mfma32(bf[step][j], af[i & 1][step], acc[i][j]);
+          // The next block's columns replace this one's behind their last use, two in three MFMAs
+          // (faster than the LDS could keep up with otherwise): the first ten under the last
+          // subtile, the others under the next block's first, where they are used last.
+          if (n >= 50 && (n - 50) % 3 != 2) get_b(s ^ 1, (n - 50) / 3 * 2 + (n - 50) % 3);
+          if (n < 10 && (n + 14) % 3 != 2 && (n + 14) / 3 * 2 + (n + 14) % 3 < 16)
+            get_b(s, (n + 14) / 3 * 2 + (n + 14) % 3);
+          // the next subtile's rows, of the next block behind the last
+          if (n >= 10 && n < 14) get_a(s, 1, n - 10);
+          if (n >= 18 && n < 22) get_a(s, 2, n - 18);
+          if (n >= 34 && n < 38) get_a(s, 3, n - 34);
+          if (n >= 49 && n < 61 && (n - 49) % 3 == 0) get_a(s ^ 1, 0, (n - 49) / 3);
           if constexpr (W && GATHER)
-            if (step == 1 && m >= 8) read_ring(m - 8);
-          // the stage is read to its end: the block after the next goes there
-          const int n = (step - 2) * 16 + m - 12;  // copies issued of it
-          if (n == 0) {
-            MOE_LDS_SYNC();
-            advance();
-          }
-          if (n == kNextAt) {
-            MOE_DMA_SYNC(kNextAt);  // the next block has landed; those copies may be on their way
-            if constexpr (W) trim(s ^ 1, c + 1 < nblk ? rows - (c + 1) * kBK : rows_after);
-          }
-          if (n >= kNextAt && n < kNextAt + 8) get(s ^ 1, 0, n - kNextAt);
-          if (n >= 0 && n < kCopies) copy_a(s, n);
-          if (n >= kCopies && n < 2 * kCopies) copy_b(s, n - kCopies);
+            if (n >= 2 && n < 10) read_ring(n - 2);
+          if (n >= 18 && n < 34 && n % 2 == 0) copy_b(s, (n - 18) / 2);
+          if (n >= 34 && n < 42 && n % 2 == 0) copy_a(s, (n - 34) / 2);
+          if (n >= 50 && n < 62 && n % 3 == 2) copy_a(s, 4 + (n - 50) / 3);
           __builtin_amdgcn_sched_barrier(0);
         }
-      }
+      };
+      using std::integral_constant;
+      mfmas(integral_constant<int, 0>{}, integral_constant<int, 17>{});
+      // Every wave has this block's columns and its rows 0 to 63 of 128 in registers: their places
+      // are free.  Landed: this block's other rows (16 copies were issued since).
+      MOE_DMA_SYNC(16);
+      if constexpr (W) trim(s, rows - c * kBK, kSecond);
+      advance();
+      mfmas(integral_constant<int, 17>{}, integral_constant<int, 33>{});
+      mfmas(integral_constant<int, 33>{}, integral_constant<int, 49>{});
+      // ... and its other rows.  Landed: the next block's columns and first rows (likewise).
+      MOE_DMA_SYNC(16);
+      if constexpr (W) trim(s ^ 1, c + 1 < nblk ? rows - (c + 1) * kBK : rows_after, kFirst);
+      mfmas(integral_constant<int, 49>{}, integral_constant<int, 64>{});
       s ^= 1;
     }
 
