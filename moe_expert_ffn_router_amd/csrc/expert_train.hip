@@ -116,6 +116,26 @@ __device__ __forceinline__ void panel_tile(int v, int mt, int nnb, int& tile, in
 
 enum Kind { kDown, kGateUp, kDh, kDx, kWeights };
 
+// h and the gradients of g and u from dh and the kept g and u (bf16 pairs), four of them.  The
+// sigmoid is on the hardware's 2^x and 1/x (one ulp each); all three are rounded to bf16 next.
+struct GradSwiglu {
+  float h[4], dg[4], du[4];
+};
+__device__ __forceinline__ GradSwiglu grad_swiglu(const f32x4& dh, const uint2& gb, const uint2& ub) {
+  const uint32_t gw[2] = {gb.x, gb.y}, uw[2] = {ub.x, ub.y};
+  GradSwiglu r;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float g = __uint_as_float(v & 1 ? gw[v / 2] & 0xffff0000u : gw[v / 2] << 16);
+    const float u = __uint_as_float(v & 1 ? uw[v / 2] & 0xffff0000u : uw[v / 2] << 16);
+    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+    r.h[v] = g * s * u;
+    r.du[v] = dh[v] * (g * s);
+    r.dg[v] = dh[v] * u * (s * fmaf(g, 1.f - s, 1.f));
+  }
+  return r;
+}
+
 struct TrainArgs {
   int E, I, k, A;
   const int* counts;
@@ -667,30 +687,256 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
           for (int t = 0; t < 4; ++t) {
             const f32x4 dh = __builtin_bit_cast(f32x4, epi_get(ep, lane, t));
             if (col >= p.N || lr + er + 8 * t >= rows) continue;
-            const uint32_t g2[2] = {gw[t].x, gw[t].y}, u2[2] = {uw[t].x, uw[t].y};
-            float h[4], dg[4], du[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const float g = __uint_as_float(v & 1 ? g2[v / 2] & 0xffff0000u : g2[v / 2] << 16);
-              const float u = __uint_as_float(v & 1 ? u2[v / 2] & 0xffff0000u : u2[v / 2] << 16);
-              const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f));
-              h[v] = g * sg * u;
-              du[v] = dh[v] * (g * sg);
-              dg[v] = dh[v] * u * (sg * fmaf(g, 1.f - sg, 1.f));
-            }
+            const GradSwiglu d = grad_swiglu(dh, gw[t], uw[t]);
             const size_t row = (size_t)(row0 + lr + er + 8 * t);
             auto put = [](uint16_t* d, const float* f) {
               *reinterpret_cast<uint2*>(d) = uint2{bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3])};
             };
-            put(static_cast<uint16_t*>(p.out) + row * p.I + col, h);
-            put(p.out2 + row * 2 * p.I + col, dg);
-            put(p.out2 + row * 2 * p.I + p.I + col, du);
+            put(static_cast<uint16_t*>(p.out) + row * p.I + col, d.h);
+            put(p.out2 + row * 2 * p.I + col, d.dg);
+            put(p.out2 + row * 2 * p.I + p.I + col, d.du);
           }
         }
       }
     }
   }
   MOE_DMA_SYNC(0);  // nothing on its way into this workgroup's LDS any more
+}
+
+// ---------------------------------------------------------------------------
+// The same products in tiles of 64 x 64 on 4 waves of 32 x 32, K in blocks of 64 through a ring of
+// kRing stages of 16 KB: for few rows or small layers, where 256 x 256 tiles would leave most
+// compute units idle and run through their K blocks one after another.  Three blocks are on
+// their way per workgroup, two workgroups share a compute unit; a block is read for 1/4 of the
+// MFMAs that the large tiles make of it, so latency and the LDS bound it, not the MFMAs.
+// ---------------------------------------------------------------------------
+constexpr int kSmall = 64;
+constexpr int kRing = 4;
+constexpr int kSmallB = kSmall * kBK * 2;                // bytes of an operand's block
+constexpr int kSmallCopies = kSmallB / 1024 / kNW;       // 1 KB copies of it per wave
+constexpr int kIds = 16;                                 // blocks of gathered rows in LDS
+
+struct SmallLds {
+  uint8_t a[kRing][kSmallB];  // behind the loop: 4 KB per wave for the results
+  uint8_t b[kRing][kSmallB];
+  int ids[kIds][kBK];         // weights, gathered: the rows of K
+};
+
+template <Kind KIND, bool F32, bool GATHER>
+__global__ __launch_bounds__(64 * kNW, 2) void train_small_kernel(TrainArgs p, int accumulate) {
+  constexpr bool W = KIND == kWeights;
+  constexpr bool BT = W || KIND == kDh || KIND == kDx;
+  constexpr int COLS = KIND == kGateUp ? kSmall / 2 : kSmall;
+  using OA = Operand<W ? kByCols : kRows>;
+  using OB = Operand<BT ? kByCols : kRows>;
+  __shared__ SmallLds lds;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mh = wave >> 1, nh = wave & 1;
+  int e, row0, rows, mb = 0, nb;
+  if constexpr (W) {
+    const unsigned per_e = (unsigned)p.mt * (unsigned)p.nnb;
+    e = (int)(blockIdx.x / per_e);
+    const int v = (int)(blockIdx.x % per_e);
+    mb = v / p.nnb;
+    nb = v - mb * p.nnb;
+    rows = p.counts[e];
+    row0 = p.offsets[e];
+    dbg_segment(row0, rows, p.A);
+    rows = __builtin_amdgcn_readfirstlane(max(rows, 0));
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    if (rows == 0 && accumulate) return;
+  } else {
+    RowTiles<kSmall> t;
+    const int mt = t.load(p.counts, p.offsets, p.E, lane);
+    const int G = mt * p.nnb, per = (G + kXcds - 1) / kXcds;
+    const int x = (int)blockIdx.x % kXcds, i = (int)blockIdx.x / kXcds;
+    if (i >= per || x * per + i >= G) return;
+    int tile;
+    panel_tile(x * per + i, mt, p.nnb, tile, nb);
+    RowTile r = t.at(tile);
+    e = r.e;
+    row0 = r.row0;
+    rows = r.rows;
+    dbg_segment(row0, rows, p.A);
+    if (rows <= 0) return;  // only where the debug check took them away
+  }
+  const int K = W ? rows : p.K, nblk = (K + kBK - 1) / kBK;
+
+  // this wave's pieces: 2 of a and 2 of b
+  const uint8_t *asrc, *bsrc;
+  uint32_t ao[kSmallCopies], bo[kSmallCopies];
+  int ak[kSmallCopies], bk[kSmallCopies];  // weights: K of the lane's part
+#pragma unroll
+  for (int q = 0; q < kSmallCopies; ++q) {
+    const int n = wave * kSmallCopies + q;
+    ak[q] = OA::k_of(n, lane);
+    bk[q] = OB::k_of(n, lane);
+    if constexpr (W) {
+      ao[q] = (uint32_t)min(mb * kSmall + OA::row_of(n, lane), p.M - 8) * 2;
+      bo[q] = (uint32_t)min(nb * kSmall + OB::row_of(n, lane), p.N - 8) * 2;
+    } else {
+      const int r = min(OA::row_of(n, lane), rows - 1);
+      const uint32_t row = GATHER
+          ? token_of((uint32_t)dbg_clamp(p.sorted_idx[row0 + r], p.A, kDbgSorted), p) : (uint32_t)r;
+      ao[q] = row * (uint32_t)(p.K * 2) + (uint32_t)ak[q] * 2;
+      const int c = OB::row_of(n, lane);
+      if constexpr (BT) {
+        bo[q] = (uint32_t)bk[q] * (uint32_t)(p.N * 2) + (uint32_t)min(nb * kSmall + c, p.N - 8) * 2;
+      } else if constexpr (KIND == kGateUp) {  // a wave's 32 weight rows: 16 gate rows, their up rows
+        const int col = min(nb * COLS + (c >> 5) * 16 + (c & 15), p.N - 1);
+        bo[q] = (uint32_t)((c & 16) ? p.I + col : col) * (uint32_t)(p.K * 2) + (uint32_t)bk[q] * 2;
+      } else {
+        bo[q] = (uint32_t)min(nb * kSmall + c, p.N - 1) * (uint32_t)(p.K * 2) + (uint32_t)bk[q] * 2;
+      }
+    }
+  }
+  if constexpr (W) {
+    asrc = p.a + (size_t)row0 * p.M * 2;
+    bsrc = GATHER ? p.b : p.b + (size_t)row0 * p.N * 2;
+  } else {
+    asrc = GATHER ? p.a : p.a + (size_t)row0 * p.K * 2;
+    bsrc = p.b + (size_t)e * p.stride;
+  }
+  auto issue_ids = [&](int c) {
+    if (wave == 0) {
+      const int first = min(c * kBK, rows - 1);  // behind the last block: its last row, not used
+      dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + row0 + first),
+           (uint32_t)min(lane, rows - 1 - first) * 4u, lds.ids[c % kIds]);
+    }
+  };
+  // Block c into its stage; behind the last block the last one again (nobody reads it).
+  auto issue = [&](int c) {
+    const int st = c % kRing, b = min(c, nblk - 1);
+#pragma unroll
+    for (int q = 0; q < kSmallCopies; ++q) {
+      const int n = wave * kSmallCopies + q;
+      if constexpr (W) {
+        const int last = min(K - b * kBK, kBK) - 1;  // rows past the segment: its last one
+        dma16(asrc + (size_t)b * kBK * p.M * 2, ao[q] + (uint32_t)min(ak[q], last) * (uint32_t)(p.M * 2),
+              lds.a[st] + n * 1024);
+        uint32_t row = (uint32_t)min(bk[q], last);
+        if (GATHER) row = token_of((uint32_t)dbg_clamp(lds.ids[b % kIds][row], p.A, kDbgSorted), p);
+        dma16(GATHER ? bsrc : bsrc + (size_t)b * kBK * p.N * 2, bo[q] + row * (uint32_t)(p.N * 2),
+              lds.b[st] + n * 1024);
+      } else {
+        dma16(asrc + (size_t)b * kBK * 2, ao[q], lds.a[st] + n * 1024);
+        dma16(bsrc + (BT ? (size_t)b * kBK * p.N * 2 : (size_t)b * kBK * 2), bo[q], lds.b[st] + n * 1024);
+      }
+    }
+  };
+
+  f32x16 acc;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) acc[q] = 0.f;
+  const int aa = OA::addr(0, mh, lane), ba = OB::addr(0, nh, lane);
+  // kDh: gate_up of the wave's 32 x 32 results, on its way while they are summed
+  const int er = lane >> 3, eu = lane & 7;
+  const int col0 = KIND == kGateUp ? nb * COLS + nh * 16 : nb * kSmall + nh * 32;
+  uint2 gw[4], uw[4];
+  if constexpr (KIND == kDh) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int r = row0 + min(mh * 32 + er + 8 * t, rows - 1);
+      const uint16_t* src = p.gu + (size_t)r * 2 * p.I + min(col0 + eu * 4, p.I - 4);
+      gw[t] = *reinterpret_cast<const uint2*>(src);
+      uw[t] = *reinterpret_cast<const uint2*>(src + p.I);
+    }
+  }
+  if (nblk > 0) {
+    if constexpr (W && GATHER) {
+      for (int c = 0; c < 2 * kRing; ++c) issue_ids(c);
+      MOE_DMA_SYNC(0);
+    }
+#pragma unroll
+    for (int c = 0; c < kRing - 1; ++c) issue(c);
+    for (int c = 0; c < nblk; ++c) {
+      // block c has landed, every wave has read block c - 1
+      MOE_DMA_SYNC((kRing - 2) * 2 * kSmallCopies);
+      if constexpr (W && GATHER) issue_ids(c + 2 * kRing);
+      issue(c + kRing - 1);
+      uint8_t *sa = lds.a[c % kRing], *sb = lds.b[c % kRing];
+      if constexpr (W) {
+        const int left = K - c * kBK;
+        if (left < kBK) {  // zeros past the segment's end
+          for (int i = tid; i < (kBK - left) * 8; i += 64 * kNW) {
+            *reinterpret_cast<uint4*>(sa + left * 128 + i * 16) = uint4{0, 0, 0, 0};
+            *reinterpret_cast<uint4*>(sb + left * 128 + i * 16) = uint4{0, 0, 0, 0};
+          }
+          __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
+          asm volatile("s_barrier" ::: "memory");
+        }
+      }
+      bf16x8 af[4], bf[4];
+#pragma unroll
+      for (int step = 0; step < 4; ++step) {
+        // the subtile's offset is in the address for K strided, in frag for K contiguous
+        af[step] = OA::frag(sa, aa, W ? 0 : mh, step);
+        bf[step] = OB::frag(sb, ba, BT ? 0 : nh, step);
+      }
+#pragma unroll
+      for (int step = 0; step < 4; ++step) acc = mfma32(bf[step], af[step], acc);
+    }
+    MOE_DMA_SYNC(0);  // nothing on its way any more, every wave is done reading: the stages are free
+  }
+
+  // -- epilogue: the wave's 32 x 32 results as rows ---------------------------------------------------
+  uint8_t* ep = lds.a[0] + wave * kEpiB;
+  static_assert(kRing * kSmallB >= kNW * kEpiB, "room for the results");
+  auto value = [&](int q) {
+    return __builtin_bit_cast(uint4, f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]});
+  };
+  auto put = [](uint16_t* d, const float* f) {
+    *reinterpret_cast<uint2*>(d) = uint2{bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3])};
+  };
+#pragma unroll
+  for (int q = 0; q < 4; ++q) epi_put16(ep, lane, 2 * q + (lane >> 5), value(q));
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int lr = mh * 32 + er + 8 * t;
+    f32x4 v = __builtin_bit_cast(f32x4, epi_get(ep, lane, t));
+    if constexpr (W) {
+      const int m = mb * kSmall + lr, col = col0 + eu * 4;
+      if (m >= p.M || col >= p.N) continue;
+      const size_t at = ((size_t)e * p.M + m) * p.N + col;
+      if constexpr (F32) {
+        f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at);
+        if (accumulate) v += *dst;
+        *dst = v;
+      } else {
+        const float f[4] = {v[0], v[1], v[2], v[3]};
+        put(static_cast<uint16_t*>(p.out) + at, f);
+      }
+    } else if constexpr (KIND == kGateUp) {
+      // lanes 0..3 of a row hold 16 gate values, lanes 4..7 the up values of the same columns
+      float u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __shfl_xor(v[i], 4, 64);
+      const int col = col0 + (eu & 3) * 4;
+      if (lr >= rows || col >= p.N) continue;
+      const size_t row = (size_t)(row0 + lr);
+      const float f[4] = {v[0], v[1], v[2], v[3]};
+      put(p.out2 + row * 2 * p.I + (eu & 4 ? p.I : 0) + col, f);
+      if (eu & 4) continue;
+      float h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = swiglu(v[i], u[i]);
+      put(static_cast<uint16_t*>(p.out) + row * p.I + col, h);
+    } else {
+      const int col = col0 + eu * 4;
+      if (lr >= rows || col >= p.N) continue;
+      const size_t row = (size_t)(row0 + lr);
+      if constexpr (KIND == kDh) {
+        const GradSwiglu d = grad_swiglu(v, gw[t], uw[t]);
+        put(static_cast<uint16_t*>(p.out) + row * p.I + col, d.h);
+        put(p.out2 + row * 2 * p.I + col, d.dg);
+        put(p.out2 + row * 2 * p.I + p.I + col, d.du);
+      } else {
+        const float f[4] = {v[0], v[1], v[2], v[3]};
+        put(static_cast<uint16_t*>(p.out) + row * p.N + col, f);
+      }
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(uint4* out, size_t n) {
@@ -708,36 +954,71 @@ unsigned grid_of(int64_t tiles) {
   return (unsigned)(n * kXcds);
 }
 
+// 64 x 64 tiles where those of 256 x 256 are fewer than 128, and would leave half the chip idle.
+// Both sides measured (us, 256 x 256 against 64 x 64; forward unless said):
+//   1024 tokens, 2 of 8 experts of 2048 x 1024, 96 tiles per product: 76 against 67
+//   2048 of them, 160 tiles: 80 against 111;  8192, 2 of 8 of 512 x 256, 136 tiles: 42 against 57
+//   weight gradients of 8192 tokens, 2 of 8 of 512 x 256 (32 and 16 tiles): 159 against 56; of
+//   4096, 4 of 16 of 1024 x 512 (256 and 128 tiles): 110 against 138
+constexpr int64_t kFewTiles = 128;
+// Products over rows take them too where an expert has no more than 64: the weights' bytes bound
+// those, and 256 rows would be mostly padding (16 tokens, 8 of 256 of 2048 x 512: 150 against 118;
+// 1024 tokens: 425 against 421; at 128 rows an expert, 2048 tokens, 4 of 64 of 2048 x 1024, 270
+// against 345).
+constexpr int64_t kFewRows = 64;
+
 template <Kind KIND>
 int launch_rows(TrainArgs p, hipStream_t s, const char* who) {
-  constexpr int COLS = KIND == kGateUp ? kTile / 2 : kTile;
-  p.nnb = (p.N + COLS - 1) / COLS;
-  const int64_t tiles = row_tiles_bound(p.A, p.E, kTile) * p.nnb;
-  if (tiles >= (int64_t)1 << 31) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-  if constexpr (KIND == kGateUp) {
-    if (p.sorted_idx) {
-      train_gemm_kernel<KIND, false, true><<<grid_of(tiles), 64 * kNW, 0, s>>>(p, 0);
-      return check_launch(who);
+  constexpr int kShare = KIND == kGateUp ? 2 : 1;  // weight rows of an output column
+  auto tiles = [&](int side) {
+    p.nnb = (p.N * kShare + side - 1) / side;
+    return row_tiles_bound(p.A, p.E, side) * p.nnb;
+  };
+  auto launch = [&](auto gather) {
+    constexpr bool G = decltype(gather)::value;
+    // as many row tiles as rows fill, and half a tile per expert
+    const int64_t touched = p.A < p.E ? p.A : p.E;
+    tiles(kTile);
+    if ((p.A / kTile + (touched + 1) / 2) * p.nnb < kFewTiles || p.A <= kFewRows * touched) {
+      const int64_t grid = (tiles(kSmall) + kXcds - 1) / kXcds * kXcds;
+      if (grid * 64 * kNW >= (int64_t)1 << 32)
+        return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+      train_small_kernel<KIND, false, G><<<(unsigned)grid, 64 * kNW, 0, s>>>(p, 0);
+    } else {
+      const int64_t n = tiles(kTile);
+      if (n >= (int64_t)1 << 31) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+      train_gemm_kernel<KIND, false, G><<<grid_of(n), 64 * kNW, 0, s>>>(p, 0);
     }
-  }
-  train_gemm_kernel<KIND, false, false><<<grid_of(tiles), 64 * kNW, 0, s>>>(p, 0);
-  return check_launch(who);
+    return check_launch(who);
+  };
+  if constexpr (KIND == kGateUp)
+    if (p.sorted_idx) return launch(std::true_type{});
+  return launch(std::false_type{});
 }
 
 int launch_weights(TrainArgs p, bool f32, int accumulate, hipStream_t s, const char* who) {
-  p.mt = (p.M + kTile - 1) / kTile;
-  p.nnb = (p.N + kTile - 1) / kTile;
-  // whole groups for every XCD
-  const int64_t groups = ((int64_t)p.E * p.mt * p.nnb + kXcdCus - 1) / kXcdCus;
-  const int64_t per = (groups + kXcds - 1) / kXcds * kXcdCus;
-  int64_t n = kXcdCus;
-  if (n * kListTiles < per) n = (per + kListTiles - 1) / kListTiles;
-  const unsigned grid = (unsigned)(n * kXcds);
-  if (f32 && p.sorted_idx) train_gemm_kernel<kWeights, true, true><<<grid, 64 * kNW, 0, s>>>(p, accumulate);
-  else if (f32) train_gemm_kernel<kWeights, true, false><<<grid, 64 * kNW, 0, s>>>(p, accumulate);
-  else if (p.sorted_idx) train_gemm_kernel<kWeights, false, true><<<grid, 64 * kNW, 0, s>>>(p, 0);
-  else train_gemm_kernel<kWeights, false, false><<<grid, 64 * kNW, 0, s>>>(p, 0);
-  return check_launch(who);
+  auto tiles = [&](int side) {
+    p.mt = (p.M + side - 1) / side;
+    p.nnb = (p.N + side - 1) / side;
+    return (int64_t)p.E * p.mt * p.nnb;
+  };
+  auto launch = [&](auto as_f32, auto gather) {
+    constexpr bool F = decltype(as_f32)::value, G = decltype(gather)::value;
+    if (tiles(kTile) < kFewTiles) {
+      const int64_t grid = tiles(kSmall);
+      train_small_kernel<kWeights, F, G><<<(unsigned)grid, 64 * kNW, 0, s>>>(p, accumulate);
+    } else {
+      // whole groups for every XCD
+      const int64_t groups = (tiles(kTile) + kXcdCus - 1) / kXcdCus;
+      const int64_t per = (groups + kXcds - 1) / kXcds * kXcdCus;
+      int64_t n = kXcdCus;
+      if (n * kListTiles < per) n = (per + kListTiles - 1) / kListTiles;
+      train_gemm_kernel<kWeights, F, G><<<(unsigned)(n * kXcds), 64 * kNW, 0, s>>>(p, accumulate);
+    }
+    return check_launch(who);
+  };
+  if (f32) return p.sorted_idx ? launch(std::true_type{}, std::true_type{}) : launch(std::true_type{}, std::false_type{});
+  return p.sorted_idx ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
 }
 
 int check_train(const char* who, const moe_experts* W, int32_t T, int32_t k, bool gathered, Layout* Lo) {

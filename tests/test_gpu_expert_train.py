@@ -166,6 +166,14 @@ CASES = [
     dict(counts=[2, 200, 20], H=2048, I=512, k=2),
     dict(counts=[0, 0, 0], H=256, I=256, behind=7),
     dict(counts=[1] * 1024, H=128, I=128, k=2),
+    # enough tiles of 256 x 256 for them to be taken: many blocks and few, columns past the last whole
+    # tile, experts' rows in short and whole blocks, one expert with most of them
+    dict(counts=[0, 700, 256, 257, 255, 1, 63, 64, 65, 0, 512, 640, 300, 128, 129, 191, 900, 31, 400, 33],
+         H=1152, I=1152, k=2, behind=5),
+    dict(counts=[3, 2900, 0, 1100, 17, 64], H=1024, I=1408, k=3, gathered=False, behind=2),
+    dict(counts=[70, 66, 130, 0, 64, 100] * 21, H=128, I=2048, k=4),
+    dict(counts=[70, 66, 130, 0, 64, 100] * 21, H=2048, I=128, k=1, gathered=False),
+    dict(counts=[80] * 300, H=256, I=256, k=8),
 ]
 IDS = [f"{len(c['counts'])}e{sum(c['counts'])}r{c['H']}x{c['I']}" for c in CASES]
 
