@@ -318,7 +318,7 @@ extern "C" int moe_clip_grad_norm(int32_t n, const void* const* grads, const int
   for (int first = 0; first < n; first += kSet)
     if (fill(first, a) < 0) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many elements", who);
   for (int first = 0; first < n; first += kSet) {
-    const int64_t chunks = fill(first, a);
+    const int64_t chunks = sets == 1 ? a.first_chunk[a.n] : fill(first, a);
     if (chunks == 0) continue;
     const int grid = (int)(chunks < most ? chunks : most);
     norm_kernel<<<grid, 256, 0, s>>>(a, (uint32_t)chunks, parts + n_parts);
@@ -331,7 +331,7 @@ extern "C" int moe_clip_grad_norm(int32_t n, const void* const* grads, const int
     if (!clipped) return MOE_OK;
   }
   for (int first = 0; first < n; first += kSet) {
-    const int64_t chunks = fill(first, a);
+    const int64_t chunks = sets == 1 ? a.first_chunk[a.n] : fill(first, a);
     if (chunks == 0) continue;
     const int grid = (int)(chunks < kMaxParts ? chunks : kMaxParts);
     if (sets == 1)

@@ -704,32 +704,40 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
 }
 
 // ---------------------------------------------------------------------------
-// The same products in tiles of 64 x 64 on 4 waves of 32 x 32, K in blocks of 64 through a ring of
-// kRing stages of 16 KB: for few rows or small layers, where 256 x 256 tiles would leave most
-// compute units idle and run through their K blocks one after another.  Three blocks are on
-// their way per workgroup, two workgroups share a compute unit; a block is read for 1/4 of the
-// MFMAs that the large tiles make of it, so latency and the LDS bound it, not the MFMAs.
+// The same products in tiles of 64 x 64 or 128 x 128 on 4 waves of 32 x 32 or 64 x 64, K in blocks
+// of 64 through a ring of stages: for few rows or small layers, where 256 x 256 tiles would leave
+// most compute units idle and run through their K blocks one after another.  Two workgroups
+// share a compute unit, with four stages of 16 KB or two of 32 KB each; a block is read for a
+// quarter or half of the MFMAs that the large tiles make of it, so latency and the LDS bound them.
 // ---------------------------------------------------------------------------
-constexpr int kSmall = 64;
-constexpr int kRing = 4;
-constexpr int kSmallB = kSmall * kBK * 2;                // bytes of an operand's block
-constexpr int kSmallCopies = kSmallB / 1024 / kNW;       // 1 KB copies of it per wave
-constexpr int kIds = 16;                                 // blocks of gathered rows in LDS
+constexpr int kIds = 16;  // blocks of gathered rows in LDS
 
-struct SmallLds {
-  uint8_t a[kRing][kSmallB];  // behind the loop: 4 KB per wave for the results
-  uint8_t b[kRing][kSmallB];
-  int ids[kIds][kBK];         // weights, gathered: the rows of K
+template <int S>
+struct Small {
+  // 64 KB for two workgroups on a compute unit: one (three stages of 32 KB) measured slower where
+  // there are many (weight gradients of 1024 tokens, 2 of 8 experts of 2048 x 1024: 68 against 85 us)
+  static constexpr int kRing = S == 64 ? 4 : 2;
+  static constexpr int kB = S * kBK * 2;             // bytes of an operand's block
+  static constexpr int kPieces = kB / 1024 / kNW;    // 1 KB copies of it per wave
+  static constexpr int kSub = S / 64;                // 32 x 32 subtiles of a wave along each side
 };
 
-template <Kind KIND, bool F32, bool GATHER>
+template <int S>
+struct SmallLds {
+  uint8_t a[Small<S>::kRing][Small<S>::kB];  // behind the loop: 4 KB per wave for the results
+  uint8_t b[Small<S>::kRing][Small<S>::kB];
+  int ids[kIds][kBK];  // weights, gathered: the rows of K
+};
+
+template <int S, Kind KIND, bool F32, bool GATHER>
 __global__ __launch_bounds__(64 * kNW, 2) void train_small_kernel(TrainArgs p, int accumulate) {
+  constexpr int kSmall = S, kRing = Small<S>::kRing, kSmallCopies = Small<S>::kPieces, SUB = Small<S>::kSub;
   constexpr bool W = KIND == kWeights;
   constexpr bool BT = W || KIND == kDh || KIND == kDx;
   constexpr int COLS = KIND == kGateUp ? kSmall / 2 : kSmall;
   using OA = Operand<W ? kByCols : kRows>;
   using OB = Operand<BT ? kByCols : kRows>;
-  __shared__ SmallLds lds;
+  __shared__ SmallLds<S> lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int mh = wave >> 1, nh = wave & 1;
@@ -826,22 +834,40 @@ __global__ __launch_bounds__(64 * kNW, 2) void train_small_kernel(TrainArgs p, i
     }
   };
 
-  f32x16 acc;
+  f32x16 acc[SUB][SUB];
 #pragma unroll
-  for (int q = 0; q < 16; ++q) acc[q] = 0.f;
-  const int aa = OA::addr(0, mh, lane), ba = OB::addr(0, nh, lane);
-  // kDh: gate_up of the wave's 32 x 32 results, on its way while they are summed
+  for (int i = 0; i < SUB; ++i)
+#pragma unroll
+    for (int j = 0; j < SUB; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+  // subtile i of this wave is the tile's mh * SUB + i (columns: nh * SUB + j)
+  int aa[SUB], ba[SUB];
+#pragma unroll
+  for (int i = 0; i < SUB; ++i) {
+    aa[i] = OA::addr(0, mh * SUB + i, lane);
+    ba[i] = OB::addr(0, nh * SUB + i, lane);
+  }
   const int er = lane >> 3, eu = lane & 7;
-  const int col0 = KIND == kGateUp ? nb * COLS + nh * 16 : nb * kSmall + nh * 32;
-  uint2 gw[4], uw[4];
+  // first row and column of the results of subtile (i, j)
+  auto row_at = [&](int i) { return (mh * SUB + i) * 32; };
+  auto col_at = [&](int j) {
+    return KIND == kGateUp ? nb * COLS + (nh * SUB + j) * 16 : nb * kSmall + (nh * SUB + j) * 32;
+  };
+  // kDh: gate_up of the wave's results, on its way while they are summed
+  uint2 gw[KIND == kDh ? SUB : 1][SUB][4], uw[KIND == kDh ? SUB : 1][SUB][4];
   if constexpr (KIND == kDh) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r = row0 + min(mh * 32 + er + 8 * t, rows - 1);
-      const uint16_t* src = p.gu + (size_t)r * 2 * p.I + min(col0 + eu * 4, p.I - 4);
-      gw[t] = *reinterpret_cast<const uint2*>(src);
-      uw[t] = *reinterpret_cast<const uint2*>(src + p.I);
-    }
+    for (int i = 0; i < SUB; ++i)
+#pragma unroll
+      for (int j = 0; j < SUB; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int r = row0 + min(row_at(i) + er + 8 * t, rows - 1);
+          const uint16_t* src = p.gu + (size_t)r * 2 * p.I + min(col_at(j) + eu * 4, p.I - 4);
+          gw[i][j][t] = *reinterpret_cast<const uint2*>(src);
+          uw[i][j][t] = *reinterpret_cast<const uint2*>(src + p.I);
+        }
   }
   if (nblk > 0) {
     if constexpr (W && GATHER) {
@@ -859,84 +885,100 @@ __global__ __launch_bounds__(64 * kNW, 2) void train_small_kernel(TrainArgs p, i
       if constexpr (W) {
         const int left = K - c * kBK;
         if (left < kBK) {  // zeros past the segment's end
-          for (int i = tid; i < (kBK - left) * 8; i += 64 * kNW) {
-            *reinterpret_cast<uint4*>(sa + left * 128 + i * 16) = uint4{0, 0, 0, 0};
-            *reinterpret_cast<uint4*>(sb + left * 128 + i * 16) = uint4{0, 0, 0, 0};
-          }
+          for (int i = tid; i < (kBK - left) * 8; i += 64 * kNW)
+#pragma unroll
+            for (int c64 = 0; c64 < SUB; ++c64) {
+              *reinterpret_cast<uint4*>(sa + c64 * 8192 + left * 128 + i * 16) = uint4{0, 0, 0, 0};
+              *reinterpret_cast<uint4*>(sb + c64 * 8192 + left * 128 + i * 16) = uint4{0, 0, 0, 0};
+            }
           __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
           asm volatile("s_barrier" ::: "memory");
         }
       }
-      bf16x8 af[4], bf[4];
+      bf16x8 af[2][SUB], bf[2][SUB];
+      auto get = [&](int step) {
+        // a subtile's place is in the address (K strided: but the 64 columns) or added by frag
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+          af[step & 1][i] = OA::frag(sa, aa[i], mh * SUB + i, step);
+          bf[step & 1][i] = OB::frag(sb, ba[i], nh * SUB + i, step);
+        }
+      };
+      get(0);
 #pragma unroll
       for (int step = 0; step < 4; ++step) {
-        // the subtile's offset is in the address for K strided, in frag for K contiguous
-        af[step] = OA::frag(sa, aa, W ? 0 : mh, step);
-        bf[step] = OB::frag(sb, ba, BT ? 0 : nh, step);
-      }
+        if (step < 3) get(step + 1);
 #pragma unroll
-      for (int step = 0; step < 4; ++step) acc = mfma32(bf[step], af[step], acc);
+        for (int i = 0; i < SUB; ++i)
+#pragma unroll
+          for (int j = 0; j < SUB; ++j) acc[i][j] = mfma32(bf[step & 1][j], af[step & 1][i], acc[i][j]);
+      }
     }
     MOE_DMA_SYNC(0);  // nothing on its way any more, every wave is done reading: the stages are free
   }
 
   // -- epilogue: the wave's 32 x 32 results as rows ---------------------------------------------------
   uint8_t* ep = lds.a[0] + wave * kEpiB;
-  static_assert(kRing * kSmallB >= kNW * kEpiB, "room for the results");
-  auto value = [&](int q) {
-    return __builtin_bit_cast(uint4, f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]});
-  };
+  static_assert(kRing * Small<S>::kB >= kNW * kEpiB, "room for the results");
   auto put = [](uint16_t* d, const float* f) {
     *reinterpret_cast<uint2*>(d) = uint2{bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3])};
   };
 #pragma unroll
-  for (int q = 0; q < 4; ++q) epi_put16(ep, lane, 2 * q + (lane >> 5), value(q));
+  for (int i = 0; i < SUB; ++i)
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int lr = mh * 32 + er + 8 * t;
-    f32x4 v = __builtin_bit_cast(f32x4, epi_get(ep, lane, t));
-    if constexpr (W) {
-      const int m = mb * kSmall + lr, col = col0 + eu * 4;
-      if (m >= p.M || col >= p.N) continue;
-      const size_t at = ((size_t)e * p.M + m) * p.N + col;
-      if constexpr (F32) {
-        f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at);
-        if (accumulate) v += *dst;
-        *dst = v;
-      } else {
-        const float f[4] = {v[0], v[1], v[2], v[3]};
-        put(static_cast<uint16_t*>(p.out) + at, f);
-      }
-    } else if constexpr (KIND == kGateUp) {
-      // lanes 0..3 of a row hold 16 gate values, lanes 4..7 the up values of the same columns
-      float u[4];
+    for (int j = 0; j < SUB; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = __shfl_xor(v[i], 4, 64);
-      const int col = col0 + (eu & 3) * 4;
-      if (lr >= rows || col >= p.N) continue;
-      const size_t row = (size_t)(row0 + lr);
-      const float f[4] = {v[0], v[1], v[2], v[3]};
-      put(p.out2 + row * 2 * p.I + (eu & 4 ? p.I : 0) + col, f);
-      if (eu & 4) continue;
-      float h[4];
+      for (int q = 0; q < 4; ++q)
+        epi_put16(ep, lane, 2 * q + (lane >> 5),
+                  __builtin_bit_cast(uint4, f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                  acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]}));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = swiglu(v[i], u[i]);
-      put(static_cast<uint16_t*>(p.out) + row * p.I + col, h);
-    } else {
-      const int col = col0 + eu * 4;
-      if (lr >= rows || col >= p.N) continue;
-      const size_t row = (size_t)(row0 + lr);
-      if constexpr (KIND == kDh) {
-        const GradSwiglu d = grad_swiglu(v, gw[t], uw[t]);
-        put(static_cast<uint16_t*>(p.out) + row * p.I + col, d.h);
-        put(p.out2 + row * 2 * p.I + col, d.dg);
-        put(p.out2 + row * 2 * p.I + p.I + col, d.du);
-      } else {
-        const float f[4] = {v[0], v[1], v[2], v[3]};
-        put(static_cast<uint16_t*>(p.out) + row * p.N + col, f);
+      for (int t = 0; t < 4; ++t) {
+        const int lr = row_at(i) + er + 8 * t, col0 = col_at(j);
+        f32x4 v = __builtin_bit_cast(f32x4, epi_get(ep, lane, t));
+        if constexpr (W) {
+          const int m = mb * kSmall + lr, col = col0 + eu * 4;
+          if (m >= p.M || col >= p.N) continue;
+          const size_t at = ((size_t)e * p.M + m) * p.N + col;
+          if constexpr (F32) {
+            f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + at);
+            if (accumulate) v += *dst;
+            *dst = v;
+          } else {
+            const float f[4] = {v[0], v[1], v[2], v[3]};
+            put(static_cast<uint16_t*>(p.out) + at, f);
+          }
+        } else if constexpr (KIND == kGateUp) {
+          // lanes 0..3 of a row hold 16 gate values, lanes 4..7 the up values of the same columns
+          float u[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) u[x] = __shfl_xor(v[x], 4, 64);
+          const int col = col0 + (eu & 3) * 4;
+          if (lr >= rows || col >= p.N) continue;
+          const size_t row = (size_t)(row0 + lr);
+          const float f[4] = {v[0], v[1], v[2], v[3]};
+          put(p.out2 + row * 2 * p.I + (eu & 4 ? p.I : 0) + col, f);
+          if (eu & 4) continue;
+          float h[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) h[x] = swiglu(v[x], u[x]);
+          put(static_cast<uint16_t*>(p.out) + row * p.I + col, h);
+        } else {
+          const int col = col0 + eu * 4;
+          if (lr >= rows || col >= p.N) continue;
+          const size_t row = (size_t)(row0 + lr);
+          if constexpr (KIND == kDh) {
+            const GradSwiglu d = grad_swiglu(v, gw[i][j][t], uw[i][j][t]);
+            put(static_cast<uint16_t*>(p.out) + row * p.I + col, d.h);
+            put(p.out2 + row * 2 * p.I + col, d.dg);
+            put(p.out2 + row * 2 * p.I + p.I + col, d.du);
+          } else {
+            const float f[4] = {v[0], v[1], v[2], v[3]};
+            put(static_cast<uint16_t*>(p.out) + row * p.N + col, f);
+          }
+        }
       }
     }
-  }
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(uint4* out, size_t n) {
@@ -954,18 +996,21 @@ unsigned grid_of(int64_t tiles) {
   return (unsigned)(n * kXcds);
 }
 
-// 64 x 64 tiles where those of 256 x 256 are fewer than 128, and would leave half the chip idle.
-// Both sides measured (us, 256 x 256 against 64 x 64; forward unless said):
-//   1024 tokens, 2 of 8 experts of 2048 x 1024, 96 tiles per product: 76 against 67
-//   2048 of them, 160 tiles: 80 against 111;  8192, 2 of 8 of 512 x 256, 136 tiles: 42 against 57
-//   weight gradients of 8192 tokens, 2 of 8 of 512 x 256 (32 and 16 tiles): 159 against 56; of
-//   4096, 4 of 16 of 1024 x 512 (256 and 128 tiles): 110 against 138
-constexpr int64_t kFewTiles = 128;
-// Products over rows take them too where an expert has no more than 64: the weights' bytes bound
-// those, and 256 rows would be mostly padding (16 tokens, 8 of 256 of 2048 x 512: 150 against 118;
-// 1024 tokens: 425 against 421; at 128 rows an expert, 2048 tokens, 4 of 64 of 2048 x 1024, 270
-// against 345).
-constexpr int64_t kFewRows = 64;
+// Which tiles: those of 256 x 256 where there are enough to fill the chip, then those of 128 x 128,
+// else those of 64 x 64.  Measured (us, 64 / 128 / 256; the row products' tiles are counted as
+// as many as the rows fill and half a one per expert):
+//   forward of 1024 tokens, 2 of 8 experts of 2048 x 1024 (96 tiles of 256 per product, 320 of 128):
+//     68 / 55 / 77;  of 2048 (160, 576): 115 / 95 / 80;  of 8192, 2 of 8 of 512 x 256 (136, 528):
+//     58 / 48 / 40;  of 777, 3 of 13 of 1024 x 384 (48 and 64, 150 and 200): 26 / 29 / 48
+//   weight gradients of 1024 tokens, 2 of 8 of 2048 x 1024 (512 and 256 tiles of 256): 103 / 68 / 53;
+//     of 777, 3 of 13 of 1024 x 384 (156 and 104, 624 and 312 of 128): 36 / 30 / 43;  of 8192, 2 of 8
+//     of 512 x 256 (32 and 16, 128 and 64): 56 / 84 / 156
+constexpr int64_t kRowTiles256 = 128, kRowTiles128 = 300, kWeightTiles256 = 200, kWeightTiles128 = 256;
+// Experts of few rows: 256 rows would be mostly padding up to 64 rows an expert, where the weights'
+// bytes bound the product (1024 tokens, 4 of 64 experts of 2048 x 1024: 245 / 232 / 252; at 128
+// rows an expert, 2048 of them, 345 / - / 270), and 128 rows up to 16 (16 tokens, 8 of 256 of
+// 2048 x 512: 118 / 135 / 150).
+constexpr int64_t kRows256 = 64, kRows128 = 16;
 
 template <Kind KIND>
 int launch_rows(TrainArgs p, hipStream_t s, const char* who) {
@@ -978,17 +1023,19 @@ int launch_rows(TrainArgs p, hipStream_t s, const char* who) {
     constexpr bool G = decltype(gather)::value;
     // as many row tiles as rows fill, and half a tile per expert
     const int64_t touched = p.A < p.E ? p.A : p.E;
-    tiles(kTile);
-    if ((p.A / kTile + (touched + 1) / 2) * p.nnb < kFewTiles || p.A <= kFewRows * touched) {
-      const int64_t grid = (tiles(kSmall) + kXcds - 1) / kXcds * kXcds;
-      if (grid * 64 * kNW >= (int64_t)1 << 32)
-        return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-      train_small_kernel<KIND, false, G><<<(unsigned)grid, 64 * kNW, 0, s>>>(p, 0);
-    } else {
-      const int64_t n = tiles(kTile);
-      if (n >= (int64_t)1 << 31) return set_error(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-      train_gemm_kernel<KIND, false, G><<<grid_of(n), 64 * kNW, 0, s>>>(p, 0);
+    auto about = [&](int side) {
+      tiles(side);
+      return (p.A / side + (touched + 1) / 2) * (int64_t)p.nnb;
+    };
+    if (about(kTile) >= kRowTiles256 && p.A > kRows256 * touched) {
+      const unsigned grid = grid_of(tiles(kTile));
+      train_gemm_kernel<KIND, false, G><<<grid, 64 * kNW, 0, s>>>(p, 0);
+      return check_launch(who);
     }
+    const bool mid = about(128) >= kRowTiles128 && p.A >= kRows128 * touched;
+    const unsigned grid = (unsigned)((tiles(mid ? 128 : 64) + kXcds - 1) / kXcds * kXcds);
+    if (mid) train_small_kernel<128, KIND, false, G><<<grid, 64 * kNW, 0, s>>>(p, 0);
+    else train_small_kernel<64, KIND, false, G><<<grid, 64 * kNW, 0, s>>>(p, 0);
     return check_launch(who);
   };
   if constexpr (KIND == kGateUp)
@@ -1004,21 +1051,25 @@ int launch_weights(TrainArgs p, bool f32, int accumulate, hipStream_t s, const c
   };
   auto launch = [&](auto as_f32, auto gather) {
     constexpr bool F = decltype(as_f32)::value, G = decltype(gather)::value;
-    if (tiles(kTile) < kFewTiles) {
-      const int64_t grid = tiles(kSmall);
-      train_small_kernel<kWeights, F, G><<<(unsigned)grid, 64 * kNW, 0, s>>>(p, accumulate);
+    int64_t n = tiles(kTile);
+    if (n >= kWeightTiles256) {
+      // an XCD's tiles come in whole groups, and a workgroup's list holds one of each group or, of
+      // more than fit there, of some
+      const int64_t groups = (n + kXcdCus - 1) / kXcdCus;
+      const unsigned grid = grid_of((groups + kXcds - 1) / kXcds * kXcds * kXcdCus);
+      train_gemm_kernel<kWeights, F, G><<<grid, 64 * kNW, 0, s>>>(p, accumulate);
+    } else if ((n = tiles(128)) >= kWeightTiles128) {
+      train_small_kernel<128, kWeights, F, G><<<(unsigned)n, 64 * kNW, 0, s>>>(p, accumulate);
     } else {
-      // whole groups for every XCD
-      const int64_t groups = (tiles(kTile) + kXcdCus - 1) / kXcdCus;
-      const int64_t per = (groups + kXcds - 1) / kXcds * kXcdCus;
-      int64_t n = kXcdCus;
-      if (n * kListTiles < per) n = (per + kListTiles - 1) / kListTiles;
-      train_gemm_kernel<kWeights, F, G><<<(unsigned)(n * kXcds), 64 * kNW, 0, s>>>(p, accumulate);
+      n = tiles(64);
+      train_small_kernel<64, kWeights, F, G><<<(unsigned)n, 64 * kNW, 0, s>>>(p, accumulate);
     }
     return check_launch(who);
   };
-  if (f32) return p.sorted_idx ? launch(std::true_type{}, std::true_type{}) : launch(std::true_type{}, std::false_type{});
-  return p.sorted_idx ? launch(std::false_type{}, std::true_type{}) : launch(std::false_type{}, std::false_type{});
+  const std::true_type yes;
+  const std::false_type no;
+  if (f32) return p.sorted_idx ? launch(yes, yes) : launch(yes, no);
+  return p.sorted_idx ? launch(no, yes) : launch(no, no);
 }
 
 int check_train(const char* who, const moe_experts* W, int32_t T, int32_t k, bool gathered, Layout* Lo) {

@@ -174,6 +174,11 @@ CASES = [
     dict(counts=[70, 66, 130, 0, 64, 100] * 21, H=128, I=2048, k=4),
     dict(counts=[70, 66, 130, 0, 64, 100] * 21, H=2048, I=128, k=1, gathered=False),
     dict(counts=[80] * 300, H=256, I=256, k=8),
+    # for the tiles of 128 x 128: products over rows, over few rows an expert, of weights
+    dict(counts=[0, 255, 256, 257, 129, 1, 511, 340, 250], H=2048, I=2048, k=2, behind=4),
+    dict(counts=[40, 0, 17, 64, 63, 100] * 10, H=1024, I=640, k=3),
+    dict(counts=[179, 128, 64, 300, 0, 1, 127, 400, 250, 65, 200, 129, 500], H=1024, I=384, k=3, behind=1),
+    dict(counts=[179, 128, 64, 300, 0, 1, 127, 400, 250], H=640, I=640, gathered=False),
 ]
 IDS = [f"{len(c['counts'])}e{sum(c['counts'])}r{c['H']}x{c['I']}" for c in CASES]
 
