@@ -129,6 +129,20 @@ def test_many_elements():
     assert float(t[-1]) == pytest.approx(0.3, rel=2 ** -7) and float(t[0]) == pytest.approx(0.4, rel=2 ** -7)
 
 
+def test_more_than_the_caches_hold():
+    """Passes that bypass the caches, into other tensors aligned alike and not."""
+    flush("[clip] 500 MB")
+    grads, _ = make([1 << 27, 60_000_001, 77], seed=8)
+    outs, obufs = make([1 << 27, 60_000_001, 77], seed=9)
+    ns = call(grads, 2.0, outs)
+    check(ns, grads, 2.0, outs)
+    outs2, _ = make([1 << 27, 60_000_001, 77], seed=9, offsets=False)
+    assert torch.equal(call(grads, 2.0, outs2), ns)
+    assert all(torch.equal(a, b) for a, b in zip(outs, outs2))
+    for (b, off), t in zip(obufs, outs):
+        assert bool((b[:off] == MARK).all()) and bool((b[off + t.numel():] == MARK).all())
+
+
 def test_repeated_calls_and_streams_and_graph():
     grads, _ = make([70000, 4097, 13], seed=4)
     outs = [torch.empty_like(t) for t in grads]

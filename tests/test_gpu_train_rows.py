@@ -122,6 +122,43 @@ def test_gather(T, k, H, drop, spare, weighted):
     assert torch.equal(own, out)
 
 
+@pytest.mark.parametrize("k,H", [(8, 4096), (2, 16384), (16, 2048)])
+def test_rows_of_more_than_the_caches_hold(k, H):
+    """Batches that pass the caches by: the same results as in two halves, which do not (each token's
+    are its own), and as in 64 bits."""
+    T = 4300
+    flush(f"[rows] large k={k} H={H}")
+    g = torch.Generator(device=DEV).manual_seed(k)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    A = T * k
+    x, rows, w = rnd(T, H).to(BF), rnd(A, H).to(BF), torch.softmax(rnd(T, k), 1).contiguous()
+    inv = torch.randperm(A, generator=g, device=DEV).int()
+    inv[7] = -1
+    out, dy = torch.full((A, H), MARK, dtype=BF, device=DEV), torch.full((A, H), MARK, dtype=BF, device=DEV)
+    dx, dw, dw2 = torch.empty_like(x), torch.empty(T, k, device=DEV), torch.empty(T, k, device=DEV)
+    moe.moe_dispatch(x, inv, k, out, topk_w=w)
+    moe.moe_combine_backward(x, inv, w, k, dy, y_perm=rows, d_topk_w=dw)
+    moe.moe_dispatch_backward(rows, inv, k, dx, topk_w=w, d_add=x, x=x, d_topk_w=dw2)
+    assert torch.equal(out, dy)
+    ok = inv >= 0
+    at, tok = inv[ok].long(), (torch.arange(A, device=DEV) // k)[ok]
+    assert torch.equal(out[at], (x[tok].float() * w.reshape(-1)[ok][:, None]).to(BF))
+    assert int((out == MARK).all(1).sum()) == 1
+    h = T // 2
+    for part in (slice(0, h), slice(h, T)):
+        i, p = inv[part.start * k:part.stop * k].contiguous(), x[part].contiguous()
+        o, d = torch.empty_like(p), torch.empty(p.shape[0], k, device=DEV)
+        moe.moe_dispatch_backward(rows, i, k, o, topk_w=w[part].contiguous(), d_add=p, x=p, d_topk_w=d)
+        assert torch.equal(o, dx[part])   # (the dots' order of columns is another there)
+    r64 = torch.where(ok.view(T, k, 1), rows[inv.clamp(min=0).long()].view(T, k, H).double(), 0.0)
+    dots, size = (r64 * x.double()[:, None]).sum(2), (r64.abs() * x.double().abs()[:, None]).sum(2)
+    for d in (dw, dw2):
+        assert bool(((d.double() - dots).abs() <= H * EPS * size).all())
+    want = (r64 * w.double()[:, :, None]).sum(1) + x.double()
+    mag = (r64.abs() * w.double()[:, :, None]).sum(1) + x.double().abs()
+    assert bool(((dx.double() - want).abs() <= (k + 2) * EPS * mag + B * want.abs()).all())
+
+
 def test_all_dropped_and_no_rows():
     T, k, H = 5, 3, 64
     x = torch.randn(T, H, device=DEV).to(BF)
