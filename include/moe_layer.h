@@ -385,7 +385,7 @@ int moe_combine_backward(const uint16_t* d_y, const uint16_t* y_perm, const int3
  *   x           device bf16 [T][H]; row p is x[sorted_idx[p] / k]
  *   sorted_idx  device int32 [T*k], or NULL: x is device bf16 [T*k][H], its
  *               rows in expert order already (as moe_dispatch leaves them)
- *   counts, offsets  device int32 [E], [E+1]; segments within [0, T*k)
+ *   counts, offsets  device int32 [E], [E+1]; disjoint segments within [0, T*k)
  *   gate_up     device bf16 [T*k][2I] (out);  y_perm  device bf16 [T*k][H] (out)
  * Other formats return MOE_ERR_UNSUPPORTED, as does T*H >= 2^31 with
  * sorted_idx; T*k <= 2^27.
@@ -433,8 +433,8 @@ int moe_expert_ffn_backward(const moe_experts* W, const uint16_t* x, int32_t T, 
  *   scale = min(1, max_norm / (norm + 1e-6))
  *   clipped_i = scale * grad_i, rounded to grad_i's type
  * Not finite: an infinite element makes norm inf and scale 0 (finite elements
- * become 0, infinite ones NaN), a NaN makes both NaN; a caller that skips such
- * steps looks at norm.
+ * become 0, infinite ones NaN; with max_norm infinity the scale stays 1), a NaN
+ * makes both NaN; a caller that skips such steps looks at norm.
  *   grads    host array of n device pointers, aligned to their element only;
  *            numel  host int64 [n] (0 allowed);  types  host int32 [n], moe_type
  *   max_norm >= 0 (infinity: no clipping)

@@ -143,8 +143,8 @@ __device__ __forceinline__ float2 finish(const double* parts, int n, float max_n
   double sum = 0;
   for (int i = threadIdx.x; i < n; i += 256) sum += parts[i];
   const double norm = sqrt(block_sum(sum, lds));
-  // a norm that is NaN gives a scale of NaN, an infinite one 0
-  const double c = (double)max_norm / (norm + 1e-6);
+  // a norm that is NaN gives a scale of NaN, an infinite one 0 (without a limit: 1)
+  const double c = isinf(max_norm) && !isnan(norm) ? 1.0 : (double)max_norm / (norm + 1e-6);
   return float2{(float)norm, (float)(c >= 1.0 ? 1.0 : c)};
 }
 

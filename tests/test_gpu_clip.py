@@ -118,6 +118,20 @@ def test_values_that_are_not_finite():
     assert bool(ns.isnan().all())
 
 
+def test_no_limit():
+    """max_norm infinity: the scale is 1 whatever the norm, NaN for a NaN norm alone."""
+    t = torch.arange(1.0, 6000.0, device=DEV)
+    u = torch.full((100,), 2.0, dtype=BF, device=DEV)
+    assert float(call([t, u], math.inf, [t, u])[1]) == 1.0
+    t[77] = -float("inf")
+    keep, out = t.clone(), [torch.zeros_like(t), torch.zeros_like(u)]
+    ns = call([t, u], math.inf, out)
+    assert ns.tolist() == [math.inf, 1.0]
+    assert torch.equal(out[0], keep) and torch.equal(out[1], u)
+    t[78] = float("nan")
+    assert bool(call([t, u] * 70, math.inf).isnan().all())
+
+
 def test_many_elements():
     """A tensor of more than 2^31 bytes, and one element past 2^31 in a bf16 one."""
     flush("[clip] 2^31 + 5 elements")
