@@ -67,6 +67,7 @@ class MoELayer:
         self.stream_ws = None                 # streamed cache path: made on first use
         self.fp8_ws = None                    # variant "fp8": made on first use
         self.train = None                     # training buffers: made on first use
+        self.kept = None                      # (T, with shared expert) of what backward can use
         self.counts_host = torch.zeros(E, dtype=torch.int32).pin_memory()
         self.plan_out = tuple(torch.zeros(E, dtype=torch.int32) for _ in range(3))
         self.hybrid_out = tuple(torch.zeros(E, dtype=torch.int32) for _ in range(4))
@@ -89,10 +90,12 @@ class MoELayer:
     # -- individual steps ---------------------------------------------------
     def route(self, logits: torch.Tensor, stream=None):
         T = logits.shape[0]
+        self.kept = None
         moe_route(logits, self.k, self.ids, self.w, self.renorm, stream)
         return T
 
     def permute(self, T: int, stream=None):
+        self.kept = None
         moe_permute(self.ids, T, self.k, self.E, self.counts, self.offsets, self.sorted_idx,
                     self.inv_idx, self.perm_ws, stream)
 
@@ -100,6 +103,7 @@ class MoELayer:
                    variant="auto", stream=None):
         """The routed experts.  variant "fp8" (FP8 records only) takes the activations of both
         products in E4M3 (moe_expert_ffn_fp8); the others keep bf16 activations."""
+        self.kept = None
         if variant == "fp8":
             if self.fp8_ws is None:
                 with _on(stream):
@@ -121,6 +125,7 @@ class MoELayer:
                     self.y_shared if with_shared else None, self.y, stream)
 
     def route_permute(self, logits: torch.Tensor, stream=None):
+        self.kept = None
         moe_route_permute(logits, self.k, self.ids, self.w, self.counts, self.offsets,
                           self.sorted_idx, self.inv_idx, self.perm_ws, self.renorm, stream)
         return logits.shape[0]
@@ -192,6 +197,7 @@ class MoELayer:
         b = self._train_buffers(stream)
         self.route_permute(logits, stream)
         if T == 0:
+            self.kept = (0, Ws is not None)
             return self.y[:0]
         moe_expert_ffn_train(W, x, T, self.k, self.counts, self.offsets, self.sorted_idx, b["gate_up"],
                              self.y_perm, b["ws"], stream)
@@ -202,6 +208,7 @@ class MoELayer:
             moe_expert_ffn_train(Ws, x, T, 1, b["shared_counts"], b["shared_offsets"], None,
                                  b["shared_gate_up"], self.y_shared, b["ws"], stream)
         self.combine(T, Ws is not None, stream)
+        self.kept = (T, Ws is not None)
         return self.y[:T]
 
     def backward(self, logits: torch.Tensor, x: torch.Tensor, W: Experts, d_y: torch.Tensor,
@@ -213,6 +220,11 @@ class MoELayer:
         returns {"d_x", "d_logits", "d_topk_w"}.  balance, d_loss, token_mask and seq_offsets as
         for route_backward.  The results are memory of `stream`, as balance_loss's are."""
         T, E = logits.shape
+        if self.kept != (T, Ws is not None):
+            raise ValueError(f"backward of {T} tokens{' with' if Ws is not None else ' without'} a shared "
+                             f"expert, but forward_train kept {self.kept}")
+        if x.shape != (T, self.H) or d_y.shape != (T, self.H):
+            raise ValueError(f"x, d_y: expected {(T, self.H)}, got {tuple(x.shape)}, {tuple(d_y.shape)}")
         b = self._train_buffers(stream)
         with _on(stream):
             r = {"d_x": torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device),
@@ -249,6 +261,7 @@ class MoELayer:
                        slot_of_expert=None, y_shared=None, stream=None) -> torch.Tensor:
         """Whole layer in two launches (decode-sized batches)."""
         T = logits.shape[0]
+        self.kept = None
         moe_forward_decode(W, slot_of_expert, logits, x, self.k, self.ids, self.w, self.counts,
                            self.offsets, self.sorted_idx, self.inv_idx, y_shared, self.y,
                            self.decode_ws, self.renorm, stream)

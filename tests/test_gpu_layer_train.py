@@ -204,3 +204,30 @@ def test_forward_train_is_the_layers_forward():
     s = Step(T=64, E=8, H=256, I=128, k=2, seed=6)
     y = s.layer.forward_train(s.logits, s.x, s.W).clone()
     near(s.layer.forward(s.logits, s.x, s.W), y.double(), 6, "y")
+
+
+def test_backward_refuses_what_was_not_kept():
+    """Backward wants the forward_train of the same tokens, with the shared expert alike, and no other
+    call on the layer since that wrote what it kept."""
+    s = Step(T=32, E=8, H=256, I=128, k=2, shared_I=128, seed=7, T_max=64)
+    back = lambda **kw: s.layer.backward(**(dict(logits=s.logits, x=s.x, W=s.W, d_y=s.d_y, Ws=s.Ws)  # noqa: E731
+                                            | s.grads(BF) | kw))
+    with pytest.raises(ValueError):
+        back()
+    fwd = lambda: s.layer.forward_train(s.logits, s.x, s.W, s.Ws)  # noqa: E731
+    fwd()
+    back()
+    for kw in (dict(logits=s.logits[:31], x=s.x[:31], d_y=s.d_y[:31]), dict(Ws=None), dict(x=s.x[:31]),
+               dict(d_y=s.d_y[:, :128]), dict(x=s.x.view(16, 512))):
+        with pytest.raises(ValueError):
+            back(**kw)
+    s.layer.balance_loss(s.logits)
+    s.layer.combine(32, True)
+    back()
+    for other in (lambda: s.layer.forward(s.logits[:8], s.x[:8], s.W), lambda: s.layer.route(s.logits[:8]),
+                  lambda: s.layer.route_permute(s.logits), lambda: s.layer.expert_ffn(s.W, s.x, 32)):
+        fwd()
+        back()
+        other()
+        with pytest.raises(ValueError):
+            back()
