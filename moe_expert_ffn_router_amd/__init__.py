@@ -681,9 +681,17 @@ def _at_least(t, name: str, dtype, need: int, dev) -> int | None:
     return p
 
 
+def _rows(t, name: str, rows: int, width: int, dev) -> int | None:
+    """Pointer of at least `rows` bf16 rows of that width (or of a flat buffer of as many)."""
+    p = _at_least(t, name, _BF16, rows * width, dev)
+    if t.dim() == 2 and t.size(1) != width:
+        raise ValueError(f"{name}: rows of {t.size(1)}, expected {width}")
+    return p
+
+
 def _ffn_args(W: Experts, x, T: int, k: int, counts, offsets, sorted_idx, dev):
     A = T * k
-    return (_at_least(x, "x", _BF16, (T if sorted_idx is not None else A) * W.H, dev), T, k,
+    return (_rows(x, "x", T if sorted_idx is not None else A, W.H, dev), T, k,
             _at_least(counts, "counts", _I32T, W.E, dev),
             _at_least(offsets, "offsets", _I32T, W.E + 1, dev),
             None if sorted_idx is None else _at_least(sorted_idx, "sorted_idx", _I32T, A, dev))
@@ -702,8 +710,8 @@ def moe_expert_ffn_train(W: Experts, x, T: int, k: int, counts, offsets, sorted_
     A = T * k
     _check(_lib.moe_expert_ffn_train(
         ctypes.byref(W), *_ffn_args(W, x, T, k, counts, offsets, sorted_idx, dev),
-        _at_least(gate_up, "gate_up", _BF16, A * 2 * W.I, dev),
-        _at_least(y_perm, "y_perm", _BF16, A * W.H, dev), _arg(ws, "ws", _U8, None, dev), ws.numel(),
+        _rows(gate_up, "gate_up", A, 2 * W.I, dev),
+        _rows(y_perm, "y_perm", A, W.H, dev), _arg(ws, "ws", _U8, None, dev), ws.numel(),
         _stream_on(stream, dev)), "moe_expert_ffn_train")
 
 
@@ -725,9 +733,9 @@ def moe_expert_ffn_backward(W: Experts, x, T: int, k: int, counts, offsets, sort
     wt = types.pop() if types else _BF16
     _check(_lib.moe_expert_ffn_backward(
         ctypes.byref(W), *_ffn_args(W, x, T, k, counts, offsets, sorted_idx, dev),
-        _at_least(gate_up, "gate_up", _BF16, A * 2 * W.I, dev),
-        _at_least(d_y_perm, "d_y_perm", _BF16, A * W.H, dev),
-        None if d_x_perm is None else _at_least(d_x_perm, "d_x_perm", _BF16, A * W.H, dev),
+        _rows(gate_up, "gate_up", A, 2 * W.I, dev),
+        _rows(d_y_perm, "d_y_perm", A, W.H, dev),
+        None if d_x_perm is None else _rows(d_x_perm, "d_x_perm", A, W.H, dev),
         _opt(d_w13, "d_w13", wt, W.E * 2 * W.I * W.H, dev), _opt(d_w2, "d_w2", wt, W.E * W.H * W.I, dev),
         _GRAD_TYPE[wt], int(accumulate), _arg(ws, "ws", _U8, None, dev), ws.numel(),
         _stream_on(stream, dev)), "moe_expert_ffn_backward")

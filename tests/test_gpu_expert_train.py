@@ -407,3 +407,71 @@ def test_binding_refuses():
     with pytest.raises(moe.MoeError) as err:
         moe.moe_expert_ffn_train(*args[:-1], c.ws[:256])
     assert err.value.status == moe.MOE_ERR_WORKSPACE
+
+
+def test_binding_refuses_rows_of_another_width():
+    """Longer buffers are taken, wider rows are not (their rows would be read out of place)."""
+    c = Case([8, 8], 128, 128, seed=16)
+    wide, gu, y = c.new(16, 256), c.new(16, 256), c.new(16, 128)
+    good = [c.W, c.x, 16, 1, c.counts, c.offsets, c.sorted_idx, gu, y, c.ws]
+    for at, bad in ((1, wide), (7, c.new(16, 512)), (8, wide)):
+        args = good[:at] + [bad] + good[at + 1:]
+        with pytest.raises(ValueError):
+            moe.moe_expert_ffn_train(*args)
+        with pytest.raises(ValueError):
+            moe.moe_expert_ffn_backward(*args, d_x_perm=c.new(16, 128))
+    with pytest.raises(ValueError):
+        moe.moe_expert_ffn_backward(*good, d_x_perm=wide)
+    moe.moe_expert_ffn_train(*good[:7], c.new(32 * 256), c.new(20, 128), c.ws)
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+def test_offsets_past_32_bits(gathered):
+    """140000 rows of which the last 260 belong to experts: gate_up and its gradient have more than
+    2^32 elements."""
+    n, H, I, A = [100, 0, 160], 128, 16384, 140000
+    flush(f"[train] offsets past 32 bits, gathered={gathered}")
+    c = Case(n, H, I, seed=17, gathered=gathered)
+    first = A - c.n
+    gu, y, dx = c.new(A, 2 * I), c.new(A, H), c.new(A, H)
+    d13, d2 = c.new(3, 2 * I, H, dtype=F32), c.new(3, H, I, dtype=F32)
+    ws = torch.empty(moe.moe_expert_ffn_backward_workspace(c.W, A, 1), dtype=torch.uint8, device=DEV)
+    x, dy = torch.zeros((A, H), dtype=BF, device=DEV), torch.zeros((A, H), dtype=BF, device=DEV)
+    x[first:], dy[first:] = c.rows, c.dy
+    order = None
+    if gathered:  # the rows in use come from the first tokens
+        x[:c.n], x[first:] = c.rows, 0
+        order = (torch.arange(A, device=DEV) - first).remainder(A).int()
+    c.offsets += first
+    moe.moe_expert_ffn_train(c.W, x, A, 1, c.counts, c.offsets, order, gu, y, ws)
+    torch.cuda.synchronize()
+    assert bool((gu[:first:1000] == MARK).all()) and bool((y[:first] == MARK).all())
+    check_forward(c, gu[first:], y[first:])
+    gu[first:] = c.gu
+    moe.moe_expert_ffn_backward(c.W, x, A, 1, c.counts, c.offsets, order, gu, dy, ws, dx, d13, d2)
+    torch.cuda.synchronize()
+    assert bool((dx[:first] == MARK).all())
+    check_backward(c, dx[first:], d13, d2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_weights_past_32_bits(dtype):
+    """9 experts of 16384 x 16384, rows in the last: the weights and their gradients have more than
+    2^32 elements."""
+    E, H, I, n = 9, 16384, 16384, 70
+    flush(f"[train] weights past 32 bits {dtype}")
+    c = Case([n], H, I, seed=18, gathered=False)
+    rec = torch.zeros((E, c.rec.shape[1]), dtype=BF, device=DEV)
+    rec[E - 1] = c.rec[0]
+    W = moe.experts("bf16", E, H, I, rec, rec.shape[1] * 2)
+    counts, offsets = torch.zeros(E, dtype=torch.int32, device=DEV), torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    counts[-1], offsets[-1] = n, n
+    gu, y, dx = c.new(n, 2 * I), c.new(n, H), c.new(n, H)
+    moe.moe_expert_ffn_train(W, c.x, n, 1, counts, offsets, None, gu, y, c.ws)
+    torch.cuda.synchronize()
+    check_forward(c, gu, y)
+    d13, d2 = c.new(E, 2 * I, H, dtype=dtype), c.new(E, H, I, dtype=dtype)
+    moe.moe_expert_ffn_backward(W, c.x, n, 1, counts, offsets, None, c.gu, c.dy, c.ws, dx, d13, d2)
+    torch.cuda.synchronize()
+    check_backward(c, dx, d13[E - 1:], d2[E - 1:])
+    assert not bool(d13[:E - 1].any()) and not bool(d2[:E - 1].any())
