@@ -9,9 +9,13 @@
 // each: a wave owns 512 columns of a token (16 bytes per lane) and has the loads of all k rows in
 // flight together.  Products and sums are fp32, one rounding to bf16; dots add a lane's products
 // column by column, then the lanes and waves of a token in a fixed order.
-//   Batches of more rows than the memory-side cache holds bypass it (NT): 16384 tokens in 8 rows
-// each, us: scatter of 7168 columns 432 -> 416 (the tokens' rows by the cache: 429 without),
-// gather of 4096 272 -> 249, scatter with dots of 7168 804 -> 792, 4.8 to 5.4 TB/s.  Smaller ones are
+//   The four waves of a workgroup share a token of more than 512 columns, so that all of its loads
+// are issued at once, and take a token each of up to 512.  us, one wave a token / four (scatter,
+// gather, scatter with dots; 8 rows a token, of the 512 columns 2): 64 tokens of 2048
+// 4.7 5.1 7.6 / 2.9 2.9 4.4, 8192 of 2048 68 67 131 / 60 62 119, 65536 of 512 39 41 69 / 51 45 79.
+//   Batches of more rows than the memory-side cache holds bypass it (NT).  us, through it / past it,
+// the same: 8192 tokens of 2048 60 62 119 / 53 54 114, 16384 of 7168 422 425 803 / 421 390 794: 4.8 to
+// 5.4 TB/s.  (The tokens' rows go by the cache in the plain scatter: 429 without.)  Smaller ones are
 // left where the next call finds them.
 #include "fp8_common.h"
 #include "moe_internal.h"
@@ -147,14 +151,15 @@ __global__ __launch_bounds__(256) void rows_kernel(RowArgs p) {
 
 template <bool GATHER, bool DOT, int KM>
 int launch_k(const RowArgs& p, hipStream_t s, const char* who) {
-  // few tokens: all four waves of a workgroup on one
-  const unsigned quads = (unsigned)((p.T + 3) / 4);
-  if (p.T <= 4096)
-    rows_kernel<GATHER, DOT, KM, 4, false><<<(unsigned)p.T, 256, 0, s>>>(p);
-  else if ((int64_t)p.T * p.k * p.H * 2 < kMemorySideCache)
-    rows_kernel<GATHER, DOT, KM, 1, false><<<quads, 256, 0, s>>>(p);
-  else
-    rows_kernel<GATHER, DOT, KM, 1, true><<<quads, 256, 0, s>>>(p);
+  const bool nt = (int64_t)p.T * p.k * p.H * 2 >= kMemorySideCache;
+  if (p.H > 512) {
+    if (nt) rows_kernel<GATHER, DOT, KM, 4, true><<<(unsigned)p.T, 256, 0, s>>>(p);
+    else rows_kernel<GATHER, DOT, KM, 4, false><<<(unsigned)p.T, 256, 0, s>>>(p);
+  } else {
+    const unsigned quads = (unsigned)((p.T + 3) / 4);
+    if (nt) rows_kernel<GATHER, DOT, KM, 1, true><<<quads, 256, 0, s>>>(p);
+    else rows_kernel<GATHER, DOT, KM, 1, false><<<quads, 256, 0, s>>>(p);
+  }
   return check_launch(who);
 }
 

@@ -25,6 +25,11 @@
 // per block).
 //   A workgroup owns its compute unit and works through a list of tiles as one sequence of blocks:
 // the next tile's first blocks are copied under the current one's last and its epilogue.
+//   Measured, 16384 tokens over 8 of 64 experts of 4096 x 1024: dh 1147 us (0.96 PFLOP/s, its
+// epilogue moves 655 KB a tile), dx 2030 (1.08), dW13 2140 (1.03), dWd 957 (1.15); library products
+// of these layouts reach 1.06 to 1.23.  The card is at its power limit (1.6 to 1.75 GHz); a block takes
+// 2630 clocks (weights: 2880), 2048 of them MFMAs, 2200 without its copies.  4096 tokens over 8 of 64
+// of 2048 x 1024: gate/up 300 to 350 us, down 157 to 180, a quarter of it rows past the experts' last.
 #include <type_traits>
 
 #include "fp8_common.h"
@@ -709,6 +714,8 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
 // most compute units idle and run through their K blocks one after another.  Two workgroups
 // share a compute unit, with four stages of 16 KB or two of 32 KB each; a block is read for a
 // quarter or half of the MFMAs that the large tiles make of it, so latency and the LDS bound them.
+//   Measured: FFN of 64 tokens over 2 of 8 experts of 256 x 128 6.6 + 4.4 us; gradient of 777 tokens
+// over 3 of 13 of 1024 x 384 13.6 us (dh) + 33 (the rest), 76 MB and 11 GFLOP: 16 us at a copy's rate.
 // ---------------------------------------------------------------------------
 constexpr int kIds = 16;  // blocks of gathered rows in LDS
 

@@ -6,8 +6,8 @@ one stream through the C ABI.  With an expert cache, the slot-table path is
 route -> permute -> counts to host -> expert_cache_lookup -> expert_cache_fill
 -> expert_ffn (through the slot table) -> combine; the streamed variant hands
 the whole step to moe_expert_ffn_streamed (waves, grouped fills on a side
-stream, the FFN behind them).  No arithmetic happens here; it only sequences
-library calls.
+stream, the FFN behind them).  forward_train and backward are a training step
+over BF16 records.  No arithmetic happens here; it only sequences library calls.
 """
 from __future__ import annotations
 

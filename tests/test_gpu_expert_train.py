@@ -475,3 +475,34 @@ def test_weights_past_32_bits(dtype):
     torch.cuda.synchronize()
     check_backward(c, dx, d13[E - 1:], d2[E - 1:])
     assert not bool(d13[:E - 1].any()) and not bool(d2[:E - 1].any())
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn on one stream, each with other eager calls between."""
+    a, b = Case([200, 0, 300], 256, 256, k=2, seed=19), Case([10, 600], 512, 256, seed=20)
+    if b.ws.numel() > a.ws.numel():
+        a.ws = b.ws
+    else:
+        b.ws = a.ws
+    want = [[t.clone() for t in (*c.forward(), *c.backward())] for c in (a, b)]
+    outs, graphs = [], []
+    for c in (a, b):
+        fo = (c.new(c.A, 2 * c.I), c.new(c.A, c.H))
+        bo = (c.new(c.A, c.H), c.new(c.E, 2 * c.I, c.H), c.new(c.E, c.H, c.I))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            moe.moe_expert_ffn_train(c.W, c.x, c.T, c.k, c.counts, c.offsets, c.sorted_idx, *fo, c.ws)
+            c.backward(out=bo)
+        outs.append((*fo, *bo))
+        graphs.append(g)
+    for r in range(4):
+        for i in ((0, 1), (1, 0), (0, 0), (1, 1))[r]:
+            for t in outs[i]:
+                t.zero_()
+            graphs[i].replay()
+            (b, a)[i].backward()
+            c = (a, b)[i]
+            for got, w in zip(outs[i], want[i]):
+                n = c.n if got.shape[0] == c.A else len(got)
+                assert torch.equal(got[:n], w[:n])
