@@ -381,6 +381,7 @@ int moe_combine_backward(const uint16_t* d_y, const uint16_t* y_perm, const int3
  *   g, u      = x_p W_gate[e]^T, x_p W_up[e]^T   (fp32 sums)
  *   gate_up_p = bf16(g), bf16(u) side by side
  *   y_perm_p  = bf16( bf16(SiLU(g) u) W_down[e]^T )
+ * (batches of at most 96 rows and 32768 values SiLU(g) u: those to 15 bits).
  * Rows in no expert's segment are left as they were, in gate_up and y_perm.
  *   x           device bf16 [T][H]; row p is x[sorted_idx[p] / k]
  *   sorted_idx  device int32 [T*k], or NULL: x is device bf16 [T*k][H], its
@@ -405,7 +406,8 @@ typedef enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 } moe_type;
  *   d_x_perm_p = bf16( dg W_gate[e] + du W_up[e] )
  *   d_w13[e]   = sum over the rows of e of (dg, du)^T x_p      [2I][H]
  *   d_w2[e]    = sum over the rows of e of d_y_p^T h           [H][I]
- * with fp32 sums; h, dg and du are rounded to bf16 as operands.  Each output
+ * with fp32 sums; h, dg and du are rounded to bf16 as operands (small batches
+ * as in moe_expert_ffn_train: to 15 bits).  Each output
  * may be NULL (not wanted).  An expert without rows gets gradients of 0.
  *   x, sorted_idx, counts, offsets   as in moe_expert_ffn_train
  *   gate_up   device bf16 [T*k][2I], as written there

@@ -7,8 +7,9 @@
 //   rows     out[p][n] = sum_k A[p][k] B[n][k]: the forward's two (weights as stored, K contiguous)
 //            and dh, dx (the weights' other index is summed over: K strided);
 //   weights  out[e][m][n] = sum_(p of e) A[p][m] B[p][n]: both operands K strided.
-// Roundings: h and (dg; du) go to bf16 once, as the operands of the next product; the forward's
-// h comes from the fp32 gate and up sums, the gradient's from the kept bf16 ones.
+// Roundings: h and (dg; du) go to bf16 once, as the operands of the next product (small batches: to
+// two bf16 parts); the forward's h comes from the fp32 gate and up sums, the gradient's from the kept
+// bf16 ones.
 //
 // Tiles of 256 x 256 outputs on 4 waves, one per SIMD, 128 x 128 outputs each (all of a wave's
 // 256 accumulation registers): a K step of 16 then reads 8 KB of operands per wave from LDS for 16
@@ -154,6 +155,9 @@ struct TrainArgs {
   void* out;               // [A][N]; kGateUp, kDh: h [A][I]; kWeights: [E][M][N]
   uint16_t* out2;          // kGateUp: gate_up; kDh: (dg; du)
   const uint16_t* gu;      // kDh: gate_up
+  // Small batches: what rounding the products between (h, dg and du) to bf16 takes off, itself in bf16,
+  // behind them by so many bytes (0: not kept): as operands (a, b), as results (h: out, dg and du: out2)
+  int64_t a_rest, b_rest, out_rest, out2_rest;
   uint32_t k_magic;        // floor(2^32 / k) + 1: a / k for k > 1 and a < 2^27 as a 64-bit product's high word
 };
 
@@ -737,7 +741,7 @@ struct SmallLds {
 };
 
 // Tile `block` of a product (rows: of those on XCD block % 8).
-template <int S, Kind KIND, bool F32, bool GATHER>
+template <int S, Kind KIND, bool F32, bool GATHER, bool TWO>
 __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, unsigned block,
                                            SmallLds<S>& lds) {
   constexpr int kSmall = S, kRing = Small<S>::kRing, kSmallCopies = Small<S>::kPieces, SUB = Small<S>::kSub;
@@ -777,7 +781,10 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
     dbg_segment(row0, rows, p.A);
     if (rows <= 0) return;  // only where the debug check took them away
   }
-  const int K = W ? rows : p.K, nblk = (K + kBK - 1) / kBK;
+  const int K = W ? rows : p.K, nk = (K + kBK - 1) / kBK;
+  // TWO: one operand is in two parts, once over K with each
+  const int nblk = TWO && KIND != kGateUp && KIND != kDh ? 2 * nk : nk;
+  auto k_block = [&](int c) { return TWO && c >= nk ? c - nk : c; };
 
   // this wave's pieces: 2 of a and 2 of b
   const uint8_t *asrc, *bsrc;
@@ -816,28 +823,30 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
   }
   auto issue_ids = [&](int c) {
     if (wave == 0) {
-      const int first = min(c * kBK, rows - 1);  // behind the last block: its last row, not used
+      const int first = min(k_block(min(c, nblk - 1)) * kBK, rows - 1);  // behind the last block: not used
       dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + row0 + first),
            (uint32_t)min(lane, rows - 1 - first) * 4u, lds.ids[c % kIds]);
     }
   };
   // Block c into its stage; behind the last block the last one again (nobody reads it).
   auto issue = [&](int c) {
-    const int st = c % kRing, b = min(c, nblk - 1);
+    const int st = c % kRing, at = min(c, nblk - 1), b = k_block(at);
+    const uint8_t* a0 = asrc + (TWO && at >= nk ? p.a_rest : 0);
+    const uint8_t* b0 = bsrc + (TWO && at >= nk ? p.b_rest : 0);
 #pragma unroll
     for (int q = 0; q < kSmallCopies; ++q) {
       const int n = wave * kSmallCopies + q;
       if constexpr (W) {
         const int last = min(K - b * kBK, kBK) - 1;  // rows past the segment: its last one
-        dma16(asrc + (size_t)b * kBK * p.M * 2, ao[q] + (uint32_t)min(ak[q], last) * (uint32_t)(p.M * 2),
+        dma16(a0 + (size_t)b * kBK * p.M * 2, ao[q] + (uint32_t)min(ak[q], last) * (uint32_t)(p.M * 2),
               lds.a[st] + n * 1024);
         uint32_t row = (uint32_t)min(bk[q], last);
-        if (GATHER) row = token_of((uint32_t)dbg_clamp(lds.ids[b % kIds][row], p.A, kDbgSorted), p);
-        dma16(GATHER ? bsrc : bsrc + (size_t)b * kBK * p.N * 2, bo[q] + row * (uint32_t)(p.N * 2),
+        if (GATHER) row = token_of((uint32_t)dbg_clamp(lds.ids[at % kIds][row], p.A, kDbgSorted), p);
+        dma16(GATHER ? b0 : b0 + (size_t)b * kBK * p.N * 2, bo[q] + row * (uint32_t)(p.N * 2),
               lds.b[st] + n * 1024);
       } else {
-        dma16(asrc + (size_t)b * kBK * 2, ao[q], lds.a[st] + n * 1024);
-        dma16(bsrc + (BT ? (size_t)b * kBK * p.N * 2 : (size_t)b * kBK * 2), bo[q], lds.b[st] + n * 1024);
+        dma16(a0 + (size_t)b * kBK * 2, ao[q], lds.a[st] + n * 1024);
+        dma16(b0 + (BT ? (size_t)b * kBK * p.N * 2 : (size_t)b * kBK * 2), bo[q], lds.b[st] + n * 1024);
       }
     }
   };
@@ -891,7 +900,7 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
       issue(c + kRing - 1);
       uint8_t *sa = lds.a[c % kRing], *sb = lds.b[c % kRing];
       if constexpr (W) {
-        const int left = K - c * kBK;
+        const int left = K - k_block(c) * kBK;
         if (left < kBK) {  // zeros past the segment's end
           for (int i = tid; i < (kBK - left) * 8; i += 64 * kNW)
 #pragma unroll
@@ -928,8 +937,28 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
   // -- epilogue: the wave's 32 x 32 results as rows ---------------------------------------------------
   uint8_t* ep = lds.a[0] + wave * kEpiB;
   static_assert(kRing * Small<S>::kB >= kNW * kEpiB, "room for the results");
+  // put: four bf16 values; put2: TWO: in two parts, `rest` bytes apart.  The first is cut, so that the second
+  // has its sign (or stands for nothing at 2^-20 of it): an infinity that meets them stays one.
   auto put = [](uint16_t* d, const float* f) {
     *reinterpret_cast<uint2*>(d) = uint2{bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3])};
+  };
+  auto put2 = [&](uint16_t* d, const float* f, int64_t rest) {
+    if constexpr (!TWO) {
+      put(d, f);
+      return;
+    }
+    uint32_t hi[4];
+    float lo[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      hi[x] = __float_as_uint(f[x]) & 0xffff0000u;
+      const float h = __uint_as_float(hi[x]), r = f[x] - h;
+      lo[x] = fabsf(r) > 0.f ? r : h * 0x1p-20f;  // also of infinities (r is NaN)
+      if (f[x] != f[x]) hi[x] |= 0x00400000u;     // a NaN whose cut bits alone said so
+    }
+    *reinterpret_cast<uint2*>(d) = uint2{hi[0] >> 16 | hi[1], hi[2] >> 16 | hi[3]};
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(d) + rest) =
+        uint2{bf16_pack2(lo[0], lo[1]), bf16_pack2(lo[2], lo[3])};
   };
 #pragma unroll
   for (int i = 0; i < SUB; ++i)
@@ -970,16 +999,16 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
           float h[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) h[x] = swiglu(v[x], u[x]);
-          put(static_cast<uint16_t*>(p.out) + row * p.I + col, h);
+          put2(static_cast<uint16_t*>(p.out) + row * p.I + col, h, p.out_rest);
         } else {
           const int col = col0 + eu * 4;
           if (lr >= rows || col >= p.N) continue;
           const size_t row = (size_t)(row0 + lr);
           if constexpr (KIND == kDh) {
             const GradSwiglu d = grad_swiglu(v, gw[i][j][t], uw[i][j][t]);
-            put(static_cast<uint16_t*>(p.out) + row * p.I + col, d.h);
-            put(p.out2 + row * 2 * p.I + col, d.dg);
-            put(p.out2 + row * 2 * p.I + p.I + col, d.du);
+            put2(static_cast<uint16_t*>(p.out) + row * p.I + col, d.h, p.out_rest);
+            put2(p.out2 + row * 2 * p.I + col, d.dg, p.out2_rest);
+            put2(p.out2 + row * 2 * p.I + p.I + col, d.du, p.out2_rest);
           } else {
             const float f[4] = {v[0], v[1], v[2], v[3]};
             put(static_cast<uint16_t*>(p.out) + row * p.N + col, f);
@@ -989,10 +1018,10 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
     }
 }
 
-template <int S, Kind KIND, bool GATHER>
+template <int S, Kind KIND, bool GATHER, bool TWO>
 __global__ __launch_bounds__(64 * kNW, 2) void train_small_kernel(TrainArgs p) {
   __shared__ SmallLds<S> lds;
-  small_tile<S, KIND, false, GATHER>(p, 0, blockIdx.x, lds);
+  small_tile<S, KIND, false, GATHER, TWO>(p, 0, blockIdx.x, lds);
 }
 
 // The gradient's three products behind dh - dx, dW13, dWd - do not depend on each other: what
@@ -1005,7 +1034,7 @@ struct SmallJob {
 };
 
 // GATHER: the rows of dW13's x.
-template <bool F32, bool GATHER>
+template <bool F32, bool GATHER, bool TWO>
 __global__ __launch_bounds__(64 * kNW, 2) void train_rest_kernel(SmallJob dx, SmallJob w13, SmallJob w2,
                                                                  int accumulate) {
   __shared__ union {
@@ -1014,19 +1043,19 @@ __global__ __launch_bounds__(64 * kNW, 2) void train_rest_kernel(SmallJob dx, Sm
   } lds;
   unsigned b = blockIdx.x;
   if (b < dx.blocks) {  // first, its XCDs being the launch's
-    if (dx.side == 64) small_tile<64, kDx, false, false>(dx.p, 0, b, lds.s64);
-    else small_tile<128, kDx, false, false>(dx.p, 0, b, lds.s128);
+    if (TWO || dx.side == 64) small_tile<64, kDx, false, false, TWO>(dx.p, 0, b, lds.s64);
+    else small_tile<128, kDx, false, false, TWO>(dx.p, 0, b, lds.s128);
     return;
   }
   b -= dx.blocks;
   if (b < w13.blocks) {
-    if (w13.side == 64) small_tile<64, kWeights, F32, GATHER>(w13.p, accumulate, b, lds.s64);
-    else small_tile<128, kWeights, F32, GATHER>(w13.p, accumulate, b, lds.s128);
+    if (w13.side == 64) small_tile<64, kWeights, F32, GATHER, TWO>(w13.p, accumulate, b, lds.s64);
+    else small_tile<128, kWeights, F32, GATHER, TWO>(w13.p, accumulate, b, lds.s128);
     return;
   }
   b -= w13.blocks;
-  if (w2.side == 64) small_tile<64, kWeights, F32, false>(w2.p, accumulate, b, lds.s64);
-  else small_tile<128, kWeights, F32, false>(w2.p, accumulate, b, lds.s128);
+  if (w2.side == 64) small_tile<64, kWeights, F32, false, TWO>(w2.p, accumulate, b, lds.s64);
+  else small_tile<128, kWeights, F32, false, TWO>(w2.p, accumulate, b, lds.s128);
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(uint4* out, size_t n) {
@@ -1060,6 +1089,20 @@ constexpr int64_t kRowTiles256 = 128, kRowTiles128 = 300, kWeightTiles256 = 200,
 // 2048 x 512: 118 / 135 / 150).
 constexpr int64_t kRows256 = 64, kRows128 = 16;
 
+// Small batches keep h, dg and du in two bf16 parts, up to this many rows and values of h: with few
+// of them a handful carries a result's norm, and how their rounding falls shows in it (up to 1.8 times the
+// error of a result rounded once, with two parts 1.0; larger batches: 1.4).  us, one part / two:
+// forward and gradient of 3 tokens over 2 experts of 256 x 512 11.0 12.7 / 13.1 17.2, of 8 over 22 of
+// 2304 x 640 23 95 / 26 84 (in the smaller tiles that two parts take).
+constexpr int kTwoRows = 96, kTwoValues = 32768;
+
+// Rows of a workspace for A rows that have second parts (smaller batches may run in it).
+size_t two_part_rows(size_t A, int I) {
+  const size_t most = kTwoValues / I < kTwoRows ? kTwoValues / I : kTwoRows;
+  return A < most ? A : most;
+}
+bool in_two_parts(const TrainArgs& p) { return two_part_rows((size_t)p.A, p.I) == (size_t)p.A; }
+
 // Tiles of a product: their side and how many workgroups.  Sets the arguments' counts of tiles.
 struct Tiling {
   int side;
@@ -1074,8 +1117,10 @@ Tiling tile_rows(TrainArgs& p) {
   // as many row tiles as rows fill, and half a tile per expert
   auto about = [&](int side) { return (p.A / side + (touched + 1) / 2) * (int64_t)columns(side); };
   auto at_most = [&](int side) { return row_tiles_bound(p.A, p.E, side) * columns(side); };
-  if (about(kTile) >= kRowTiles256 && p.A > kRows256 * touched) return {kTile, grid_of(at_most(kTile))};
-  const int side = about(128) >= kRowTiles128 && p.A >= kRows128 * touched ? 128 : 64;
+  const bool two = in_two_parts(p);
+  if (!two && about(kTile) >= kRowTiles256 && p.A > kRows256 * touched)
+    return {kTile, grid_of(at_most(kTile))};
+  const int side = !two && about(128) >= kRowTiles128 && p.A >= kRows128 * touched ? 128 : 64;
   return {side, (unsigned)((at_most(side) + kXcds - 1) / kXcds * kXcds)};
 }
 
@@ -1086,7 +1131,7 @@ Tiling tile_weights(TrainArgs& p) {
     return (int64_t)p.E * p.mt * p.nnb;
   };
   const int64_t n = tiles(kTile);
-  if (n >= kWeightTiles256) {
+  if (n >= kWeightTiles256 && !in_two_parts(p)) {
     // an XCD's tiles come in whole groups, and a workgroup's list holds one of each group or, of
     // more than fit there, of some
     const int64_t groups = (n + kXcdCus - 1) / kXcdCus;
@@ -1104,8 +1149,9 @@ int launch_rows(TrainArgs p, hipStream_t s, const char* who) {
   auto launch = [&](auto gather) {
     constexpr bool G = decltype(gather)::value;
     if (t.side == kTile) train_gemm_kernel<KIND, false, G><<<t.grid, 64 * kNW, 0, s>>>(p, 0);
-    else if (t.side == 128) train_small_kernel<128, KIND, G><<<t.grid, 64 * kNW, 0, s>>>(p);
-    else train_small_kernel<64, KIND, G><<<t.grid, 64 * kNW, 0, s>>>(p);
+    else if (t.side == 128) train_small_kernel<128, KIND, G, false><<<t.grid, 64 * kNW, 0, s>>>(p);
+    else if (!in_two_parts(p)) train_small_kernel<64, KIND, G, false><<<t.grid, 64 * kNW, 0, s>>>(p);
+    else train_small_kernel<64, KIND, G, true><<<t.grid, 64 * kNW, 0, s>>>(p);
     return check_launch(who);
   };
   if constexpr (KIND == kGateUp)
@@ -1118,7 +1164,7 @@ struct Rest {
   SmallJob dx{}, w13{}, w2{};
 };
 
-int launch_rest(Rest& r, bool f32, int accumulate, hipStream_t s, const char* who) {
+int launch_rest(Rest& r, bool two, bool f32, int accumulate, hipStream_t s, const char* who) {
   bool any = false;
   auto large = [&](SmallJob& j, const Tiling& t) {
     j.side = t.side;
@@ -1152,9 +1198,12 @@ int launch_rest(Rest& r, bool f32, int accumulate, hipStream_t s, const char* wh
   }
   if (!any) return MOE_OK;
   return pick(r.w13.p.sorted_idx, [&](auto as_f32, auto gather) {
-    train_rest_kernel<decltype(as_f32)::value, decltype(gather)::value>
-        <<<r.dx.blocks + r.w13.blocks + r.w2.blocks, 64 * kNW, 0, s>>>(r.dx, r.w13, r.w2, accumulate);
-    return check_launch(who);
+    auto launch = [&](auto kernel) {
+      kernel<<<r.dx.blocks + r.w13.blocks + r.w2.blocks, 64 * kNW, 0, s>>>(r.dx, r.w13, r.w2, accumulate);
+      return check_launch(who);
+    };
+    constexpr bool F = decltype(as_f32)::value, G = decltype(gather)::value;
+    return two ? launch(train_rest_kernel<F, G, true>) : launch(train_rest_kernel<F, G, false>);
   });
 }
 
@@ -1198,10 +1247,11 @@ uint32_t dbg_take_train() { return dbg_take_unit(); }
 
 using namespace moe;
 
-// Workspace: h bf16 [T*k][I].
+// Workspace: h bf16 [T*k][I], and the second parts of a small batch's.
 extern "C" size_t moe_expert_ffn_train_workspace(const moe_experts* W, int32_t T, int32_t k) {
-  if (!W || T < 0 || k < 1) return 0;
-  return align256((size_t)T * k * W->I * 2);
+  if (!W || T < 0 || k < 1 || W->I < 1) return 0;
+  const size_t A = (size_t)T * k;
+  return align256(A * W->I * 2) + align256(two_part_rows(A, W->I) * W->I * 2);
 }
 
 extern "C" int moe_expert_ffn_train(const moe_experts* W, const uint16_t* x, int32_t T, int32_t k,
@@ -1224,19 +1274,23 @@ extern "C" int moe_expert_ffn_train(const moe_experts* W, const uint16_t* x, int
   p.a = reinterpret_cast<const uint8_t*>(x);
   p.K = W->H; p.N = W->I;
   p.out = ws; p.out2 = gate_up;
+  const int64_t rest = in_two_parts(p) ? (int64_t)align256((size_t)p.A * W->I * 2) : 0;
+  p.out_rest = rest;
   if (int st = launch_rows<kGateUp>(p, s, who)) return st;
   p.sorted_idx = nullptr;
   p.b = static_cast<const uint8_t*>(W->base) + Lo.w2;
   p.a = static_cast<const uint8_t*>(ws);
   p.K = W->I; p.N = W->H;
   p.out = y_perm; p.out2 = nullptr;
+  p.a_rest = rest; p.out_rest = 0;
   return launch_rows<kDown>(p, s, who);
 }
 
-// Workspace: h bf16 [T*k][I], (dg; du) bf16 [T*k][2I].
+// Workspace: h bf16 [T*k][I], (dg; du) bf16 [T*k][2I], and their second parts.
 extern "C" size_t moe_expert_ffn_backward_workspace(const moe_experts* W, int32_t T, int32_t k) {
-  if (!W || T < 0 || k < 1) return 0;
-  return align256((size_t)T * k * W->I * 2) + align256((size_t)T * k * W->I * 4);
+  if (!W || T < 0 || k < 1 || W->I < 1) return 0;
+  const size_t A = (size_t)T * k, two = two_part_rows(A, W->I);
+  return align256(A * W->I * 2) + align256(A * W->I * 4) + align256(two * W->I * 2) + align256(two * W->I * 4);
 }
 
 extern "C" int moe_expert_ffn_backward(const moe_experts* W, const uint16_t* x, int32_t T, int32_t k,
@@ -1282,15 +1336,24 @@ extern "C" int moe_expert_ffn_backward(const moe_experts* W, const uint16_t* x, 
   p.a = reinterpret_cast<const uint8_t*>(d_y_perm);
   p.K = H; p.N = I;
   p.out = h; p.out2 = dgu; p.gu = gate_up;
+  const bool two = in_two_parts(p);
+  if (two) {  // the parts lie h, (dg; du), h's rest, (dg; du)'s rest
+    const size_t hb = align256((size_t)A * I * 2), gb = align256((size_t)A * I * 4);
+    p.out_rest = (int64_t)(hb + gb);
+    p.out2_rest = (int64_t)(gb + hb);
+  }
+  const int64_t h_rest = p.out_rest, dgu_rest = p.out2_rest;
   if (int st = launch_rows<kDh>(p, s, who)) return st;
   Rest rest;
   p.out2 = nullptr; p.gu = nullptr;
+  p.out_rest = p.out2_rest = 0;
   if (d_x_perm) {
     TrainArgs& q = rest.dx.p = p;
     q.b = static_cast<const uint8_t*>(W->base) + Lo.w13;
     q.a = reinterpret_cast<const uint8_t*>(dgu);
     q.K = 2 * I; q.N = H;
     q.out = d_x_perm;
+    q.a_rest = dgu_rest;
   }
   if (d_w13) {
     TrainArgs& q = rest.w13.p = p;
@@ -1298,12 +1361,14 @@ extern "C" int moe_expert_ffn_backward(const moe_experts* W, const uint16_t* x, 
     q.a = reinterpret_cast<const uint8_t*>(dgu);
     q.b = reinterpret_cast<const uint8_t*>(x);
     q.M = 2 * I; q.N = H; q.out = d_w13;
+    q.a_rest = dgu_rest;
   }
   if (d_w2) {
     TrainArgs& q = rest.w2.p = p;
     q.a = reinterpret_cast<const uint8_t*>(d_y_perm);
     q.b = reinterpret_cast<const uint8_t*>(h);
     q.M = H; q.N = I; q.out = d_w2;
+    q.b_rest = h_rest;
   }
-  return launch_rest(rest, d_w_type == MOE_T_F32, accumulate, s, who);
+  return launch_rest(rest, two, d_w_type == MOE_T_F32, accumulate, s, who);
 }

@@ -16,6 +16,8 @@ These bounds add every rounding's worst case; besides, the 2-norm of the whole e
 to what independent roundings give: each is at most b relative and uniform over its step, so
 b / sqrt(3) of the result's norm, two of them in a row (operand and result) sqrt(2) of that; 1.5
 times that is allowed for outputs of a thousand elements and more.
+Batches of at most 96 rows and 32768 values of h keep h, dg and du in two parts: the first cut to bf16, what is left
+below 2^-7 of it rounded to bf16, so 2^-15 stands for their b above (and one rounding less).
 """
 from __future__ import annotations
 
@@ -96,8 +98,15 @@ def close(got, want, tol, what, roundings=2):
         assert rel <= 1.5 * math.sqrt(roundings) * B / math.sqrt(3), (what, rel)
 
 
-def check_forward(c, gu, y):
+def two_parts(rows, I):
+    return rows <= 96 and rows * I <= 32768
+
+
+def check_forward(c, gu, y, rows=None):
+    """rows: of the batch, where they are more than the case's."""
     I, H = c.I, c.H
+    few = two_parts(rows or c.A, I)
+    hb, roundings = (2.0 ** -15, 1) if few else (B, 2)
     for e in range(c.E):
         p = slice(c.ends[e], c.ends[e + 1])
         if p.start == p.stop:
@@ -109,16 +118,18 @@ def check_forward(c, gu, y):
         g, u = z[:, :I], z[:, I:]
         sg = torch.sigmoid(g) * g
         h = sg * u
-        eh = 1.1 * u.abs() * ez[:, :I] + sg.abs() * ez[:, I:] + ((g.abs() + 8) * 2.0 ** -22 + B) * h.abs()
+        eh = 1.1 * u.abs() * ez[:, :I] + sg.abs() * ez[:, I:] + ((g.abs() + 8) * 2.0 ** -22 + hb) * h.abs()
         eh = eh + 2.0 ** -126 * (g * u).abs()
         want = h @ w2.t()
         tol = eh @ w2.abs().t() + 2 * I * U * (h.abs() @ w2.abs().t()) + B * want.abs()
-        close(y[p], want, tol, f"y {e}")
+        close(y[p], want, tol, f"y {e}", roundings)
     assert bool((gu[c.n:] == MARK).all()) and bool((y[c.n:] == MARK).all())
 
 
-def check_backward(c, dx, d13, d2, base=0.0):
+def check_backward(c, dx, d13, d2, base=0.0, rows=None):
     I, H = c.I, c.H
+    few = two_parts(rows or c.A, I)
+    hb, roundings = (2.0 ** -15, 1) if few else (B, 2)
     f32 = d13.dtype is F32
     r = 0.0 if f32 else B
     for e in range(c.E):
@@ -132,20 +143,20 @@ def check_backward(c, dx, d13, d2, base=0.0):
         du, dg, h = dh * sg, dh * u * d, sg * u
         k22 = (g.abs() + 8) * 2.0 ** -22
         tiny = 2.0 ** -126 * (1 + g.abs()) * (1 + u.abs()) * (1 + dh.abs())
-        edu = sg.abs() * edh + (k22 + B) * du.abs() + tiny
-        edg = (u * d).abs() * edh + k22 * (dh * u).abs() * s * (1 + 2 * g.abs()) + B * dg.abs() + tiny
-        eh = (k22 + B) * h.abs() + tiny
+        edu = sg.abs() * edh + (k22 + hb) * du.abs() + tiny
+        edg = (u * d).abs() * edh + k22 * (dh * u).abs() * s * (1 + 2 * g.abs()) + hb * dg.abs() + tiny
+        eh = (k22 + hb) * h.abs() + tiny
         dz, edz = torch.cat([dg, du], 1), torch.cat([edg, edu], 1)
         if n:
             want = dz @ w13
             tol = edz @ w13.abs() + 4 * I * U * (dz.abs() @ w13.abs()) + B * want.abs()
-            close(dx[p], want, tol, f"dx {e}")
+            close(dx[p], want, tol, f"dx {e}", roundings)
         want = dz.t() @ x
         tol = edz.t() @ x.abs() + 2 * (n + 1) * U * (dz.abs().t() @ x.abs() + abs(base)) + r * want.abs()
-        close(d13[e] - base, want, tol, f"d_w13 {e}")
+        close(d13[e] - base, want, tol, f"d_w13 {e}", roundings)
         want = dy.t() @ h
         tol = dy.abs().t() @ eh + 2 * (n + 1) * U * (dy.abs().t() @ h.abs() + abs(base)) + r * want.abs()
-        close(d2[e] - base, want, tol, f"d_w2 {e}")
+        close(d2[e] - base, want, tol, f"d_w2 {e}", roundings)
         if n == 0:
             assert bool((d13[e] == base).all()) and bool((d2[e] == base).all())
     assert bool((dx[c.n:] == MARK).all())
@@ -179,6 +190,19 @@ CASES = [
     dict(counts=[40, 0, 17, 64, 63, 100] * 10, H=1024, I=640, k=3),
     dict(counts=[179, 128, 64, 300, 0, 1, 127, 400, 250, 65, 200, 129, 500], H=1024, I=384, k=3, behind=1),
     dict(counts=[179, 128, 64, 300, 0, 1, 127, 400, 250], H=640, I=640, gathered=False),
+]
+CASES += [
+    dict(counts=[96], H=256, I=256),
+    dict(counts=[97], H=256, I=256),
+    dict(counts=[2, 83], H=256, I=384),
+    dict(counts=[86], H=256, I=384, gathered=False),
+    dict(counts=[129], H=256, I=384),
+    dict(counts=[0, 20, 12, 0], H=1024, I=1024, k=2),
+    dict(counts=[1], H=1152, I=16384),
+    dict(counts=[1, 0, 2], H=512, I=1024, gathered=False),
+    dict(counts=[65, 0, 31], H=128, I=128),
+    dict(counts=[3, 0, 1, 0] * 8, H=2048, I=1024, k=4),
+    dict(counts=[60, 4, 0, 32], H=4096, I=512, gathered=False),
 ]
 IDS = [f"{len(c['counts'])}e{sum(c['counts'])}r{c['H']}x{c['I']}" for c in CASES]
 
@@ -446,12 +470,12 @@ def test_offsets_past_32_bits(gathered):
     moe.moe_expert_ffn_train(c.W, x, A, 1, c.counts, c.offsets, order, gu, y, ws)
     torch.cuda.synchronize()
     assert bool((gu[:first:1000] == MARK).all()) and bool((y[:first] == MARK).all())
-    check_forward(c, gu[first:], y[first:])
+    check_forward(c, gu[first:], y[first:], A)
     gu[first:] = c.gu
     moe.moe_expert_ffn_backward(c.W, x, A, 1, c.counts, c.offsets, order, gu, dy, ws, dx, d13, d2)
     torch.cuda.synchronize()
     assert bool((dx[:first] == MARK).all())
-    check_backward(c, dx[first:], d13, d2)
+    check_backward(c, dx[first:], d13, d2, rows=A)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -506,3 +530,40 @@ def test_two_graphs_share_a_workspace():
             for got, w in zip(outs[i], want[i]):
                 n = c.n if got.shape[0] == c.A else len(got)
                 assert torch.equal(got[:n], w[:n])
+
+
+def test_smaller_batches_in_a_larger_ones_workspace():
+    """A workspace for 97 rows holds what any batch of fewer needs (their parts are two)."""
+    for E, H, I, k in ((3, 128, 128, 1), (2, 256, 384, 3)):
+        W = moe.experts("bf16", E, H, I, torch.empty(E * 3 * H * I, dtype=BF, device=DEV), 6 * H * I)
+        for f in (moe.moe_expert_ffn_train_workspace, moe.moe_expert_ffn_backward_workspace):
+            sizes = [f(W, T, k) for T in range(1, 300)]
+            assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("n", [9, 200])
+def test_infinities_stay_infinite(n):
+    """An infinite weight or row against values that bf16 holds exactly (whose second part is nothing)
+    and ones that it does not: infinite results, not NaN."""
+    H = I = 128
+    c = Case([n], H, I, gathered=False, seed=21)
+    c.gu[:] = torch.randn(n, 2 * I, device=DEV).to(BF)
+    c.gu[:, :I] = 300.0                 # silu(g) = g: h = 300 u, exact and not
+    c.gu[0, I:] = 2.0
+    c.dy.abs_()
+    rec = c.rec.clone()
+    w13, w2 = rec[0, :2 * I * H].view(2 * I, H), rec[0, 2 * I * H:].view(H, I)
+    w2[:] = 0.25
+    w13[I:] = 0.0
+    w13[I + 5, 7] = float("inf")        # dx[:, 7] = du[:, 5] inf + finite ones, du > 0
+    W = moe.experts("bf16", 1, H, I, rec, rec.shape[1] * 2)
+    dx, d13, d2 = c.new(n, H), c.new(1, 2 * I, H), c.new(1, H, I)
+    c.gu[:, I:].abs_()
+    c.gu[:, I + 9] = float("inf")       # h[:, 9] = inf: d_w2[:, 9]
+    moe.moe_expert_ffn_backward(W, c.x, n, 1, c.counts, c.offsets, None, c.gu, c.dy, c.ws, dx, d13, d2)
+    assert bool((d2[0, :, 9] == float("inf")).all())
+    assert not bool(d2[0, :, :9].isinf().any()) and not bool(d2[0, :, :9].isnan().any())
+    c.gu[:, I + 9] = 1.0
+    moe.moe_expert_ffn_backward(W, c.x, n, 1, c.counts, c.offsets, None, c.gu, c.dy, c.ws, dx, d13, d2)
+    assert bool((dx[:, 7] == float("inf")).all())
+    assert bool(dx[:, :7].isfinite().all()) and bool(dx[:, 8:].isfinite().all())
