@@ -193,8 +193,11 @@ def test_clip_refuses(kw, status):
 def test_workspace_queries():
     W = _experts()
     up = lambda v: -(-v // 256) * 256  # noqa: E731
-    assert m.moe_expert_ffn_train_workspace(W, 7, 2) == up(14 * 128 * 2)
-    assert m.moe_expert_ffn_backward_workspace(W, 7, 2) == up(14 * 128 * 2) + up(14 * 256 * 2)
+    for T, two in ((7, 14), (48, 96), (700, 96)):  # rows that are held in two parts, or may be in a smaller batch
+        A = 2 * T
+        h, dgu = up(A * 128 * 2) + up(two * 128 * 2), up(A * 256 * 2) + up(two * 256 * 2)
+        assert m.moe_expert_ffn_train_workspace(W, T, 2) == h
+        assert m.moe_expert_ffn_backward_workspace(W, T, 2) == h + dgu
     assert m.moe_expert_ffn_train_workspace(W, -1, 2) == 0
     assert m.moe_clip_grad_norm_workspace(1) >= 8 and m.moe_clip_grad_norm_workspace(-1) == 0
     assert m.moe_clip_grad_norm_workspace(1 << 16) >= m.moe_clip_grad_norm_workspace(129)
