@@ -51,7 +51,7 @@ class Rows:
 
 
 # k covers every register count; H: one lane, less than, just and more than one wave's and one
-# workgroup's columns; T on both sides of the split over a workgroup's waves
+# workgroup's columns, on both sides of the split over a workgroup's waves
 CASES = [(1, 1, 8, 0, 0), (1, 16, 2048, 0, 0), (3, 2, 40, 2, 5), (64, 2, 256, 0, 0), (333, 4, 2048, 9, 0),
          (17, 3, 520, 4, 1), (9, 9, 4104, 11, 2), (40, 8, 7168, 0, 0), (4099, 2, 512, 20, 3),
          (4097, 5, 72, 0, 0), (4200, 8, 1032, 31, 0), (5000, 16, 24, 7, 7)]
@@ -122,12 +122,12 @@ def test_gather(T, k, H, drop, spare, weighted):
     assert torch.equal(own, out)
 
 
-@pytest.mark.parametrize("k,H", [(8, 4096), (2, 16384), (16, 2048)])
-def test_rows_of_more_than_the_caches_hold(k, H):
+@pytest.mark.parametrize("k,H,T", [(8, 4096, 4300), (2, 16384, 4300), (16, 2048, 4300), (4, 1032, 33000),
+                                   (8, 512, 33000), (4, 256, 132000), (2, 504, 134000), (16, 136, 62000)])
+def test_rows_of_more_than_the_caches_hold(k, H, T):
     """Batches that pass the caches by: the same results as in two halves, which do not (each token's
     are its own), and as in 64 bits."""
-    T = 4300
-    flush(f"[rows] large k={k} H={H}")
+    flush(f"[rows] large k={k} H={H} T={T}")
     g = torch.Generator(device=DEV).manual_seed(k)
     rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
     A = T * k
