@@ -765,7 +765,16 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
     dbg_segment(row0, rows, p.A);
     rows = __builtin_amdgcn_readfirstlane(max(rows, 0));
     row0 = __builtin_amdgcn_readfirstlane(row0);
-    if (rows == 0 && accumulate) return;
+    // without rows: zeros (8 tokens over 22 experts of 2304 x 640: 76 us, through the MFMAs 84).  M and N
+    // are multiples of 128, so the tile is whole.
+    if (rows == 0) {
+      if (accumulate) return;
+      constexpr int kUnits = S * (F32 ? 4 : 2) / 16;  // 16 bytes each, of a row
+      uint8_t* out = static_cast<uint8_t*>(p.out) + (((size_t)e * p.M + mb * S) * p.N + nb * S) * (F32 ? 4 : 2);
+      for (int i = tid; i < S * kUnits; i += 64 * kNW)
+        *reinterpret_cast<uint4*>(out + (size_t)(i / kUnits) * p.N * (F32 ? 4 : 2) + i % kUnits * 16) = uint4{0, 0, 0, 0};
+      return;
+    }
   } else {
     RowTiles<kSmall> t;
     const int mt = t.load(p.counts, p.offsets, p.E, lane);
@@ -1026,7 +1035,8 @@ __global__ __launch_bounds__(64 * kNW, 2) void train_small_kernel(TrainArgs p) {
 
 // The gradient's three products behind dh - dx, dW13, dWd - do not depend on each other: what
 // takes small tiles of them runs as one launch, so that they fill the chip together (777 tokens
-// over 13 experts of 1024 x 384: 45 us one after another, 33 in one).
+// over 13 experts of 1024 x 384: 45 us one after another, 33 in one; with dx, whose tiles have most
+// blocks, last in the launch: 36).
 struct SmallJob {
   TrainArgs p;
   unsigned blocks;  // 0: not in this launch
@@ -1042,7 +1052,7 @@ __global__ __launch_bounds__(64 * kNW, 2) void train_rest_kernel(SmallJob dx, Sm
     SmallLds<128> s128;
   } lds;
   unsigned b = blockIdx.x;
-  if (b < dx.blocks) {  // first, its XCDs being the launch's
+  if (b < dx.blocks) {
     if (TWO || dx.side == 64) small_tile<64, kDx, false, false, TWO>(dx.p, 0, b, lds.s64);
     else small_tile<128, kDx, false, false, TWO>(dx.p, 0, b, lds.s128);
     return;
@@ -1093,7 +1103,7 @@ constexpr int64_t kRows256 = 64, kRows128 = 16;
 // of them a handful carries a result's norm, and how their rounding falls shows in it (up to 1.8 times the
 // error of a result rounded once, with two parts 1.0; larger batches: 1.4).  us, one part / two:
 // forward and gradient of 3 tokens over 2 experts of 256 x 512 11.0 12.7 / 13.1 17.2, of 8 over 22 of
-// 2304 x 640 23 95 / 26 84 (in the smaller tiles that two parts take).
+// 2304 x 640 23 95 / 26 76 (in the smaller tiles that two parts take).
 constexpr int kTwoRows = 96, kTwoValues = 32768;
 
 // Rows of a workspace for A rows that have second parts (smaller batches may run in it).
