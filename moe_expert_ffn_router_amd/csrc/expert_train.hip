@@ -719,7 +719,7 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
 // share a compute unit, with four stages of 16 KB or two of 32 KB each; a block is read for a
 // quarter or half of the MFMAs that the large tiles make of it, so latency and the LDS bound them.
 //   Measured: FFN of 64 tokens over 2 of 8 experts of 256 x 128 6.6 + 4.4 us; gradient of 777 tokens
-// over 3 of 13 of 1024 x 384 13.6 us (dh) + 33 (the rest), 76 MB and 11 GFLOP: 16 us at a copy's rate.
+// over 3 of 13 of 1024 x 384 13.3 us (dh) + 32 (the rest), 76 MB and 11 GFLOP: 16 us at a copy's rate.
 // ---------------------------------------------------------------------------
 constexpr int kIds = 16;  // blocks of gathered rows in LDS
 
@@ -969,6 +969,27 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
     *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(d) + rest) =
         uint2{bf16_pack2(lo[0], lo[1]), bf16_pack2(lo[2], lo[3])};
   };
+  // bf16 rows of 64 columns at 16 bytes a lane (8 bytes of 32 columns, as below: the gradient of 777 tokens
+  // over 13 experts of 1024 x 384 43.9 instead of 42.2 us)
+  if constexpr (SUB == 2 && !F32 && (W || KIND == kDown || KIND == kDx)) {
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) {
+#pragma unroll
+      for (int j = 0; j < SUB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) epi_put8(ep, lane, j * 4 + q, pack4(acc[i][j], q));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint4 v = epi_get(ep, lane, t);
+        const int lr = row_at(i) + er + 8 * t, col = col_at(0) + eu * 8;
+        if (W ? mb * kSmall + lr >= p.M : lr >= rows) continue;
+        if (col >= p.N) continue;
+        const size_t row = W ? (size_t)e * p.M + mb * kSmall + lr : (size_t)(row0 + lr);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.N + col) = v;
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < SUB; ++i)
 #pragma unroll
@@ -1103,7 +1124,7 @@ constexpr int64_t kRows256 = 64, kRows128 = 16;
 // of them a handful carries a result's norm, and how their rounding falls shows in it (up to 1.8 times the
 // error of a result rounded once, with two parts 1.0; larger batches: 1.4).  us, one part / two:
 // forward and gradient of 3 tokens over 2 experts of 256 x 512 11.0 12.7 / 13.1 17.2, of 8 over 22 of
-// 2304 x 640 23 95 / 26 76 (in the smaller tiles that two parts take).
+// 2304 x 640 23 95 / 26 73 (in the smaller tiles that two parts take).
 constexpr int kTwoRows = 96, kTwoValues = 32768;
 
 // Rows of a workspace for A rows that have second parts (smaller batches may run in it).
