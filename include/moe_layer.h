@@ -385,7 +385,8 @@ int moe_combine_backward(const uint16_t* d_y, const uint16_t* y_perm, const int3
  * Rows in no expert's segment are left as they were, in gate_up and y_perm.
  *   x           device bf16 [T][H]; row p is x[sorted_idx[p] / k]
  *   sorted_idx  device int32 [T*k], or NULL: x is device bf16 [T*k][H], its
- *               rows in expert order already (as moe_dispatch leaves them)
+ *               rows in expert order already (as moe_dispatch leaves them);
+ *               entries in no expert's segment may hold anything
  *   counts, offsets  device int32 [E], [E+1]; disjoint segments within [0, T*k)
  *   gate_up     device bf16 [T*k][2I] (out);  y_perm  device bf16 [T*k][H] (out)
  * Other formats return MOE_ERR_UNSUPPORTED, as does T*H >= 2^31 with

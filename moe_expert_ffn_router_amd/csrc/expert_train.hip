@@ -322,17 +322,21 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
   const size_t astep = W ? (size_t)kBK * p.M * 2 : (size_t)kBK * 2;
   const size_t bstep = GATHER && W ? 0 : BT ? (size_t)kBK * p.N * 2 : (size_t)kBK * 2;
   // Gathered rows of a block of weights come by the ring lds.src, two blocks ahead of the copies:
-  // cursor of the block whose rows are next, tile sr, first of its rows sp of sn.
+  // cursor of the block whose rows are next, tile sr, first of its rows sp of sn.  An expert without
+  // rows owns no entry of the index, and its offset may name one that holds anything: token 0.
   int sr = 0, sp = 0, sn = 0, srow = 0, sq = 0;
   auto issue_ring = [&]() {
     if (wave == 0) {
       if (sp == 0) {
-        srow = min(max(entry(sr, 1), 0), p.A - 1);  // an expert without rows may start at A
-        sn = max(entry(sr, 2), 1);
+        srow = entry(sr, 1);
+        sn = entry(sr, 2);
       }
-      // rows past the segment: its last one
-      dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + srow + sp), (uint32_t)min(lane, sn - 1 - sp) * 4u,
-           lds.src[sq & 3]);
+      if (sn > 0) {  // rows past the segment: its last one
+        dma4(reinterpret_cast<const uint8_t*>(p.sorted_idx + srow + sp), (uint32_t)min(lane, sn - 1 - sp) * 4u,
+             lds.src[sq & 3]);
+      } else {
+        lds.src[sq & 3][lane] = 0;
+      }
       ++sq;
       if (sp + kBK < sn) {
         sp += kBK;
