@@ -149,18 +149,33 @@ __global__ __launch_bounds__(256) void rows_kernel(RowArgs p) {
   }
 }
 
+// A grid has fewer than 2^32 threads: a batch goes in slices of 2^23 workgroups (of one token each or four).
 template <bool GATHER, bool DOT, int KM>
-int launch_k(const RowArgs& p, hipStream_t s, const char* who) {
+int launch_k(RowArgs p, hipStream_t s, const char* who) {
   const bool nt = (int64_t)p.T * p.k * p.H * 2 >= kMemorySideCache;
-  if (p.H > 512) {
-    if (nt) rows_kernel<GATHER, DOT, KM, 4, true><<<(unsigned)p.T, 256, 0, s>>>(p);
-    else rows_kernel<GATHER, DOT, KM, 4, false><<<(unsigned)p.T, 256, 0, s>>>(p);
-  } else {
-    const unsigned quads = (unsigned)((p.T + 3) / 4);
-    if (nt) rows_kernel<GATHER, DOT, KM, 1, true><<<quads, 256, 0, s>>>(p);
-    else rows_kernel<GATHER, DOT, KM, 1, false><<<quads, 256, 0, s>>>(p);
+  const int per = p.H > 512 ? 1 : 4;
+  for (int left = p.T;;) {
+    p.T = left < per << 23 ? left : per << 23;
+    const unsigned grid = (unsigned)((p.T + per - 1) / per);
+    auto launch = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(p); };
+    if (per == 1) launch(nt ? rows_kernel<GATHER, DOT, KM, 4, true> : rows_kernel<GATHER, DOT, KM, 4, false>);
+    else launch(nt ? rows_kernel<GATHER, DOT, KM, 1, true> : rows_kernel<GATHER, DOT, KM, 1, false>);
+    if (int st = check_launch(who)) return st;
+    left -= p.T;
+    if (left == 0) return MOE_OK;
+    // what goes by token; the rows in expert order are the whole batch's
+    const size_t a = (size_t)p.T * p.k, rows = (size_t)p.T * p.H;
+    p.inv += a;
+    if (p.w) p.w += a;
+    if (p.dot) p.dot += a;
+    if (GATHER) {
+      p.out += rows;
+      if (p.add) p.add += rows;
+      if (p.other) p.other += rows;
+    } else {
+      p.src += rows;
+    }
   }
-  return check_launch(who);
 }
 
 template <bool GATHER, bool DOT>
