@@ -574,9 +574,11 @@ def _stream_on(stream, dev) -> int | None:
 
 
 def _matrix(t, name: str) -> tuple[int, int]:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a matrix")
     try:
         rows, cols = t.shape
-    except (AttributeError, ValueError):
+    except ValueError:
         raise ValueError(f"{name}: expected a matrix") from None
     return rows, cols
 
