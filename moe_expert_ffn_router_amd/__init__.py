@@ -580,6 +580,8 @@ def _matrix(t, name: str) -> tuple[int, int]:
         rows, cols = t.shape
     except ValueError:
         raise ValueError(f"{name}: expected a matrix") from None
+    if rows >> 31 or cols >> 31:   # ctypes would cut them
+        raise ValueError(f"{name}: {rows} x {cols}, sizes are of 32 bits")
     return rows, cols
 
 
