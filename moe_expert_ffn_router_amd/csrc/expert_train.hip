@@ -1339,7 +1339,7 @@ extern "C" int moe_expert_ffn_backward(const moe_experts* W, const uint16_t* x, 
   if (int st = check_train(who, W, T, k, sorted_idx != nullptr, &Lo)) return st;
   if (d_w_type != MOE_T_BF16 && d_w_type != MOE_T_F32)
     return set_error(MOE_ERR_UNSUPPORTED, "%s: weight gradients of type %d (bf16 or fp32)", who, d_w_type);
-  if (accumulate && d_w_type != MOE_T_F32)
+  if (accumulate && (d_w13 || d_w2) && d_w_type != MOE_T_F32)
     return set_error(MOE_ERR_UNSUPPORTED, "%s: only fp32 weight gradients accumulate", who);
   if ((d_w13 && !aligned16(d_w13)) || (d_w2 && !aligned16(d_w2)))
     return set_error(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", who);
