@@ -194,6 +194,8 @@ class MoELayer:
         shared expert's record."""
         T = logits.shape[0]
         assert T <= self.T_max and x.shape == (T, self.H)
+        if Ws is not None and not self.shared_I:
+            raise ValueError("forward_train: Ws given, but the layer was made without a shared expert")
         b = self._train_buffers(stream)
         self.route_permute(logits, stream)
         if T == 0:
