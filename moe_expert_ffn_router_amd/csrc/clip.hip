@@ -15,7 +15,8 @@
 //   Gradients of more bytes than the memory-side cache holds bypass it in both passes (NT): 1.6 GB
 // clipped into other tensors 921 -> 850 us, 5.8 TB/s over the three times it moves them; bypassing
 // the cache with the loads or the stores alone 925 and 893.  Fewer are in the cache for the
-// second pass.
+// second pass.  Outputs that lie otherwise in their 16 bytes than their gradients are written element by
+// element (1.6 GB of bf16: 2407 us instead of 823).
 #include <algorithm>
 #include <new>
 #include <utility>

@@ -9,7 +9,10 @@
 //   weights  out[e][m][n] = sum_(p of e) A[p][m] B[p][n]: both operands K strided.
 // Roundings: h and (dg; du) go to bf16 once, as the operands of the next product (small batches: to
 // two bf16 parts); the forward's h comes from the fp32 gate and up sums, the gradient's from the kept
-// bf16 ones.
+// bf16 ones.  Why: the bf16 MFMA takes them, and a rounded operand is off by as much as the result's own
+// rounding, so a result is off by 0.0023 to 0.0024 of its norm instead of 0.0017; two parts for all batches
+// would leave 0.0017 but take 1.33 times the operations of the forward and 1.83 times the gradient's,
+// which the MFMAs bound.
 //
 // Tiles of 256 x 256 outputs on 4 waves, one per SIMD, 128 x 128 outputs each (all of a wave's
 // 256 accumulation registers): a K step of 16 then reads 8 KB of operands per wave from LDS for 16
@@ -26,11 +29,13 @@
 // per block).
 //   A workgroup owns its compute unit and works through a list of tiles as one sequence of blocks:
 // the next tile's first blocks are copied under the current one's last and its epilogue.
-//   Measured, 16384 tokens over 8 of 64 experts of 4096 x 1024: dh 1147 us (0.96 PFLOP/s, its
-// epilogue moves 655 KB a tile), dx 2030 (1.08), dW13 2140 (1.03), dWd 957 (1.15); library products
-// of these layouts reach 1.06 to 1.23.  The card is at its power limit (1.6 to 1.75 GHz); a block takes
-// 2630 clocks (weights: 2880), 2048 of them MFMAs, 2200 without its copies.  4096 tokens over 8 of 64
-// of 2048 x 1024: gate/up 300 to 350 us, down 157 to 180, a quarter of it rows past the experts' last.
+//   Measured (averages of a kernel trace), 16384 tokens over 8 of 64 experts of 4096 x 1024: dh 1155 us
+// (0.95 PFLOP/s, its epilogue moves 655 KB a tile), dx 2021 (1.09), dW13 2199 (1.00), dWd 958 (1.15);
+// library products of these layouts reach 1.06 to 1.23.  A block takes 2630 clocks (weights: 2880), 2048 of
+// them MFMAs, 2200 without its copies, at 1.6 to 1.75 GHz (the power limit).  4096 tokens over 8 of 64 of
+// 2048 x 1024: gate/up 380 us, down 196, a quarter of it rows past the experts' last, the MFMAs busy for
+// 63 and 61 % of the clocks; library products of as many MFMAs, both operands K-contiguous like these,
+// take 251 and 135 us (78 and 67 %; 92 % at 8192^3), so it is the loop and not the power limit that is short.
 #include <type_traits>
 
 #include "fp8_common.h"
@@ -722,8 +727,9 @@ __global__ __launch_bounds__(64 * kNW, 1) void train_gemm_kernel(TrainArgs p, in
 // most compute units idle and run through their K blocks one after another.  Two workgroups
 // share a compute unit, with four stages of 16 KB or two of 32 KB each; a block is read for a
 // quarter or half of the MFMAs that the large tiles make of it, so latency and the LDS bound them.
-//   Measured: FFN of 64 tokens over 2 of 8 experts of 256 x 128 6.6 + 4.4 us; gradient of 777 tokens
-// over 3 of 13 of 1024 x 384 13.3 us (dh) + 32 (the rest), 76 MB and 11 GFLOP: 16 us at a copy's rate.
+//   Measured (averages of a kernel trace): FFN of 64 tokens over 2 of 8 experts of 256 x 128 6.9 + 4.3 us;
+// gradient of 777 tokens over 3 of 13 of 1024 x 384 13.9 us (dh) + 32.6 (the rest), 76 MB and 11 GFLOP: 16 us
+// at a copy's rate.  (Without the trace a call takes 41 to 45 us, back to back.)
 // ---------------------------------------------------------------------------
 constexpr int kIds = 16;  // blocks of gathered rows in LDS
 
@@ -769,7 +775,8 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
     dbg_segment(row0, rows, p.A);
     rows = __builtin_amdgcn_readfirstlane(max(rows, 0));
     row0 = __builtin_amdgcn_readfirstlane(row0);
-    // without rows: zeros (8 tokens over 22 experts of 2304 x 640: 76 us, through the MFMAs 84).  M and N
+    // without rows: zeros (gradient of 8 tokens over 22 experts of 2304 x 640, k = 1: 65.0 us a call, with the
+    // epilogue of a tile of zeros 67.6).  M and N
     // are multiples of 128, so the tile is whole.
     if (rows == 0) {
       if (accumulate) return;
@@ -799,7 +806,7 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
   const int nblk = TWO && KIND != kGateUp && KIND != kDh ? 2 * nk : nk;
   auto k_block = [&](int c) { return TWO && c >= nk ? c - nk : c; };
 
-  // this wave's pieces: 2 of a and 2 of b
+  // this wave's pieces: kSmallCopies of a and of b
   const uint8_t *asrc, *bsrc;
   uint32_t ao[kSmallCopies], bo[kSmallCopies];
   int ak[kSmallCopies], bk[kSmallCopies];  // weights: K of the lane's part
@@ -973,8 +980,8 @@ __device__ __forceinline__ void small_tile(const TrainArgs& p, int accumulate, u
     *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(d) + rest) =
         uint2{bf16_pack2(lo[0], lo[1]), bf16_pack2(lo[2], lo[3])};
   };
-  // bf16 rows of 64 columns at 16 bytes a lane (8 bytes of 32 columns, as below: the gradient of 777 tokens
-  // over 13 experts of 1024 x 384 43.9 instead of 42.2 us)
+  // bf16 rows of 64 columns at 16 bytes a lane (8 bytes of 32 columns, as below: a call for the gradient of 777
+  // tokens, 3 of 13 experts of 1024 x 384, 46.7 instead of 44.9 us)
   if constexpr (SUB == 2 && !F32 && (W || KIND == kDown || KIND == kDx)) {
 #pragma unroll
     for (int i = 0; i < SUB; ++i) {
@@ -1124,11 +1131,16 @@ constexpr int64_t kRowTiles256 = 128, kRowTiles128 = 300, kWeightTiles256 = 200,
 // 2048 x 512: 118 / 135 / 150).
 constexpr int64_t kRows256 = 64, kRows128 = 16;
 
-// Small batches keep h, dg and du in two bf16 parts, up to this many rows and values of h: with few
-// of them a handful carries a result's norm, and how their rounding falls shows in it (up to 1.8 times the
-// error of a result rounded once, with two parts 1.0; larger batches: 1.4).  us, one part / two:
-// forward and gradient of 3 tokens over 2 experts of 256 x 512 11.0 12.7 / 13.1 17.2, of 8 over 22 of
-// 2304 x 640 23 95 / 26 73 (in the smaller tiles that two parts take).
+// Small batches keep h, dg and du in two bf16 parts, up to this many rows and values of h: with few of them
+// a handful carries a result's norm, and how their rounding falls shows in it.  Worst error of 24 batches
+// each, over layers of 256 to 4096 x 128 to 1024, in errors of a result rounded once, one part / two: 4 rows
+// 1.78 / 1.10, 16 rows 1.68, 32 rows 1.58, 48 rows 1.53, 64 to 96 rows 1.51, 112 and 128 rows 1.52, more 1.49; by
+// values of h up to 8192 1.68, up to 16384 1.53, up to 32768 1.51, more 1.49 (1.42 in the mean at any size;
+// two parts never above 1.05 from 16 rows on).  So the border stands where the worst batch comes down
+// to within a tenth of the mean.  What two parts cost, the same layers: the forward 1.03 to 1.35 times,
+// the gradient 0.87 to 1.6 times (below 1 where one part takes larger tiles).  us a call, one part / two:
+// forward and gradient of 3 tokens over 2 experts of 256 x 512 11.9 14.2 / 13.0 18.1, of 8 over 22 of
+// 2304 x 640 19.2 87 / 21.5 65.
 constexpr int kTwoRows = 96, kTwoValues = 32768;
 
 // Rows of a workspace for A rows that have second parts (smaller batches may run in it).
