@@ -187,6 +187,14 @@ class MoELayer:
             self.train = b
         return self.train
 
+    def _check_step(self, logits: torch.Tensor, W: Experts) -> None:
+        """The library takes the sizes of what it is given; the buffers are of the layer's."""
+        if logits.dim() != 2 or logits.shape[1] != self.E:
+            raise ValueError(f"logits: {tuple(logits.shape)}, expected [T][{self.E}]")
+        if (W.E, W.H, W.I) != (self.E, self.H, self.I):
+            raise ValueError(f"W: {W.E} experts of {W.H} x {W.I}, the layer has {self.E} experts of "
+                             f"{self.H} x {self.I}")
+
     def forward_train(self, logits: torch.Tensor, x: torch.Tensor, W: Experts,
                       Ws: Experts | None = None, stream=None) -> torch.Tensor:
         """The layer's forward over BF16 records, keeping what `backward` needs until the next
@@ -196,6 +204,7 @@ class MoELayer:
         assert T <= self.T_max and x.shape == (T, self.H)
         if Ws is not None and not self.shared_I:
             raise ValueError("forward_train: Ws given, but the layer was made without a shared expert")
+        self._check_step(logits, W)
         b = self._train_buffers(stream)
         self.route_permute(logits, stream)
         if T == 0:
@@ -221,6 +230,7 @@ class MoELayer:
         the weights' gradients that are given, d_s13 and d_s2 being the shared expert's, and
         returns {"d_x", "d_logits", "d_topk_w"}.  balance, d_loss, token_mask and seq_offsets as
         for route_backward.  The results are memory of `stream`, as balance_loss's are."""
+        self._check_step(logits, W)
         T, E = logits.shape
         if self.kept != (T, Ws is not None):
             raise ValueError(f"backward of {T} tokens{' with' if Ws is not None else ' without'} a shared "
